@@ -352,7 +352,7 @@ def _run_own(s):
     if c["op"] == "gemm":
         capi.moe_grouped_gemm_fp8(c["E"], c["N"], c["C"], s["a"], s["as"], s["a"].shape[0],
                                   s["offset"], s["count"], s["b"], s["bs"], s["out"], c["flags"],
-                                  expect_rows=c["T"] * c["K"])
+                                  max_count=c["T"])
         return {"out": s["out"]}
     capi.moe_swiglu_fp8(c["E"], c["I"], s["x"].shape[0], s["x"], s["offset"], s["count"], s["q"],
                         s["qs"])
