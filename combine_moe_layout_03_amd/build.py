@@ -14,7 +14,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_ep.so")
 SOURCES = ["capi.hip", "layout.hip", "fused.hip", "scatter.hip", "fp8.hip", "ranks.hip",
-           "rank_fused.hip", "replica.hip"]
+           "rank_fused.hip", "replica.hip",
+           # the operators around the experts (moe_experts.h)
+           "experts/experts.hip", "experts/gate.hip", "experts/combine_grad.hip",
+           "experts/swiglu.hip", "experts/grouped_gemm.hip"]
 # floor kernels for the benchmark (measurement only; not part of the C ABI)
 FLOOR_LIB = os.path.join(PKG, "libmoe_floors.so")
 FLOOR_SOURCES = ["floors.hip"]

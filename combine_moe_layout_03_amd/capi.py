@@ -28,6 +28,12 @@ MOE_STATUS_LL_OVERFLOW = 2
 MOE_STATUS_BAD_SLOT = 4
 MOE_STATUS_BAD_REPLICA = 8
 
+MOE_STATUS_BAD_LOGIT = 16
+
+MOE_GATE_BF16 = 1
+MOE_GATE_SIGMOID = 2
+MOE_GATE_RENORM = 4
+
 MOE_FP8_ROUND_SCALE = 1
 MOE_FP8_UE8M0 = 2
 MOE_FP8_SCALE_ROWS = 4
@@ -90,6 +96,14 @@ def _load():
         "moe_rank_combine": (C.c_int, [P, P, I64, P, P, P, P, P, P, P]),
         "moe_replica_weight_sync": (C.c_int, [I32, I32, I64, P, P, P, P, P]),
         "moe_replica_grad_reduce": (C.c_int, [I32, I32, I64, P, P, P, P, P]),
+        # moe_experts.h
+        "moe_gate": (C.c_int, [I32, I32, I32, P, P, P, I32, C.c_float, P, P]),
+        "moe_gate_grad": (C.c_int, [I32, I32, I32, P, P, P, P, I32, C.c_float, P, P]),
+        "moe_combine_grad": (C.c_int, [P, P, P, I64, P, P, P, P, P, P, P, P]),
+        "moe_grouped_gemm_fp8": (C.c_int, [I32, I32, I32, P, P, I64, P, P, P, P, P, I32, I32, P,
+                                           P]),
+        "moe_swiglu_fp8": (C.c_int, [I32, I32, I64, P, P, P, P, P, I32, P, P]),
+        "moe_swiglu_grad": (C.c_int, [I32, I32, I64, P, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -109,6 +123,9 @@ EXPORTED = ("moe_abi_version", "moe_strerror", "moe_recv_rows_worst", "moe_ll_re
             "moe_rank_layout", "moe_rank_dispatch", "moe_rank_layout_dispatch",
             "moe_rank_combine",
             "moe_replica_weight_sync", "moe_replica_grad_reduce")
+# the entry points of moe_experts.h
+EXPORTED_EXPERTS = ("moe_gate", "moe_gate_grad", "moe_combine_grad", "moe_grouped_gemm_fp8",
+                    "moe_swiglu_fp8", "moe_swiglu_grad")
 
 
 def lib():
@@ -565,3 +582,112 @@ def moe_replica_grad_reduce(E: int, E_phys: int, S: int, replica_count: torch.Te
         _dev(replica_phys, "replica_phys", i32, 2 * E),
         _dev(g, "g", (torch.float32,), E_phys * S),
         _dev(status, "status", i32, 1, optional=True), _stream(stream)))
+
+
+# -- the operators around the experts (moe_experts.h) --------------------------
+
+_F32, _I32, _I64 = (torch.float32,), (torch.int32,), (torch.int64,)
+_BF16 = (torch.bfloat16,)
+
+
+def _here(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    """Refuses a call whose tensors do not all live on the current device, the
+    one the library launches on."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device} in one call")
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _logits(x: torch.Tensor, flags: int) -> int:
+    """The caller's router flags with the logits' type added."""
+    if flags & MOE_GATE_BF16 and x.dtype != torch.bfloat16:
+        raise TypeError(f"MOE_GATE_BF16 with logits of dtype {x.dtype}")
+    return int(flags) | (MOE_GATE_BF16 if x.dtype == torch.bfloat16 else 0)
+
+
+def moe_gate(T: int, E: int, K: int, logits: torch.Tensor, topk_idx: torch.Tensor,
+             topk_weights: torch.Tensor, flags: int = 0, scale: float = 1.0,
+             status: Optional[torch.Tensor] = None, stream=None) -> int:
+    """logits float32 or bfloat16 (MOE_GATE_BF16 follows from their dtype)."""
+    _here(logits, topk_idx, topk_weights, status)
+    return _check("moe_gate", _lib.moe_gate(
+        T, E, K, _dev(logits, "logits", _F32 + _BF16, T * E),
+        _dev(topk_idx, "topk_idx", _I64, T * K), _dev(topk_weights, "topk_weights", _F32, T * K),
+        _logits(logits, flags), float(scale), _dev(status, "status", _I32, 1, optional=True),
+        _stream(stream)))
+
+
+def moe_gate_grad(T: int, E: int, K: int, logits: torch.Tensor, topk_idx: torch.Tensor,
+                  d_weights: torch.Tensor, d_logits: torch.Tensor, flags: int = 0,
+                  scale: float = 1.0, status: Optional[torch.Tensor] = None, stream=None) -> int:
+    _here(logits, topk_idx, d_weights, d_logits, status)
+    return _check("moe_gate_grad", _lib.moe_gate_grad(
+        T, E, K, _dev(logits, "logits", _F32 + _BF16, T * E),
+        _dev(topk_idx, "topk_idx", _I64, T * K), _dev(d_weights, "d_weights", _F32, T * K),
+        _dev(d_logits, "d_logits", (logits.dtype,), T * E), _logits(logits, flags), float(scale),
+        _dev(status, "status", _I32, 1, optional=True), _stream(stream)))
+
+
+def moe_combine_grad(shape: moe_shape, d_out: torch.Tensor, y: Optional[torch.Tensor],
+                     recv_rows: int, slot: torch.Tensor, topk_weights: Optional[torch.Tensor],
+                     d_y: torch.Tensor, d_weights: Optional[torch.Tensor] = None,
+                     topk_idx: Optional[torch.Tensor] = None,
+                     rank_mask: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None) -> int:
+    T, H, K = shape.T, shape.H, shape.K
+    _here(d_out, y, slot, topk_weights, d_y, d_weights, topk_idx, rank_mask, status)
+    return _check("moe_combine_grad", _lib.moe_combine_grad(
+        C.byref(shape), _dev(d_out, "d_out", _BF16_LIKE, T * H),
+        _dev(y, "y", _BF16_LIKE, int(recv_rows) * H, optional=d_weights is None), int(recv_rows),
+        _dev(slot, "slot", _I32, T * K),
+        _dev(topk_weights, "topk_weights", _F32, T * K, optional=True),
+        _dev(d_y, "d_y", _BF16_LIKE, int(recv_rows) * H),
+        _dev(d_weights, "d_weights", _F32, T * K, optional=True),
+        _dev(topk_idx, "topk_idx", _I64, T * K, optional=True),
+        _dev(rank_mask, "rank_mask", _I32, shape.R, optional=True),
+        _dev(status, "status", _I32, 1, optional=True), _stream(stream)))
+
+
+def moe_grouped_gemm_fp8(E: int, N: int, C_: int, a: torch.Tensor, a_scale: torch.Tensor,
+                         rows: int, row_start: torch.Tensor, count: torch.Tensor,
+                         w: torch.Tensor, w_scale: torch.Tensor, out: torch.Tensor,
+                         flags: int = 0, max_count: int = 0,
+                         status: Optional[torch.Tensor] = None, stream=None) -> int:
+    rows = int(rows)
+    _here(a, a_scale, row_start, count, w, w_scale, out, status)
+    return _check("moe_grouped_gemm_fp8", _lib.moe_grouped_gemm_fp8(
+        E, N, C_, _dev(a, "a", _FP8_CODES, rows * C_),
+        _dev(a_scale, "a_scale", _fp8_scale_dtypes(flags), rows * fp8_scale_cols(C_, flags)),
+        rows, _dev(row_start, "row_start", _I32, E), _dev(count, "count", _I32, E),
+        _dev(w, "w", _FP8_CODES, E * N * C_),
+        _dev(w_scale, "w_scale", _F32, E * ((N + FP8_GROUP - 1) // FP8_GROUP) * (C_ // FP8_GROUP)),
+        _dev(out, "out", _BF16_LIKE, rows * N), int(flags), int(max_count),
+        _dev(status, "status", _I32, 1, optional=True), _stream(stream)))
+
+
+def moe_swiglu_fp8(E: int, I: int, rows: int, x: torch.Tensor, row_start: torch.Tensor,
+                   count: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, flags: int = 0,
+                   status: Optional[torch.Tensor] = None, stream=None) -> int:
+    rows = int(rows)
+    _here(x, row_start, count, q, scale, status)
+    return _check("moe_swiglu_fp8", _lib.moe_swiglu_fp8(
+        E, I, rows, _dev(x, "x", _BF16_LIKE, rows * 2 * I), _dev(row_start, "row_start", _I32, E),
+        _dev(count, "count", _I32, E), _dev(q, "q", _FP8_CODES, rows * I),
+        _dev(scale, "scale", _fp8_scale_dtypes(flags), rows * fp8_scale_cols(I, flags)),
+        int(flags), _dev(status, "status", _I32, 1, optional=True), _stream(stream)))
+
+
+def moe_swiglu_grad(E: int, I: int, rows: int, x: torch.Tensor, d_h: torch.Tensor,
+                    row_start: torch.Tensor, count: torch.Tensor, d_x: torch.Tensor,
+                    status: Optional[torch.Tensor] = None, stream=None) -> int:
+    rows = int(rows)
+    _here(x, d_h, row_start, count, d_x, status)
+    return _check("moe_swiglu_grad", _lib.moe_swiglu_grad(
+        E, I, rows, _dev(x, "x", _BF16_LIKE, rows * 2 * I), _dev(d_h, "d_h", _BF16_LIKE, rows * I),
+        _dev(row_start, "row_start", _I32, E), _dev(count, "count", _I32, E),
+        _dev(d_x, "d_x", _BF16_LIKE, rows * 2 * I),
+        _dev(status, "status", _I32, 1, optional=True), _stream(stream)))

@@ -1,0 +1,282 @@
+// Router: top-k experts of each token and their weights, and the gradient of
+// the weights with respect to the logits.
+//
+// One wave holds one token's E <= 1024 logits, expert e = lane + 64 * j in
+// register j, as unsigned keys whose integer order is the float order (the sign
+// bit flipped, negatives complemented), 0 for an expert that cannot be
+// selected. K times: the largest key of the wave (a maximum per lane, then four
+// DPP steps and four readlanes), and the lowest expert holding it (a ballot per
+// register, lowest register and lane first), which is taken out. Selection thus
+// compares the logits themselves: sigmoid and softmax keep their order, and two
+// logits that a rounded score would merge still rank as they stand. -0 is
+// turned into +0 first, so that the two tie.
+//
+// Lane k then holds the k-th logit, and the weights of a token are computed in
+// its lanes at once. All statistics are float; the renormalised weights come
+// from exponentials of differences to the largest selected term, whose sum is
+// at least 1.
+//
+// The gradient recomputes the softmax statistics from the logits (reading them
+// is needed anyway, and it keeps nothing between the calls). With p the scores,
+// d = scale * d_weights of the selected places:
+//   softmax:  dx_e = p_e * ( [e selected] d_e - sum_k d_k p_k )
+//   renorm:   dx_k = p_k * ( d_k - sum_j d_j p_j )   (sigmoid: times sigmoid(-x_k))
+//   sigmoid:  dx_k = d_k * s_k * sigmoid(-x_k)
+#include "experts.hpp"
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kKeyNegInf = 0x007fffffu;  // the key of -infinity
+
+__device__ __forceinline__ float gate_load(const void *x, int64_t i, bool bf16) {
+  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(x)[i] << 16)
+              : static_cast<const float *>(x)[i];
+}
+
+// Key of a selectable logit, 0 for -infinity; NaN and +infinity also give 0 and set bad.
+__device__ __forceinline__ uint32_t gate_key(float x, bool *bad) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  const uint32_t k = (u >> 31) ? ~u : (u | 0x80000000u);
+  const bool fin = (u & 0x7f800000u) != 0x7f800000u;
+  *bad = *bad || (!fin && u != 0xff800000u);
+  return fin ? k : 0u;
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {  // 0 -> -infinity
+  if (k <= kKeyNegInf) return -INFINITY;
+  return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);
+}
+
+__device__ __forceinline__ float log_sigmoid(float x) {  // x may be -infinity
+  return fminf(x, 0.0f) - log1pf(expf(-fabsf(x)));
+}
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// The scores of lanes 0 .. K-1 (x = the lane's logit, -infinity where there is
+// none); top and sum are the softmax statistics over all experts.
+template <int kMode>
+__device__ __forceinline__ float gate_score(float x, float top, float sum) {
+  constexpr bool kSig = kMode & kGateSigmoid, kRenorm = kMode & kGateRenorm;
+  float p;
+  if (kRenorm) {
+    const float z = kSig ? log_sigmoid(x) : x;
+    // the largest term of the selected ones
+    float m = z;
+    for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const float ez = x == -INFINITY ? 0.0f : expf(z - m);
+    const float s = wave_sum_f(ez);
+    p = x == -INFINITY ? 0.0f : ez / s;
+  } else if (kSig) {
+    p = x == -INFINITY ? 0.0f : sigmoid(x);
+  } else {
+    p = x == -INFINITY ? 0.0f : expf(x - top) / sum;
+  }
+  return p;
+}
+
+template <int V, int kMode>
+__global__ __launch_bounds__(256) void gate_kernel(const void *__restrict__ x, int32_t T,
+                                                   int32_t E, int32_t K, float scale, bool bf16,
+                                                   int64_t *__restrict__ idx,
+                                                   float *__restrict__ w, int32_t *status) {
+  const int lane = threadIdx.x & 63;
+  const int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (blockDim.x >> 6) +
+                                                     (threadIdx.x >> 6)));
+  if (t >= T) return;
+  uint32_t key[V];
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int e = lane + 64 * j;
+    key[j] = e < E ? gate_key(gate_load(x, (int64_t)t * E + e, bf16), &bad) : 0u;
+  }
+  uint32_t k0[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) k0[j] = key[j];
+  int my_id = -1;
+  uint32_t my_key = 0, top_key = 0;
+  for (int k = 0; k < K; ++k) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) m = umax32(m, key[j]);
+    m = wave_max_u(m);
+    if (k == 0) top_key = m;
+    if (m == 0) break;  // no selectable expert is left (uniform)
+    int id = -1;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint64_t b = __ballot(key[j] == m);
+      if (id < 0 && b) {  // uniform
+        const int l = __ffsll((unsigned long long)b) - 1;
+        id = l + 64 * j;
+        if (lane == l) key[j] = 0;
+      }
+    }
+    if (lane == k) {
+      my_id = id;
+      my_key = m;
+    }
+  }
+  const float top = key_logit(top_key);
+  float sum = 1.0f;
+  if (!(kMode & (kGateSigmoid | kGateRenorm))) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) s += k0[j] ? expf(key_logit(k0[j]) - top) : 0.0f;
+    sum = wave_sum_f(s);
+  }
+  const float p = gate_score<kMode>(key_logit(my_key), top, sum);
+  if (lane < K) {
+    const int64_t o = (int64_t)t * K + lane;
+    idx[o] = my_id;
+    w[o] = my_id < 0 ? 0.0f : p * scale;
+  }
+  if (status && __ballot(bad) && lane == 0) atomicOr(status, kStBadLogit);
+}
+
+template <int V, int kMode>
+__global__ __launch_bounds__(256) void gate_grad_kernel(
+    const void *__restrict__ x, const int64_t *__restrict__ idx, const float *__restrict__ dw,
+    int32_t T, int32_t E, int32_t K, float scale, bool bf16, void *__restrict__ dx,
+    int32_t *status) {
+  constexpr bool kSig = kMode & kGateSigmoid, kRenorm = kMode & kGateRenorm;
+  const int lane = threadIdx.x & 63;
+  const int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (blockDim.x >> 6) +
+                                                     (threadIdx.x >> 6)));
+  if (t >= T) return;
+  int id = -1;
+  float d = 0.0f, xs = -INFINITY;
+  int st = 0;
+  bool bad = false;
+  if (lane < K) {
+    const int64_t e = idx[(int64_t)t * K + lane];
+    if (e >= 0 && e < E) {
+      id = (int)e;
+      d = dw[(int64_t)t * K + lane] * scale;
+      xs = key_logit(gate_key(gate_load(x, (int64_t)t * E + id, bf16), &bad));
+    } else if (e != -1) {
+      st = kStBadExpert;
+    }
+  }
+  if (xs == -INFINITY) id = -1;  // masked: contributes nothing
+  float v[V], top = -INFINITY, sum = 1.0f;
+  constexpr bool kAll = !kSig && !kRenorm;  // softmax over all experts
+  uint32_t key[V];
+  if (kAll) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = lane + 64 * j;
+      key[j] = e < E ? gate_key(gate_load(x, (int64_t)t * E + e, bf16), &bad) : 0u;
+      m = umax32(m, key[j]);
+    }
+    top = key_logit(wave_max_u(m));
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      v[j] = key[j] ? expf(key_logit(key[j]) - top) : 0.0f;
+      s += v[j];
+    }
+    sum = wave_sum_f(s);
+  }
+  const float p = gate_score<kMode>(xs, top, sum);
+  float g;  // the gradient that lane k adds to its expert
+  if (kAll) {
+    g = id < 0 ? 0.0f : d * p;
+    const float dot = wave_sum_f(g);
+    const float r = sum > 0.0f ? dot / sum : 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = -v[j] * r;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = 0.0f;
+    g = id < 0 ? 0.0f : d;
+    if (kRenorm) {
+      const float dot = wave_sum_f(id < 0 ? 0.0f : d * p);
+      g = id < 0 ? 0.0f : p * (d - dot);
+    } else if (id >= 0) {
+      g = d * p;
+    }
+    if (kSig && id >= 0) g *= sigmoid(-xs);
+  }
+  for (int k = 0; k < K; ++k) {  // the same expert twice adds up
+    const int ik = __builtin_amdgcn_readlane(id, k);
+    const float gk = lane_f(g, k);
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] += (ik == lane + 64 * j) ? gk : 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int e = lane + 64 * j;
+    if (e >= E) continue;
+    const int64_t o = (int64_t)t * E + e;
+    if (bf16)
+      static_cast<uint16_t *>(dx)[o] = (uint16_t)ex_bf16(v[j]);
+    else
+      static_cast<float *>(dx)[o] = v[j];
+  }
+  const uint64_t be = __ballot(st != 0), bl = __ballot(bad);
+  if (status && lane == 0 && (be | bl))
+    atomicOr(status, (be ? kStBadExpert : 0) | (bl ? kStBadLogit : 0));
+}
+
+template <int V, int kMode>
+hipError_t gate_vm(const void *x, int32_t T, int32_t E, int32_t K, bool bf16, float scale,
+                   int64_t *idx, float *w, int32_t *status, hipStream_t s) {
+  hipLaunchKernelGGL((gate_kernel<V, kMode>), dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, x, T,
+                     E, K, scale, bf16, idx, w, status);
+  return hipGetLastError();
+}
+template <int V, int kMode>
+hipError_t gate_grad_vm(const void *x, const int64_t *idx, const float *dw, int32_t T, int32_t E,
+                        int32_t K, bool bf16, float scale, void *dx, int32_t *status,
+                        hipStream_t s) {
+  hipLaunchKernelGGL((gate_grad_kernel<V, kMode>), dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s,
+                     x, idx, dw, T, E, K, scale, bf16, dx, status);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+#define MOE_GATE_BY_V(FN, MODE, ...)                    \
+  do {                                                  \
+    if (E <= 64) return FN<1, MODE>(__VA_ARGS__);       \
+    if (E <= 128) return FN<2, MODE>(__VA_ARGS__);      \
+    if (E <= 256) return FN<4, MODE>(__VA_ARGS__);      \
+    if (E <= 512) return FN<8, MODE>(__VA_ARGS__);      \
+    return FN<16, MODE>(__VA_ARGS__);                   \
+  } while (0)
+
+hipError_t launch_gate(const void *x, int32_t T, int32_t E, int32_t K, int32_t flags, float scale,
+                       int64_t *idx, float *w, int32_t *status, hipStream_t s) {
+  const bool bf16 = flags & kGateBf16;
+  switch (flags & (kGateSigmoid | kGateRenorm)) {
+    case 0: MOE_GATE_BY_V(gate_vm, 0, x, T, E, K, bf16, scale, idx, w, status, s);
+    case kGateSigmoid:
+      MOE_GATE_BY_V(gate_vm, kGateSigmoid, x, T, E, K, bf16, scale, idx, w, status, s);
+    case kGateRenorm:
+      MOE_GATE_BY_V(gate_vm, kGateRenorm, x, T, E, K, bf16, scale, idx, w, status, s);
+    default:
+      MOE_GATE_BY_V(gate_vm, (kGateSigmoid | kGateRenorm), x, T, E, K, bf16, scale, idx, w, status,
+                    s);
+  }
+}
+
+hipError_t launch_gate_grad(const void *x, const int64_t *idx, const float *dw, int32_t T,
+                            int32_t E, int32_t K, int32_t flags, float scale, void *dx,
+                            int32_t *status, hipStream_t s) {
+  const bool bf16 = flags & kGateBf16;
+  switch (flags & (kGateSigmoid | kGateRenorm)) {
+    case 0: MOE_GATE_BY_V(gate_grad_vm, 0, x, idx, dw, T, E, K, bf16, scale, dx, status, s);
+    case kGateSigmoid:
+      MOE_GATE_BY_V(gate_grad_vm, kGateSigmoid, x, idx, dw, T, E, K, bf16, scale, dx, status, s);
+    case kGateRenorm:
+      MOE_GATE_BY_V(gate_grad_vm, kGateRenorm, x, idx, dw, T, E, K, bf16, scale, dx, status, s);
+    default:
+      MOE_GATE_BY_V(gate_grad_vm, (kGateSigmoid | kGateRenorm), x, idx, dw, T, E, K, bf16, scale,
+                    dx, status, s);
+  }
+}
+#undef MOE_GATE_BY_V
+
+}  // namespace moe

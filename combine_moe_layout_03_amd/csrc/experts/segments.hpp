@@ -1,0 +1,81 @@
+// What a workgroup needs to walk the rows of all segments when only the device
+// knows the counts: the running sum of the experts' pieces in LDS.
+#pragma once
+
+#include "experts.hpp"
+
+namespace moe {
+
+constexpr int kPlanThreads = 256;
+
+struct SegmentPlan {
+  int32_t first[kMaxExperts + 1];  // pieces of the experts before e; first[E] = all
+  int32_t start[kMaxExperts];      // first buffer row of expert e
+  int32_t wave[kPlanThreads / 64];
+};
+
+// Cuts every segment into ceil(rows / piece) pieces and returns their number.
+// Every thread of the workgroup (kPlanThreads) must call it. Bad segments are
+// reported by workgroup 0 alone.
+__device__ __forceinline__ int plan_segments(const Segments &seg, int piece, SegmentPlan &p,
+                                             int32_t *status) {
+  constexpr int kMost = kMaxExperts / kPlanThreads;
+  const int per = (seg.E + kPlanThreads - 1) / kPlanThreads;  // consecutive experts per thread
+  const int e0 = threadIdx.x * per;
+  int n[kMost], mine = 0;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    n[i] = 0;
+    if (i < per && e0 + i < seg.E) {
+      int32_t st;
+      bool ok;
+      const int r = segment_rows(seg, e0 + i, &st, &ok);
+      p.start[e0 + i] = st;
+      n[i] = (int)(((int64_t)r + piece - 1) / piece);
+      bad = bad || !ok;
+      mine += n[i];
+    }
+  }
+  int total;
+  if (seg.rows >= (1 << 20)) {
+    // Segments that overlap against the rules could overflow the 32-bit sums
+    // (up to 1024 segments of up to 2^31 rows): a coarse sum first, in units
+    // of 1024 rows, and no pieces at all if it passes the buffer's rows.
+    int coarse = 0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) coarse += (n[i] + 1023) >> 10;
+    // n is in pieces: at most as many as rows, so the bound holds for any piece
+    block_exclusive_scan(coarse, p.wave, kPlanThreads / 64, &total);
+    if (total > (int)(seg.rows >> 10) + 1 + seg.E) {
+      mine = 0;
+      bad = true;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) n[i] = 0;
+    }
+  }
+  int at = block_exclusive_scan(mine, p.wave, kPlanThreads / 64, &total);
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    if (i < per && e0 + i < seg.E) {
+      p.first[e0 + i] = at;
+      at += n[i];
+    }
+  }
+  if (threadIdx.x == 0) p.first[seg.E] = total;
+  if (bad && status && blockIdx.x == 0) atomicOr(status, kStBadSlot);
+  __syncthreads();
+  return total;
+}
+
+// The expert of piece i, 0 <= i < first[E].
+__device__ __forceinline__ int plan_find(const SegmentPlan &p, int E, int i) {
+  int lo = 0, hi = E;  // first[lo] <= i < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.first[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace moe

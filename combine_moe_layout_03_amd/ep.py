@@ -292,3 +292,130 @@ def reroute(topk_idx: torch.Tensor, plan: ReplicaPlan,
     capi.moe_reroute(T, K, E, topk_idx.contiguous(), plan.replica_count, plan.replica_phys,
                      plan.num_physical, phys, status)
     return phys
+
+
+# -- around the experts: router, FP8 products, activation, gradients -----------
+
+
+def _gate_flags(score: str, renormalize: bool) -> int:
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f"score is {score!r}, expected 'softmax' or 'sigmoid'")
+    return ((capi.MOE_GATE_SIGMOID if score == "sigmoid" else 0)
+            | (capi.MOE_GATE_RENORM if renormalize else 0))
+
+
+def gate(logits: torch.Tensor, num_topk: int, score: str = "softmax", renormalize: bool = False,
+         scale: float = 1.0, status: Optional[torch.Tensor] = None):
+    """Router: (topk_idx [T, K] int64, topk_weights [T, K] float32) of logits
+    [T, E] (float32 or bfloat16), ready for the dispatch calls. -inf masks an
+    expert; places no expert is left for get id -1 and weight 0."""
+    T, E = logits.shape
+    idx = torch.empty(T, num_topk, dtype=torch.int64, device=logits.device)
+    w = torch.empty(T, num_topk, dtype=torch.float32, device=logits.device)
+    capi.moe_gate(T, E, num_topk, logits.contiguous(), idx, w, _gate_flags(score, renormalize),
+                  scale, status)
+    return idx, w
+
+
+def gate_grad(logits: torch.Tensor, topk_idx: torch.Tensor, d_weights: torch.Tensor,
+              score: str = "softmax", renormalize: bool = False, scale: float = 1.0,
+              status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of ``gate``'s weights: d_logits [T, E] in the logits' type."""
+    T, E = logits.shape
+    x = logits.contiguous()
+    d = torch.empty_like(x)
+    capi.moe_gate_grad(T, E, topk_idx.shape[1], x, topk_idx.contiguous(), d_weights.contiguous(),
+                       d, _gate_flags(score, renormalize), scale, status)
+    return d
+
+
+def combine_grad(d_out: torch.Tensor, y: torch.Tensor, handle: Handle,
+                 topk_weights: Optional[torch.Tensor] = None,
+                 rank_mask: Optional[torch.Tensor] = None):
+    """Gradient of ``combine`` and ``low_latency_combine``: (d_y [rows, H],
+    d_weights [T, K] float32). Rows of d_y that no pair maps to are not
+    written. rank_mask as in low_latency_combine (it needs the handle of a
+    low-latency dispatch, which carries the routing)."""
+    T, H = d_out.shape
+    shape = capi.make_shape(T, H, handle.shape.E, handle.shape.R, handle.shape.K, handle.shape.A)
+    if rank_mask is not None and handle.topk_idx is None:
+        raise ValueError("rank_mask needs a handle that carries topk_idx")
+    d_y = torch.empty(max(handle.recv_rows, 1), H, dtype=y.dtype, device=y.device)
+    d_w = torch.empty(T, shape.K, dtype=torch.float32, device=y.device)
+    capi.moe_combine_grad(
+        shape, d_out.contiguous(), y.reshape(-1, H).contiguous(), handle.recv_rows,
+        handle.layout.slot, topk_weights.contiguous() if topk_weights is not None else None, d_y,
+        d_w, handle.topk_idx if rank_mask is not None else None,
+        rank_mask.contiguous() if rank_mask is not None else None, handle.layout.status)
+    return d_y, d_w
+
+
+def dispatch_grad(d_recv: torch.Tensor, handle: Handle) -> torch.Tensor:
+    """Gradient of the dispatch: each token's rows summed back, [T, H] bf16
+    (the combine without weights)."""
+    return combine(d_recv.reshape(-1, d_recv.shape[-1]), handle)
+
+
+def _most_rows(handle: Handle) -> int:
+    """The largest segment a handle can hold: M rows of a stripe, or every pair."""
+    return handle.ll_M if handle.ll_M is not None else handle.shape.T * handle.shape.K
+
+
+def expert_gemm(x: Tuple[torch.Tensor, torch.Tensor], weight: Tuple[torch.Tensor, torch.Tensor],
+                handle: Handle, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Each expert's product on its receive rows: x is the (codes, scales) tuple
+    of an FP8 dispatch or of ``swiglu_fp8`` (float or UE8M0 scales, row-major or
+    the low-latency dispatch's column-major), weight the (codes [E, N, C],
+    scales [E, ceil(N/128), C/128] float32) tuple. Returns [rows, N] bf16; rows
+    of no expert are not written."""
+    q, sc = x
+    w, ws = weight
+    E, N, Cc = w.shape
+    rows = handle.recv_rows
+    flags = capi.MOE_FP8_SCALE_ROWS
+    if sc.dtype == torch.int32:
+        flags |= capi.MOE_FP8_ROUND_SCALE | capi.MOE_FP8_UE8M0
+    if not sc.is_contiguous():  # the page's view of a column-major tensor
+        sc = sc.transpose(-1, -2)
+        flags &= ~capi.MOE_FP8_SCALE_ROWS
+        if handle.ll_M is None or not sc.is_contiguous():
+            raise ValueError("scales are neither row-major nor a low-latency dispatch's "
+                             "column-major tensor")
+    if out is None:
+        out = torch.empty(max(rows, 1), N, dtype=torch.bfloat16, device=q.device)
+    lay = handle.layout
+    capi.moe_grouped_gemm_fp8(E, N, Cc, q.reshape(-1, Cc), sc, rows, lay.offset, lay.count,
+                              w.contiguous(), ws.contiguous(), out, flags, _most_rows(handle),
+                              lay.status)
+    return out
+
+
+def swiglu_fp8(x: torch.Tensor, handle: Handle, round_scale: bool = False,
+               use_ue8m0: bool = False):
+    """silu(gate) * up of the receive rows x [rows, 2I] bf16, cast to FP8:
+    (codes [rows, I], row-major scales [rows, I/128] float32, or [rows, I/512]
+    int32 with use_ue8m0), as ``expert_gemm`` takes them."""
+    x = x.reshape(-1, x.shape[-1]).contiguous()
+    I = x.shape[1] // 2
+    rows = handle.recv_rows
+    flags = ((capi.MOE_FP8_ROUND_SCALE if round_scale or use_ue8m0 else 0)
+             | (capi.MOE_FP8_UE8M0 if use_ue8m0 else 0))
+    q = torch.empty(max(rows, 1), I, dtype=torch.float8_e4m3fn, device=x.device)
+    sc = torch.empty(max(rows, 1), capi.fp8_scale_cols(I, flags),
+                     dtype=torch.int32 if use_ue8m0 else torch.float32, device=x.device)
+    lay = handle.layout
+    capi.moe_swiglu_fp8(handle.shape.E, I, rows, x, lay.offset, lay.count, q, sc, flags,
+                        lay.status)
+    return q, sc
+
+
+def swiglu_grad(x: torch.Tensor, d_h: torch.Tensor, handle: Handle) -> torch.Tensor:
+    """Gradient of the activation: d_x [rows, 2I] bf16 from x [rows, 2I] and
+    d_h [rows, I]; rows of no expert are not written."""
+    x = x.reshape(-1, x.shape[-1]).contiguous()
+    I = x.shape[1] // 2
+    d_x = torch.empty_like(x)
+    lay = handle.layout
+    capi.moe_swiglu_grad(handle.shape.E, I, handle.recv_rows, x,
+                         d_h.reshape(-1, I).contiguous(), lay.offset, lay.count, d_x, lay.status)
+    return d_x

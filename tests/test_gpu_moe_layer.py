@@ -1,0 +1,242 @@
+"""Router, FP8 dispatch, the experts' products and activation, combine, and the
+gradients, run together through the allocating calls as a layer uses them; and
+captured into HIP graphs. Each step is held to the 64-bit reference on what the
+step before it handed on."""
+import numpy as np
+import pytest
+import torch
+
+import experts_ref as ref
+import moe_inputs as mi
+from gpu_path import dev, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ep():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from combine_moe_layout_03_amd import ep as e
+
+    return e
+
+
+def weights(rng, E, N, C):
+    w = to_dev(ref.random_codes(rng, (E, N, C))).view(torch.float8_e4m3fn)
+    s = (np.exp(rng.standard_normal((E, (N + 127) // 128, C // 128)) * 0.3)
+         * 4 / 448 / np.sqrt(C)).astype(np.float32)
+    return w, to_dev(s)
+
+
+def host(t):
+    return t.detach().cpu()
+
+
+def scales64(sc):
+    s = host(sc).numpy()
+    if s.dtype == np.int32:
+        b = np.stack([(s.astype(np.int64) >> k) & 255 for k in (0, 8, 16, 24)], -1)
+        return np.exp2(b.reshape(s.shape[:-1] + (-1,)) - 127.0)
+    return s.astype(np.float64)
+
+
+def check_product(x, w, rows_of, got):
+    q = host(x[0].reshape(-1, x[0].shape[-1]).view(torch.uint8)).numpy()
+    s = scales64(x[1]).reshape(q.shape[0], -1)
+    wq, ws = host(w[0].view(torch.uint8)).numpy(), host(w[1]).numpy().astype(np.float64)
+    N, C = wq.shape[1:]
+    g = host(got.float()).numpy().astype(np.float64)
+    for e, r in rows_of.items():
+        a = ref.e4m3_values(q[r]) * np.repeat(s[r], 128, 1)
+        b = ref.e4m3_values(wq[e]) * np.repeat(np.repeat(ws[e], 128, 0)[:N], 128, 1)
+        tol = ref.HALF_BF16 * np.abs(a @ b.T) + ref.product_bound(a, b, C // 128)
+        off = np.abs(g[r] - a @ b.T) / tol
+        assert off.max() <= 1, (e, off.max(), np.unravel_index(off.argmax(), off.shape))
+
+
+def check_activation(x, h, rows):
+    gu = host(x.float()).numpy()[rows]
+    _, _, _, want = ref.silu_mul(gu)
+    q = host(h[0].view(torch.uint8)).numpy()[rows]
+    s = scales64(h[1])[rows]
+    v = ref.e4m3_values(q).reshape(len(rows), -1, 128) * s[..., None]
+    want = want.reshape(v.shape)
+    assert np.all(np.abs(v - want) <= (2.0 ** -4 + 20 * ref.EPS24) * np.abs(want)
+                  + (2.0 ** -10 + 450 * 20 * ref.EPS24) * s[..., None])
+
+
+@pytest.mark.parametrize("mode", ["ll", "ll_words", "ll_rows", "contiguous"])
+def test_forward(ep, orc, mode):
+    T, H, E, R, K, I, M = 40, 1024, 32, 4, 4, 512, 64
+    rng = np.random.default_rng(17)
+    logits = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).to(dev())
+    logits[:, 8:16] = -float("inf")  # rank 1 is out
+    x = to_dev(mi.to_bf16_bits(rng.standard_normal((T, H)).astype(np.float32))).view(torch.bfloat16)
+    w1, w2 = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+    idx, wt = ep.gate(logits, K, score="sigmoid", renormalize=True, scale=2.5)
+    assert np.array_equal(host(idx).numpy(), ref.gate_select(host(logits).numpy(), K))
+    words = mode == "ll_words"
+    if mode == "contiguous":
+        _, _, _, _, handle = ep.get_dispatch_layout(idx, E, R, 16, H)
+        qz = orc.quantize_fp8(host(x.view(torch.int16)).numpy().view(np.uint16), 0)
+        xq = torch.from_numpy(qz["q"]).to(dev()).view(torch.float8_e4m3fn)
+        recv = ep.dispatch((xq, to_dev(qz["scale"])), handle)
+    else:
+        recv, _, handle = ep.low_latency_dispatch(x, idx, M, E, R, 2, use_fp8=True,
+                                                  use_ue8m0=words, scale_rows=mode == "ll_rows")
+    start, count = host(handle.layout.offset).numpy(), host(handle.layout.count).numpy()
+    assert count.sum() == T * K and np.all(count[8:16] == 0)
+    rows_of = {e: np.arange(start[e], start[e] + count[e]) for e in range(E) if count[e]}
+    live = np.concatenate(list(rows_of.values()))
+    y1 = ep.expert_gemm(recv, w1, handle)
+    check_product(recv, w1, rows_of, y1)
+    h = ep.swiglu_fp8(y1, handle, use_ue8m0=words)
+    check_activation(y1, h, live)
+    y2 = ep.expert_gemm(h, w2, handle)
+    check_product(h, w2, rows_of, y2)
+    out = ep.combine(y2, handle, wt)
+    slot = host(handle.layout.slot).numpy().reshape(T, K)
+    y64 = host(y2.float()).numpy().astype(np.float64)
+    terms = host(wt).numpy().astype(np.float64)[..., None] * y64[slot]
+    got = host(out.float()).numpy().astype(np.float64)
+    assert np.all(np.abs(got - terms.sum(1)) <= ref.HALF_BF16 * np.abs(terms.sum(1))
+                  + 2 * K * ref.EPS24 * np.abs(terms).sum(1))
+    assert int(handle.layout.status.item()) == 0
+
+
+def test_backward(ep, orc):
+    """Gradients through combine, activation, dispatch and router."""
+    T, H, E, R, K, I = 33, 256, 16, 4, 4, 128
+    rng = np.random.default_rng(23)
+    logits = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).to(dev())
+    idx, wt = ep.gate(logits, K)
+    x = to_dev(mi.to_bf16_bits(rng.standard_normal((T, H)).astype(np.float32))).view(torch.bfloat16)
+    recv, handle = ep.dispatch_with_layout(x, idx, E, R, 8)
+    rows = handle.recv_rows
+    y = to_dev(mi.to_bf16_bits(rng.standard_normal((rows, H)).astype(np.float32))).view(
+        torch.bfloat16)
+    d_out = to_dev(mi.to_bf16_bits(rng.standard_normal((T, H)).astype(np.float32))).view(
+        torch.bfloat16)
+    d_y, d_w = ep.combine_grad(d_out, y, handle, wt)
+    slot = host(handle.layout.slot).numpy().reshape(T, K)
+    do, yy = host(d_out.float()).numpy(), host(y.float()).numpy()
+    w32 = host(wt).numpy()
+    want = mi.bf16_bits_to_f32(mi.to_bf16_bits((w32[..., None] * do[:, None, :]).reshape(-1, H)))
+    assert np.array_equal(host(d_y.float()).numpy()[slot.reshape(-1)], want)
+    t64 = do.astype(np.float64)[:, None, :] * yy.astype(np.float64)[slot]
+    assert np.all(np.abs(host(d_w).numpy() - t64.sum(-1)) <= 20 * ref.EPS24 * np.abs(t64).sum(-1))
+    gu = to_dev(mi.to_bf16_bits(rng.standard_normal((rows, 2 * I)).astype(np.float32))).view(
+        torch.bfloat16)
+    d_h = d_y[:, :I].contiguous()
+    d_gu = ep.swiglu_grad(gu, d_h, handle)
+    r = slot.reshape(-1)
+    g, u, s, _ = ref.silu_mul(host(gu.float()).numpy()[r])
+    d = host(d_h.float()).numpy()[r].astype(np.float64)
+    want = np.concatenate([d * u * s * (1 + g * (1 - s)), d * g * s], 1)
+    big = np.concatenate([np.abs(d * u * s) * (1 + np.abs(g)), np.abs(d * g * s)], 1)
+    assert np.all(np.abs(host(d_gu.float()).numpy()[r] - want)
+                  <= ref.HALF_BF16 * np.abs(want) + 16 * ref.EPS24 * big + 1e-40)
+    # the gradient of the dispatch: the plain sum of a token's rows
+    d_x = ep.dispatch_grad(d_gu, handle)
+    rows64 = host(d_gu.float()).numpy().astype(np.float64)[slot]
+    tot = rows64.sum(1)
+    assert np.all(np.abs(host(d_x.float()).numpy() - tot) <= ref.HALF_BF16 * np.abs(tot)
+                  + K * ref.EPS24 * np.abs(rows64).sum(1))
+    d_logits = host(ep.gate_grad(logits, idx, d_w)).numpy()
+    xl, ids, dw = host(logits).numpy(), host(idx).numpy(), host(d_w).numpy()
+    want = ref.gate_grad(xl, ids, dw, False, False, 1.0)
+    size = (np.abs(dw) * ref.gate_weights(xl, ids, False, False, 1.0)).sum(1, keepdims=True)
+    assert np.all(np.abs(d_logits - want) <= 200 * ref.EPS24 * (np.abs(want) + size))
+    # a masked rank, as the low-latency combine leaves it out
+    recv, _, h2 = ep.low_latency_dispatch(x, idx, 64, E, R, 1)
+    y2 = recv.reshape(-1, H)
+    mask = torch.tensor([0, 1, 0, 0], dtype=torch.int32, device=dev())
+    d_y, d_w = ep.combine_grad(d_out, y2, h2, wt, mask)
+    dead = (ids // (E // R)) == 1
+    sl = host(h2.layout.slot).numpy().reshape(T, K)
+    assert np.all(host(d_w).numpy()[dead] == 0) and np.all(host(d_w).numpy()[~dead] != 0)
+    assert np.all(host(d_y.float()).numpy()[sl[dead]] == 0)
+    with pytest.raises(ValueError, match="topk_idx"):
+        ep.combine_grad(d_out, y, handle, wt, mask)
+
+
+def test_scale_views_are_told_apart(ep):
+    rng = np.random.default_rng(2)
+    T, H, E, R, K, M = 9, 256, 8, 2, 2, 16
+    x = torch.randn(T, H, device=dev()).to(torch.bfloat16)
+    idx = torch.from_numpy(mi._uniform_subsets(rng, T, E, K)).to(dev())
+    w = weights(rng, E, 64, H)
+    got = []
+    for rows in (False, True):
+        recv, _, h = ep.low_latency_dispatch(x, idx, M, E, R, 0, use_fp8=True, scale_rows=rows)
+        assert recv[1].is_contiguous() == rows
+        out = ep.expert_gemm(recv, w, h)
+        got.append(out[h.layout.slot.long()])
+    assert torch.equal(*got)
+    _, _, _, _, hc = ep.get_dispatch_layout(idx, E, R, 1, H)
+    with pytest.raises(ValueError, match="row-major"):
+        q = torch.zeros(T * K, H, dtype=torch.float8_e4m3fn, device=dev())
+        ep.expert_gemm((q, torch.ones(H // 128, T * K, device=dev()).t()), w, hc)
+
+
+def test_empty_batch(ep):
+    w = weights(np.random.default_rng(0), 8, 64, 128)
+    logits = torch.empty(0, 8, device=dev())
+    idx, wt = ep.gate(logits, 2)
+    assert idx.shape == (0, 2) and wt.shape == (0, 2)
+    x = torch.empty(0, 128, dtype=torch.bfloat16, device=dev())
+    recv, _, h = ep.low_latency_dispatch(x, idx, 4, 8, 2, 0, use_fp8=True)
+    out = torch.full((h.recv_rows, 64), 3.0, dtype=torch.bfloat16, device=dev())
+    ep.expert_gemm(recv, w, h, out)
+    assert bool((out == 3).all())
+    assert ep.gate_grad(logits, idx, wt).shape == (0, 8)
+
+
+def test_layer_in_a_graph(ep):
+    """Forward and backward captured once and replayed on new inputs, with eager
+    work of the same shapes between the replays: every replay equals the eager
+    run on those inputs, bit for bit."""
+    T, H, E, R, K, I, M = 48, 512, 16, 4, 4, 256, 48
+    rng = np.random.default_rng(29)
+    w1, w2 = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+    logits = torch.zeros(T, E, device=dev())
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=dev())
+    d_out = torch.zeros(T, H, dtype=torch.bfloat16, device=dev())
+
+    def layer():
+        idx, wt = ep.gate(logits, K, renormalize=True)
+        recv, _, h = ep.low_latency_dispatch(x, idx, M, E, R, 1, use_fp8=True)
+        y1 = ep.expert_gemm(recv, w1, h)
+        y2 = ep.expert_gemm(ep.swiglu_fp8(y1, h), w2, h)
+        out = ep.combine(y2, h, wt)
+        d_y, d_w = ep.combine_grad(d_out, y2, h, wt)
+        d_gu = ep.swiglu_grad(y1, d_y[:, :I].contiguous(), h)
+        # rows as the tokens see them: the rest of the buffers is not written
+        s = h.layout.slot.long()
+        return idx, wt, y1[s], y2[s], out, d_y[s], d_w, d_gu[s], ep.gate_grad(
+            logits, idx, d_w, renormalize=True)
+
+    def fill(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        logits.copy_(torch.randn(T, E, generator=g, device=dev()))
+        x.copy_(torch.randn(T, H, generator=g, device=dev()))
+        d_out.copy_(torch.randn(T, H, generator=g, device=dev()))
+
+    stream = torch.cuda.Stream()
+    fill(0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        held = layer()
+    for seed in (1, 2, 3, 1):
+        fill(seed)
+        want = [t.clone() for t in layer()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(held, want)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (seed, i)

@@ -1,0 +1,177 @@
+"""The experts' activation with its FP8 cast, and its gradient, on the GPU
+against the 64-bit formulas, row by row of the segments."""
+import numpy as np
+import pytest
+import torch
+
+import experts_ref as ref
+import moe_inputs as mi
+from gpu_path import dev, to_dev
+
+pytestmark = pytest.mark.gpu
+
+ROUND, WORDS = 1, 2
+
+
+@pytest.fixture(scope="module")
+def capi():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from combine_moe_layout_03_amd import capi as c
+
+    return c
+
+
+def inputs(seed, counts, width, mode="rows", per=0, spread=1.0):
+    start, rows = ref.lay_rows(counts, mode, per, 4, 3)
+    live = ref.live_rows(start, counts)
+    rng = np.random.default_rng(seed)
+    x = np.full((rows, width), 0x7FC0, np.uint16)  # NaN where nothing may be read
+    x[live] = mi.to_bf16_bits((rng.standard_normal((len(live), width)) * spread).astype(np.float32))
+    return start, rows, live, x
+
+
+def fp8(capi, counts, start, rows, x, I, flags, status=None):
+    q = torch.full((rows, I), 0xA5, dtype=torch.uint8, device=dev())
+    words = bool(flags & WORDS)
+    sc = torch.full((rows, I // 512 if words else I // 128), -5,
+                    dtype=torch.int32 if words else torch.float32, device=dev())
+    capi.moe_swiglu_fp8(len(counts), I, rows, to_dev(x), to_dev(start),
+                        to_dev(np.array(counts, np.int32)), q, sc, flags, status)
+    torch.cuda.synchronize()
+    return q.cpu().numpy(), sc.cpu().numpy()
+
+
+def check_fp8(live, x, q, sc, I, flags):
+    rows = q.shape[0]
+    dead = np.setdiff1d(np.arange(rows), live)
+    assert np.all(q[dead] == 0xA5) and np.all(sc[dead] == -5)
+    if not len(live):
+        return
+    *_, h = ref.silu_mul(mi.bf16_bits_to_f32(x[live]))
+    # exp (2 steps), sum, quotient, product: 8 half steps of h with a margin of 2;
+    # the scale adds its quotient
+    n = 10 * ref.EPS24
+    hg = h.reshape(len(live), -1, 128)
+    want = np.maximum(np.abs(hg).max(-1), np.float32(1e-4)) / 448.0
+    if flags & WORDS:
+        b = np.stack([(sc[live].astype(np.int64) >> k) & 255 for k in (0, 8, 16, 24)], -1)
+        s = np.exp2(b.reshape(len(live), -1) - 127.0)
+    else:
+        s = sc[live].astype(np.float64)
+    if flags & ROUND:
+        assert np.array_equal(s, np.exp2(np.round(np.log2(s))))
+        assert np.all(s >= want * (1 - n)) and np.all(s / 2 < want * (1 + n))
+    else:
+        assert np.all(np.abs(s - want) <= n * want)
+    v = ref.e4m3_values(q[live]).reshape(hg.shape) * s[..., None]
+    # a code is off by at most half an E4M3 step: 2^-4 of the value, 2^-10 below
+    # the smallest normal 2^-6; the scaled value by n, or n of the largest where
+    # it saturates
+    tol = (2.0 ** -4 * np.abs(hg) * (1 + n) + 2.0 ** -10 * s[..., None] + n * np.abs(hg)
+           + n * 448 * s[..., None] * (np.abs(hg) >= 440 * s[..., None]))
+    assert np.all(np.abs(v - hg) <= tol)
+    # signs survive, also those of values that round to zero
+    assert np.array_equal((q[live] >> 7).reshape(hg.shape)[hg != 0], np.signbit(hg)[hg != 0])
+
+
+COUNTS = [[1], [0], [0, 3, 0, 1, 0], [5, 0, 17, 1, 64], [1] * 40, [200, 1, 0, 77]]
+
+
+@pytest.mark.parametrize("flags", [0, ROUND, ROUND | WORDS])
+@pytest.mark.parametrize("I", [128, 512, 640, 2048])
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{sum(c)}")
+def test_swiglu_fp8(capi, counts, I, flags):
+    if flags & WORDS and I % 512:
+        I = 1024
+    start, rows, live, x = inputs(sum(counts) + I, counts, 2 * I, spread=2.0)
+    q, sc = fp8(capi, counts, start, rows, x, I, flags)
+    check_fp8(live, x, q, sc, I, flags)
+
+
+def test_padded_layout_many_experts(capi):
+    rng = np.random.default_rng(4)
+    counts = rng.integers(0, 4, size=1024).tolist()
+    start, rows, live, x = inputs(6, counts, 512, "padded", 6)
+    q, sc = fp8(capi, counts, start, rows, x, 256, 0)
+    check_fp8(live, x, q, sc, 256, 0)
+
+
+def test_extreme_values(capi):
+    """Zero groups, subnormals, far negative gates (silu = -0), products past the
+    float range (kept at the largest float)."""
+    I = 256
+    g = np.zeros((6, I), np.float32)
+    u = np.ones((6, I), np.float32)
+    g[1], u[1] = -3.3e38, 3.3e38
+    g[2], u[2] = 1e-39, 1e-3
+    g[3, ::2], u[3] = 3e38, 3e38
+    g[4], u[4] = np.linspace(-90, 90, I), -2.0
+    g[5], u[5] = 1.0, np.linspace(-3e38, 3e38, I)
+    x = mi.to_bf16_bits(np.concatenate([g, u], 1))
+    start = np.array([0], np.int32)
+    q, sc = fp8(capi, [6], start, 6, x, I, 0)
+    assert np.isfinite(sc).all() and np.all((q & 0x7F) != 0x7F)
+    assert np.all((q[:3] & 0x7F) == 0)
+    assert np.all(sc[0] == np.float32(1e-4) / np.float32(448))
+    assert np.all(q[3, ::2] == 0x7E) and np.all((q[3, 1::2] & 0x7F) == 0)
+    check_fp8(np.array([4, 5]), x, *[np.where(np.isin(np.arange(6), [4, 5])[:, None], a, b)
+                                    for a, b in ((q, 0xA5), (sc, -5))], I, 0)
+
+
+def grad_tol(g, u, s, d, want):
+    """A rounding to bf16, and 16 half float steps of each factor: 1 + g (1 - s)
+    cancels near g = -1.28, so its rounding counts against 1 + |g|."""
+    big = np.concatenate([np.abs(d * u * s) * (1 + np.abs(g)), np.abs(d * g * s)], 1)
+    return ref.HALF_BF16 * np.abs(want) + 16 * ref.EPS24 * big + 1e-40
+
+
+@pytest.mark.parametrize("I", [8, 24, 512, 1416, 2048])
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{sum(c)}")
+def test_swiglu_grad(capi, counts, I):
+    start, rows, live, x = inputs(sum(counts) * 3 + I, counts, 2 * I, spread=3.0)
+    rng = np.random.default_rng(I)
+    dh = np.full((rows, I), 0x7FC0, np.uint16)
+    dh[live] = mi.to_bf16_bits(rng.standard_normal((len(live), I)).astype(np.float32))
+    dx = torch.full((rows, 2 * I), 0x1234, dtype=torch.int16, device=dev())
+    cnt = to_dev(np.array(counts, np.int32))
+    capi.moe_swiglu_grad(len(counts), I, rows, to_dev(x), to_dev(dh), to_dev(start), cnt, dx)
+    torch.cuda.synchronize()
+    got = dx.cpu().numpy().view(np.uint16)
+    assert np.all(got[np.setdiff1d(np.arange(rows), live)] == 0x1234)
+    g, u, s, _ = ref.silu_mul(mi.bf16_bits_to_f32(x[live]))
+    d = mi.bf16_bits_to_f32(dh[live]).astype(np.float64)
+    want = np.concatenate([d * u * s * (1 + g * (1 - s)), d * g * s], 1)
+    have = mi.bf16_bits_to_f32(got[live]).astype(np.float64)
+    assert np.all(np.abs(have - want) <= grad_tol(g, u, s, d, want))
+    # the derivative by central differences: off by h^2 / 6 of a third
+    # derivative, below 1 in size for silu, and by the rounding of h
+    if len(live):
+        h = 1e-4
+        silu = lambda z: z / (1 + np.exp(-z))  # noqa: E731
+        num = np.concatenate([d * u * (silu(g + h) - silu(g - h)) / (2 * h),
+                              d * silu(g)], 1)
+        ext = np.concatenate([np.abs(d * u), np.abs(d * u)], 1) * (h * h + 1e-11 / h)
+        assert np.all(np.abs(have - num) <= grad_tol(g, u, s, d, want) + ext)
+    # in place: the gradient over x itself
+    xin = to_dev(x)
+    capi.moe_swiglu_grad(len(counts), I, rows, xin, to_dev(dh), to_dev(start), cnt, xin)
+    torch.cuda.synchronize()
+    assert np.array_equal(xin.cpu().numpy().view(np.uint16)[live], got[live])
+
+
+def test_bad_segments(capi):
+    """Segments outside the buffer are skipped and reported, the others done."""
+    I, rows = 128, 32
+    rng = np.random.default_rng(0)
+    x = mi.to_bf16_bits(rng.standard_normal((rows, 2 * I)).astype(np.float32))
+    start = np.array([-1, 30, 4, 2 ** 31 - 1, 8, 12], np.int32)
+    counts = [2, 3, 3, 5, -4, 2 ** 31 - 1]
+    st = torch.zeros(1, dtype=torch.int32, device=dev())
+    q, sc = fp8(capi, counts, start, rows, x, I, 0, st)
+    assert int(st.item()) == capi.MOE_STATUS_BAD_SLOT
+    check_fp8(np.arange(4, 7), x, q, sc, I, 0)
+    st.zero_()
+    q, sc = fp8(capi, [0, -3, 2], np.array([-9, 99, 1], np.int32), rows, x, I, 0, st)
+    assert int(st.item()) == 0  # empty segments may point anywhere
+    check_fp8(np.arange(1, 3), x, q, sc, I, 0)
