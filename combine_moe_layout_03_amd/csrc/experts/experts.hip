@@ -147,7 +147,8 @@ MOE_API int moe_grouped_gemm_fp8(int32_t E, int32_t N, int32_t C, const uint8_t 
     return MOE_ERR_ALIGN;
   rc = current_device_ok();
   if (rc) return rc;
-  const Segments seg{row_start, count, E, rows, columns ? (int32_t)(rows / E) : 0, max_count};
+  const Segments seg{row_start, count, E, rows, columns ? (int32_t)(rows / E) : 0, max_count,
+                     0, 0};
   const GemmArgs g{a, a_scale, w, w_scale, out, N, C, flags, status};
   return launched(launch_grouped_gemm(seg, g, stream));
 }
@@ -167,7 +168,7 @@ MOE_API int moe_swiglu_fp8(int32_t E, int32_t I, int64_t rows, const uint16_t *x
     return MOE_ERR_ALIGN;
   rc = current_device_ok();
   if (rc) return rc;
-  const Segments seg{row_start, count, E, rows, 0, 0};
+  const Segments seg{row_start, count, E, rows, 0, 0, 0, 0};
   return launched(launch_swiglu_fp8(seg, I, x, q, scale, flags, status, stream));
 }
 
@@ -184,6 +185,6 @@ MOE_API int moe_swiglu_grad(int32_t E, int32_t I, int64_t rows, const uint16_t *
     return MOE_ERR_ALIGN;
   rc = current_device_ok();
   if (rc) return rc;
-  const Segments seg{row_start, count, E, rows, 0, 0};
+  const Segments seg{row_start, count, E, rows, 0, 0, 0, 0};
   return launched(launch_swiglu_grad(seg, I, x, d_h, d_x, status, stream));
 }

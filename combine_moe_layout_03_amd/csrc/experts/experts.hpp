@@ -68,6 +68,8 @@ struct Segments {
   int64_t rows;        // rows of the buffer
   int32_t per_expert;  // > 0: segment e must lie in rows [e * per_expert, (e + 1) * per_expert)
   int32_t max_count;   // > 0: no segment may hold more rows
+  int32_t over, upto;  // a kernel's share: segments of more than `over`, at most `upto` rows
+                       // (0: all); the one with over = 0 reports the bad segments
 };
 
 __device__ __forceinline__ int segment_rows(const Segments &s, int e, int32_t *start, bool *ok) {

@@ -152,18 +152,248 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_gemm_stream_kernel(Segme
   }
 }
 
+// ---- tiles: segments of many rows -------------------------------------------
+
+constexpr int kTileTokens = 128;  // most token rows of a tile
+constexpr int kTileN = 256;       // weight rows of a tile, 64 per wave
+constexpr int kTileWaves = 4;
+
+// Copies 16 (4) bytes per lane from global memory to LDS at base + 16 (4) * lane
+// without passing registers.
+__device__ __forceinline__ void copy16_to_lds(const void *src, void *base) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                   (__attribute__((address_space(3))) void *)base, 16, 0, 0);
+}
+__device__ __forceinline__ void copy4_to_lds(const void *src, void *base) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                   (__attribute__((address_space(3))) void *)base, 4, 0, 0);
+}
+
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+struct TilePos {
+  int e, n0;
+  int tokens;
+  int64_t row0, scale_base, r_stride, g_stride;
+};
+
+template <int TT, bool kWords>
+__device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &p,
+                                             uint8_t *buf0, uint8_t *buf1, uint32_t *sc0,
+                                             uint32_t *sc1) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int C = ga.C, G = C / kFp8Group;
+  const int l16 = lane & 15, quad = lane >> 4;
+  const int nw = p.n0 + wave * 64;  // the wave's weight rows
+  // uniform bases and 32-bit lane offsets (64 rows of at most 2^20 bytes)
+  const int n_first = min(nw, ga.N - 1);
+  const uint8_t *wbase = ga.w + ((int64_t)p.e * ga.N + n_first) * C;
+  uint32_t wo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    wo[i] = (uint32_t)(min(nw + i * 16 + l16, ga.N - 1) - n_first) * (uint32_t)C + quad * 16;
+  const float *wsbase = ga.w_scale + ((int64_t)p.e * ((ga.N + 127) / 128) + p.n0 / 128) * G;
+  // token rows: the wave copies rows 8 (TT * wave / 2 + i) ... + 7, a lane 16 bytes of one
+  constexpr int kCopies = TT * 2 / kTileWaves + (TT * 2 % kTileWaves != 0);
+  const uint8_t *tbase = ga.a + p.row0 * C;
+  uint32_t to[kCopies];
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    const int r = (i * kTileWaves + wave) * 8 + (lane >> 3);
+    to[i] = (uint32_t)min(r, p.tokens - 1) * (uint32_t)C + (((lane & 7) ^ (lane >> 3)) * 16);
+  }
+  // scales of a group: waves 0 and 1 copy those of the tokens, wave 2 those of the waves' weights
+  const uint32_t *sbase = static_cast<const uint32_t *>(ga.a_scale) + p.scale_base;
+  const int64_t so = (int64_t)min((wave & 1) * 64 + lane, p.tokens - 1) * p.r_stride;
+  const int wo4 = (min(p.n0 + (lane & 3) * 64, ga.N - 1) / 128 - p.n0 / 128) * G;
+  f32x4 acc[4][TT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto load_w = [&](int g, i32x8 (&w)[4]) {
+    const uint8_t *b = wbase + (int64_t)min(g, G - 1) * kFp8Group;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = frag(*reinterpret_cast<const ex_u32x4 *>(b + wo[i]),
+                  *reinterpret_cast<const ex_u32x4 *>(b + wo[i] + 64));
+  };
+  auto copy_tokens = [&](int g, uint8_t *buf, uint32_t *sc) {
+    g = min(g, G - 1);
+    const uint8_t *a = tbase + (int64_t)g * kFp8Group;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      if ((i + 1) * kTileWaves <= TT * 2 || i * kTileWaves + wave < TT * 2)
+        copy16_to_lds(a + to[i], buf + (i * kTileWaves + wave) * 1024);
+    if (wave < 2)
+      copy4_to_lds(sbase + (kWords ? g >> 2 : g) * p.g_stride + so, sc + wave * 64);
+    else if (wave == 2)
+      copy4_to_lds(wsbase + g + wo4, sc + kTileTokens);
+  };
+  // row l16's 16 bytes at chunk quad, chunks permuted by the row's low bits
+  const int frag0 = l16 * 128 + ((quad ^ (l16 & 7)) * 16);
+  // Product q = 4 t + i (token tile t, weight rows i) is issued while product
+  // q - 2 is scaled and added. The empty asm orders the two: left alone, the
+  // compiler issues all products first, and their results do not fit the
+  // registers.
+  auto compute = [&](int g, const uint8_t *buf, const uint32_t *sc, const i32x8 (&w)[4]) {
+    const float b = __uint_as_float(sc[kTileTokens + wave]);
+    auto tokens = [&](int t) {
+      return frag(*reinterpret_cast<const ex_u32x4 *>(buf + t * 2048 + frag0),
+                  *reinterpret_cast<const ex_u32x4 *>(buf + t * 2048 + (frag0 ^ 64)));
+    };
+    auto scale = [&](int t) {
+      const uint32_t x = sc[t * 16 + l16];
+      if (!kWords) return __uint_as_float(x);
+      const uint32_t e = (x >> (8 * (g & 3))) & 255u;
+      return __uint_as_float(e ? e << 23 : 0x00400000u);
+    };
+    f32x4 m[3];
+    i32x8 a = tokens(0), next = a;
+    float s = scale(0) * b, s_next = s;
+#pragma unroll
+    for (int q = 0; q < 4 * TT + 2; ++q) {
+      const int t = q >> 2, i = q & 3;
+      if (q < 4 * TT) {
+        if (i == 0 && t > 0) a = next;
+        if (i == 0 && t + 1 < TT) next = tokens(t + 1);
+        if (q >= 3) {
+          f32x4 &done = acc[(q - 3) & 3][(q - 3) >> 2];
+          asm volatile("" : "+v"(a), "+v"(done));
+        }
+        m[q % 3] = mfma_group(w[i], a);
+      }
+      if (q >= 2) {
+        const int d = q - 2;
+        f32x4 &to_add = acc[d & 3][d >> 2];
+        if ((d & 3) == 0 && d > 0) s = s_next;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) to_add[c] = __builtin_fmaf(m[d % 3][c], s, to_add[c]);
+        if ((d & 3) == 0 && (d >> 2) + 1 < TT) s_next = scale((d >> 2) + 1) * b;
+      }
+    }
+  };
+  auto settle = [&]() {  // the copies of every wave have landed, the other buffer is free
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    lds_barrier();
+  };
+
+  i32x8 wa[4], wb[4];
+  copy_tokens(0, buf0, sc0);
+  load_w(0, wa);
+  settle();
+  for (int g = 0; g + 1 < G; g += 2) {  // a group past the last is loaded again, not used
+    copy_tokens(g + 1, buf1, sc1);
+    load_w(g + 1, wb);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(g, buf0, sc0, wa);
+    settle();
+    copy_tokens(g + 2, buf0, sc0);
+    load_w(g + 2, wa);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(g + 1, buf1, sc1, wb);
+    settle();
+  }
+  if (G & 1) {
+    compute(G - 1, buf0, sc0, wa);
+    lds_barrier();
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int r = t * 16 + l16;
+    if (r >= p.tokens) continue;
+    uint16_t *o = ga.out + (p.row0 + r) * ga.N + nw + quad * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (nw + i * 16 + quad * 4 < ga.N)
+        *reinterpret_cast<ex_u32x2 *>(o + i * 16) =
+            ex_u32x2{ex_bf16x2(acc[i][t][0], acc[i][t][1]), ex_bf16x2(acc[i][t][2], acc[i][t][3])};
+  }
+}
+
+template <bool kWords>
+__global__ __launch_bounds__(kPlanThreads, 2) void grouped_gemm_tile_kernel(Segments seg,
+                                                                            GemmArgs ga) {
+  __shared__ SegmentPlan plan;
+  __shared__ __align__(16) uint8_t buf0[kTileTokens * 128];
+  __shared__ __align__(16) uint8_t buf1[kTileTokens * 128];
+  __shared__ uint32_t sc0[kTileTokens + 64], sc1[kTileTokens + 64];
+  const int pieces = plan_segments(seg, kTileTokens, plan, ga.status);
+  const int G = ga.C / kFp8Group, SG = kWords ? G / 4 : G;  // scale entries of a row
+  const int nblk = (ga.N + kTileN - 1) / kTileN;
+  // Workgroup b runs on XCD b % 8: each XCD takes one run of the tiles, so the
+  // tiles in flight on it share weights and token rows in its L2.
+  const int64_t tiles = (int64_t)pieces * nblk;
+  const int xcd = blockIdx.x & 7, lanes = gridDim.x >> 3;
+  const int64_t lo = tiles * xcd / 8, hi = tiles * (xcd + 1) / 8;
+  for (int64_t u = lo + (blockIdx.x >> 3); u < hi; u += lanes) {
+    TilePos p;
+    // wave-uniform values, kept in scalar registers
+    p.e = scalar(plan_find(plan, seg.E, (int)(u / nblk)));
+    const int first = scalar(plan.first[p.e]), np = scalar(plan.first[p.e + 1]) - first;
+    const int r = (int)(u - (int64_t)first * nblk);
+    const int nb = scalar(r / np), piece = r - nb * np;
+    const int count = scalar(seg.count[p.e]);
+    const int per = scalar(((count + np - 1) / np + 15) & ~15);  // the pieces are even
+    p.tokens = min(count - piece * per, per);
+    p.row0 = (int64_t)scalar(plan.start[p.e]) + piece * per;
+    p.n0 = nb * kTileN;
+    if (seg.per_expert > 0) {
+      p.scale_base = (int64_t)p.e * SG * seg.per_expert + (p.row0 - (int64_t)p.e * seg.per_expert);
+      p.r_stride = 1;
+      p.g_stride = seg.per_expert;
+    } else {
+      p.scale_base = p.row0 * SG;
+      p.r_stride = SG;
+      p.g_stride = 1;
+    }
+    if (per <= 48)
+      tile_product<3, kWords>(ga, p, buf0, buf1, sc0, sc1);
+    else if (per <= 64)
+      tile_product<4, kWords>(ga, p, buf0, buf1, sc0, sc1);
+    else if (per <= 80)
+      tile_product<5, kWords>(ga, p, buf0, buf1, sc0, sc1);
+    else if (per <= 96)
+      tile_product<6, kWords>(ga, p, buf0, buf1, sc0, sc1);
+    else if (per <= 112)
+      tile_product<7, kWords>(ga, p, buf0, buf1, sc0, sc1);
+    else
+      tile_product<8, kWords>(ga, p, buf0, buf1, sc0, sc1);
+  }
+}
+
+// Segments of up to this many rows are streamed, larger ones tiled.
+constexpr int kStreamMost = 32;
+
 }  // namespace
 
 hipError_t launch_grouped_gemm(const Segments &seg, const GemmArgs &g, hipStream_t s) {
+  const bool words = g.flags & kFp8Ue8m0;
   const int64_t nblk = (g.N + kRow16 - 1) / kRow16;
   const int64_t most = ((seg.rows + kStreamTokens - 1) / kStreamTokens + seg.E) * nblk;
   const unsigned grid = (unsigned)(most < 2048 ? most : 2048);
-  if (g.flags & kFp8Ue8m0)
+  // how many rows a segment can have at most decides which kernels are needed
+  const int64_t bound = seg.max_count > 0 ? seg.max_count
+                                          : (seg.per_expert > 0 ? seg.per_expert : seg.rows);
+  Segments part = seg;
+  part.upto = kStreamMost;
+  if (words)
     hipLaunchKernelGGL((grouped_gemm_stream_kernel<true>), dim3(grid), dim3(kPlanThreads), 0, s,
-                       seg, g);
+                       part, g);
   else
     hipLaunchKernelGGL((grouped_gemm_stream_kernel<false>), dim3(grid), dim3(kPlanThreads), 0, s,
-                       seg, g);
+                       part, g);
+  if (bound > kStreamMost) {
+    part.over = kStreamMost;
+    part.upto = 0;
+    if (words)
+      hipLaunchKernelGGL((grouped_gemm_tile_kernel<true>), dim3(512), dim3(kPlanThreads), 0, s,
+                         part, g);
+    else
+      hipLaunchKernelGGL((grouped_gemm_tile_kernel<false>), dim3(512), dim3(kPlanThreads), 0, s,
+                         part, g);
+  }
   return hipGetLastError();
 }
 

@@ -22,7 +22,7 @@ __device__ __forceinline__ int plan_segments(const Segments &seg, int piece, Seg
   constexpr int kMost = kMaxExperts / kPlanThreads;
   const int per = (seg.E + kPlanThreads - 1) / kPlanThreads;  // consecutive experts per thread
   const int e0 = threadIdx.x * per;
-  int n[kMost], mine = 0;
+  int n[kMost], mine = 0, coarse = 0;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
@@ -30,7 +30,9 @@ __device__ __forceinline__ int plan_segments(const Segments &seg, int piece, Seg
     if (i < per && e0 + i < seg.E) {
       int32_t st;
       bool ok;
-      const int r = segment_rows(seg, e0 + i, &st, &ok);
+      int r = segment_rows(seg, e0 + i, &st, &ok);
+      coarse += (int)(((int64_t)r + 1023) >> 10);
+      if (r <= seg.over || (seg.upto > 0 && r > seg.upto)) r = 0;
       p.start[e0 + i] = st;
       n[i] = (int)(((int64_t)r + piece - 1) / piece);
       bad = bad || !ok;
@@ -40,12 +42,9 @@ __device__ __forceinline__ int plan_segments(const Segments &seg, int piece, Seg
   int total;
   if (seg.rows >= (1 << 20)) {
     // Segments that overlap against the rules could overflow the 32-bit sums
-    // (up to 1024 segments of up to 2^31 rows): a coarse sum first, in units
-    // of 1024 rows, and no pieces at all if it passes the buffer's rows.
-    int coarse = 0;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) coarse += (n[i] + 1023) >> 10;
-    // n is in pieces: at most as many as rows, so the bound holds for any piece
+    // (up to 1024 segments of up to 2^31 rows): a coarse sum of all of them
+    // first, in units of 1024 rows, and no pieces at all if it passes the
+    // buffer's rows.
     block_exclusive_scan(coarse, p.wave, kPlanThreads / 64, &total);
     if (total > (int)(seg.rows >> 10) + 1 + seg.E) {
       mine = 0;
@@ -63,7 +62,7 @@ __device__ __forceinline__ int plan_segments(const Segments &seg, int piece, Seg
     }
   }
   if (threadIdx.x == 0) p.first[seg.E] = total;
-  if (bad && status && blockIdx.x == 0) atomicOr(status, kStBadSlot);
+  if (bad && status && blockIdx.x == 0 && seg.over == 0) atomicOr(status, kStBadSlot);
   __syncthreads();
   return total;
 }
