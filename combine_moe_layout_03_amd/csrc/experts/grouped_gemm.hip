@@ -154,9 +154,12 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_gemm_stream_kernel(Segme
 
 // ---- tiles: segments of many rows -------------------------------------------
 
-constexpr int kTileTokens = 128;  // most token rows of a tile
-constexpr int kTileN = 256;       // weight rows of a tile, 64 per wave
-constexpr int kTileWaves = 4;
+constexpr int kTileWaves = 8;      // 4 along the weight rows x 2 along the token rows
+constexpr int kTileThreads = kTileWaves * 64;
+constexpr int kTileN = 256;        // weight rows of a tile, 64 per wave
+constexpr int kTileMost = 9;       // 16-row token tiles per wave
+constexpr int kTileTokens = 2 * 16 * kTileMost;
+constexpr int kScaleSlots = 6 * 64;  // 288 token scales (5 copies of 64), then the weights'
 
 // Copies 16 (4) bytes per lane from global memory to LDS at base + 16 (4) * lane
 // without passing registers.
@@ -177,71 +180,80 @@ struct TilePos {
   int64_t row0, scale_base, r_stride, g_stride;
 };
 
+// One group of 128 channels of a tile in LDS: rows of 128 bytes, the 16-byte
+// chunk c of row r at chunk c ^ (r & 7), so that the 16 rows a fragment reads
+// at one chunk fall on all banks.
+struct TileStage {
+  uint8_t w[kTileN * 128];
+  uint8_t a[kTileTokens * 128];
+  uint32_t scale[kScaleSlots];
+};
+
 template <int TT, bool kWords>
-__device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &p,
-                                             uint8_t *buf0, uint8_t *buf1, uint32_t *sc0,
-                                             uint32_t *sc1) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &p, TileStage &st0,
+                                             TileStage &st1) {
+  const int lane = threadIdx.x & 63, wave = scalar(threadIdx.x >> 6);
+  const int wn = wave & 3, wt = wave >> 2;
   const int C = ga.C, G = C / kFp8Group;
   const int l16 = lane & 15, quad = lane >> 4;
-  const int nw = p.n0 + wave * 64;  // the wave's weight rows
-  // uniform bases and 32-bit lane offsets (64 rows of at most 2^20 bytes)
-  const int n_first = min(nw, ga.N - 1);
-  const uint8_t *wbase = ga.w + ((int64_t)p.e * ga.N + n_first) * C;
-  uint32_t wo[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    wo[i] = (uint32_t)(min(nw + i * 16 + l16, ga.N - 1) - n_first) * (uint32_t)C + quad * 16;
-  const float *wsbase = ga.w_scale + ((int64_t)p.e * ((ga.N + 127) / 128) + p.n0 / 128) * G;
-  // token rows: the wave copies rows 8 (TT * wave / 2 + i) ... + 7, a lane 16 bytes of one
-  constexpr int kCopies = TT * 2 / kTileWaves + (TT * 2 % kTileWaves != 0);
+  const int nw = p.n0 + wn * 64;  // the wave's weight rows
+  // What the wave copies of a group: 8 rows per instruction, 8 lanes a row (a
+  // whole 128-byte line; 16 lanes on 16 rows, as a fragment holds them, load
+  // at a quarter of the rate). Uniform bases, 32-bit lane offsets.
+  constexpr int kCopies = (TT * 4 + kTileWaves - 1) / kTileWaves;
+  const uint8_t *wbase = ga.w + ((int64_t)p.e * ga.N + p.n0) * C;
   const uint8_t *tbase = ga.a + p.row0 * C;
-  uint32_t to[kCopies];
+  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t wo[4], to[kCopies];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (i * kTileWaves + wave) * 8 + (lane >> 3);
+    wo[i] = (uint32_t)min(r, ga.N - 1 - p.n0) * (uint32_t)C + chunk;
+  }
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) {
     const int r = (i * kTileWaves + wave) * 8 + (lane >> 3);
-    to[i] = (uint32_t)min(r, p.tokens - 1) * (uint32_t)C + (((lane & 7) ^ (lane >> 3)) * 16);
+    to[i] = (uint32_t)min(r, p.tokens - 1) * (uint32_t)C + chunk;
   }
-  // scales of a group: waves 0 and 1 copy those of the tokens, wave 2 those of the waves' weights
+  // scales of a group: waves 0-4 copy the tokens', wave 5 those of the weight rows
   const uint32_t *sbase = static_cast<const uint32_t *>(ga.a_scale) + p.scale_base;
-  const int64_t so = (int64_t)min((wave & 1) * 64 + lane, p.tokens - 1) * p.r_stride;
-  const int wo4 = (min(p.n0 + (lane & 3) * 64, ga.N - 1) / 128 - p.n0 / 128) * G;
+  const int64_t so = (int64_t)min(wave * 64 + lane, p.tokens - 1) * p.r_stride;
+  const float *wsbase = ga.w_scale + ((int64_t)p.e * ((ga.N + 127) / 128) + p.n0 / 128) * G;
+  const int ws = (min(p.n0 + (lane & 3) * 64, ga.N - 1) / 128 - p.n0 / 128) * G;
+  auto copy_group = [&](int g, TileStage &st) {
+    g = min(g, G - 1);
+    const int64_t k = (int64_t)g * kFp8Group;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      copy16_to_lds(wbase + k + wo[i], st.w + (i * kTileWaves + wave) * 1024);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      if ((i + 1) * kTileWaves <= TT * 4 || i * kTileWaves + wave < TT * 4)
+        copy16_to_lds(tbase + k + to[i], st.a + (i * kTileWaves + wave) * 1024);
+    if (wave < (TT + 1) / 2)
+      copy4_to_lds(sbase + (kWords ? g >> 2 : g) * p.g_stride + so, st.scale + wave * 64);
+    else if (wave == 5)
+      copy4_to_lds(wsbase + g + ws, st.scale + 5 * 64);
+  };
+
   f32x4 acc[4][TT];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  auto load_w = [&](int g, i32x8 (&w)[4]) {
-    const uint8_t *b = wbase + (int64_t)min(g, G - 1) * kFp8Group;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = frag(*reinterpret_cast<const ex_u32x4 *>(b + wo[i]),
-                  *reinterpret_cast<const ex_u32x4 *>(b + wo[i] + 64));
-  };
-  auto copy_tokens = [&](int g, uint8_t *buf, uint32_t *sc) {
-    g = min(g, G - 1);
-    const uint8_t *a = tbase + (int64_t)g * kFp8Group;
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i)
-      if ((i + 1) * kTileWaves <= TT * 2 || i * kTileWaves + wave < TT * 2)
-        copy16_to_lds(a + to[i], buf + (i * kTileWaves + wave) * 1024);
-    if (wave < 2)
-      copy4_to_lds(sbase + (kWords ? g >> 2 : g) * p.g_stride + so, sc + wave * 64);
-    else if (wave == 2)
-      copy4_to_lds(wsbase + g + wo4, sc + kTileTokens);
-  };
-  // row l16's 16 bytes at chunk quad, chunks permuted by the row's low bits
+  // row l16's 16 bytes at chunk quad
   const int frag0 = l16 * 128 + ((quad ^ (l16 & 7)) * 16);
   // Product q = 4 t + i (token tile t, weight rows i) is issued while product
   // q - 2 is scaled and added. The empty asm orders the two: left alone, the
   // compiler issues all products first, and their results do not fit the
   // registers.
-  auto compute = [&](int g, const uint8_t *buf, const uint32_t *sc, const i32x8 (&w)[4]) {
-    const float b = __uint_as_float(sc[kTileTokens + wave]);
-    auto tokens = [&](int t) {
-      return frag(*reinterpret_cast<const ex_u32x4 *>(buf + t * 2048 + frag0),
-                  *reinterpret_cast<const ex_u32x4 *>(buf + t * 2048 + (frag0 ^ 64)));
+  auto compute = [&](int g, const TileStage &st) {
+    const uint8_t *wbuf = st.w + wn * 8192, *buf = st.a + wt * TT * 2048;
+    const uint32_t *sc = st.scale + wt * TT * 16;
+    const float b = __uint_as_float(st.scale[5 * 64 + wn]);
+    auto rows16 = [&](const uint8_t *from, int t) {
+      return frag(*reinterpret_cast<const ex_u32x4 *>(from + t * 2048 + frag0),
+                  *reinterpret_cast<const ex_u32x4 *>(from + t * 2048 + (frag0 ^ 64)));
     };
     auto scale = [&](int t) {
       const uint32_t x = sc[t * 16 + l16];
@@ -249,15 +261,18 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
       const uint32_t e = (x >> (8 * (g & 3))) & 255u;
       return __uint_as_float(e ? e << 23 : 0x00400000u);
     };
+    i32x8 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = rows16(wbuf, i);
     f32x4 m[3];
-    i32x8 a = tokens(0), next = a;
+    i32x8 a = rows16(buf, 0), next = a;
     float s = scale(0) * b, s_next = s;
 #pragma unroll
     for (int q = 0; q < 4 * TT + 2; ++q) {
       const int t = q >> 2, i = q & 3;
       if (q < 4 * TT) {
         if (i == 0 && t > 0) a = next;
-        if (i == 0 && t + 1 < TT) next = tokens(t + 1);
+        if (i == 0 && t + 1 < TT) next = rows16(buf, t + 1);
         if (q >= 3) {
           f32x4 &done = acc[(q - 3) & 3][(q - 3) >> 2];
           asm volatile("" : "+v"(a), "+v"(done));
@@ -274,34 +289,28 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
       }
     }
   };
-  auto settle = [&]() {  // the copies of every wave have landed, the other buffer is free
+  auto settle = [&]() {  // the copies of every wave have landed, the other stage is free
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
     lds_barrier();
   };
 
-  i32x8 wa[4], wb[4];
-  copy_tokens(0, buf0, sc0);
-  load_w(0, wa);
+  copy_group(0, st0);
   settle();
-  for (int g = 0; g + 1 < G; g += 2) {  // a group past the last is loaded again, not used
-    copy_tokens(g + 1, buf1, sc1);
-    load_w(g + 1, wb);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(g, buf0, sc0, wa);
+  for (int g = 0; g + 1 < G; g += 2) {  // a group past the last is copied again, not used
+    copy_group(g + 1, st1);
+    compute(g, st0);
     settle();
-    copy_tokens(g + 2, buf0, sc0);
-    load_w(g + 2, wa);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(g + 1, buf1, sc1, wb);
+    copy_group(g + 2, st0);
+    compute(g + 1, st1);
     settle();
   }
   if (G & 1) {
-    compute(G - 1, buf0, sc0, wa);
+    compute(G - 1, st0);
     lds_barrier();
   }
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-    const int r = t * 16 + l16;
+    const int r = (wt * TT + t) * 16 + l16;
     if (r >= p.tokens) continue;
     uint16_t *o = ga.out + (p.row0 + r) * ga.N + nw + quad * 4;
 #pragma unroll
@@ -313,13 +322,12 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
 }
 
 template <bool kWords>
-__global__ __launch_bounds__(kPlanThreads, 2) void grouped_gemm_tile_kernel(Segments seg,
+__global__ __launch_bounds__(kTileThreads, 2) void grouped_gemm_tile_kernel(Segments seg,
                                                                             GemmArgs ga) {
   __shared__ SegmentPlan plan;
-  __shared__ __align__(16) uint8_t buf0[kTileTokens * 128];
-  __shared__ __align__(16) uint8_t buf1[kTileTokens * 128];
-  __shared__ uint32_t sc0[kTileTokens + 64], sc1[kTileTokens + 64];
-  const int pieces = plan_segments(seg, kTileTokens, plan, ga.status);
+  __shared__ __align__(16) TileStage st0;
+  __shared__ __align__(16) TileStage st1;
+  const int pieces = plan_segments<kTileThreads>(seg, kTileTokens, plan, ga.status);
   const int G = ga.C / kFp8Group, SG = kWords ? G / 4 : G;  // scale entries of a row
   const int nblk = (ga.N + kTileN - 1) / kTileN;
   // Workgroup b runs on XCD b % 8: each XCD takes one run of the tiles, so the
@@ -335,7 +343,7 @@ __global__ __launch_bounds__(kPlanThreads, 2) void grouped_gemm_tile_kernel(Segm
     const int r = (int)(u - (int64_t)first * nblk);
     const int nb = scalar(r / np), piece = r - nb * np;
     const int count = scalar(seg.count[p.e]);
-    const int per = scalar(((count + np - 1) / np + 15) & ~15);  // the pieces are even
+    const int per = scalar(((count + np - 1) / np + 31) & ~31);  // the pieces are even
     p.tokens = min(count - piece * per, per);
     p.row0 = (int64_t)scalar(plan.start[p.e]) + piece * per;
     p.n0 = nb * kTileN;
@@ -348,18 +356,16 @@ __global__ __launch_bounds__(kPlanThreads, 2) void grouped_gemm_tile_kernel(Segm
       p.r_stride = SG;
       p.g_stride = 1;
     }
-    if (per <= 48)
-      tile_product<3, kWords>(ga, p, buf0, buf1, sc0, sc1);
-    else if (per <= 64)
-      tile_product<4, kWords>(ga, p, buf0, buf1, sc0, sc1);
-    else if (per <= 80)
-      tile_product<5, kWords>(ga, p, buf0, buf1, sc0, sc1);
-    else if (per <= 96)
-      tile_product<6, kWords>(ga, p, buf0, buf1, sc0, sc1);
-    else if (per <= 112)
-      tile_product<7, kWords>(ga, p, buf0, buf1, sc0, sc1);
-    else
-      tile_product<8, kWords>(ga, p, buf0, buf1, sc0, sc1);
+    switch (per >> 5) {
+      case 1: case 2: tile_product<2, kWords>(ga, p, st0, st1); break;
+      case 3: tile_product<3, kWords>(ga, p, st0, st1); break;
+      case 4: tile_product<4, kWords>(ga, p, st0, st1); break;
+      case 5: tile_product<5, kWords>(ga, p, st0, st1); break;
+      case 6: tile_product<6, kWords>(ga, p, st0, st1); break;
+      case 7: tile_product<7, kWords>(ga, p, st0, st1); break;
+      case 8: tile_product<8, kWords>(ga, p, st0, st1); break;
+      default: tile_product<9, kWords>(ga, p, st0, st1); break;
+    }
   }
 }
 
@@ -388,10 +394,10 @@ hipError_t launch_grouped_gemm(const Segments &seg, const GemmArgs &g, hipStream
     part.over = kStreamMost;
     part.upto = 0;
     if (words)
-      hipLaunchKernelGGL((grouped_gemm_tile_kernel<true>), dim3(512), dim3(kPlanThreads), 0, s,
+      hipLaunchKernelGGL((grouped_gemm_tile_kernel<true>), dim3(256), dim3(kTileThreads), 0, s,
                          part, g);
     else
-      hipLaunchKernelGGL((grouped_gemm_tile_kernel<false>), dim3(512), dim3(kPlanThreads), 0, s,
+      hipLaunchKernelGGL((grouped_gemm_tile_kernel<false>), dim3(256), dim3(kTileThreads), 0, s,
                          part, g);
   }
   return hipGetLastError();

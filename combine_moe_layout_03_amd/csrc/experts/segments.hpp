@@ -6,21 +6,22 @@
 
 namespace moe {
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 256;  // workgroup size of the stream kernels
 
 struct SegmentPlan {
   int32_t first[kMaxExperts + 1];  // pieces of the experts before e; first[E] = all
   int32_t start[kMaxExperts];      // first buffer row of expert e
-  int32_t wave[kPlanThreads / 64];
+  int32_t wave[16];
 };
 
 // Cuts every segment into ceil(rows / piece) pieces and returns their number.
-// Every thread of the workgroup (kPlanThreads) must call it. Bad segments are
+// Every thread of the workgroup (kThreads) must call it. Bad segments are
 // reported by workgroup 0 alone.
+template <int kThreads = kPlanThreads>
 __device__ __forceinline__ int plan_segments(const Segments &seg, int piece, SegmentPlan &p,
                                              int32_t *status) {
-  constexpr int kMost = kMaxExperts / kPlanThreads;
-  const int per = (seg.E + kPlanThreads - 1) / kPlanThreads;  // consecutive experts per thread
+  constexpr int kMost = kMaxExperts / kThreads;
+  const int per = (seg.E + kThreads - 1) / kThreads;  // consecutive experts per thread
   const int e0 = threadIdx.x * per;
   int n[kMost], mine = 0, coarse = 0;
   bool bad = false;
@@ -45,7 +46,7 @@ __device__ __forceinline__ int plan_segments(const Segments &seg, int piece, Seg
     // (up to 1024 segments of up to 2^31 rows): a coarse sum of all of them
     // first, in units of 1024 rows, and no pieces at all if it passes the
     // buffer's rows.
-    block_exclusive_scan(coarse, p.wave, kPlanThreads / 64, &total);
+    block_exclusive_scan(coarse, p.wave, kThreads / 64, &total);
     if (total > (int)(seg.rows >> 10) + 1 + seg.E) {
       mine = 0;
       bad = true;
@@ -53,7 +54,7 @@ __device__ __forceinline__ int plan_segments(const Segments &seg, int piece, Seg
       for (int i = 0; i < kMost; ++i) n[i] = 0;
     }
   }
-  int at = block_exclusive_scan(mine, p.wave, kPlanThreads / 64, &total);
+  int at = block_exclusive_scan(mine, p.wave, kThreads / 64, &total);
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
     if (i < per && e0 + i < seg.E) {
