@@ -156,23 +156,37 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_gemm_stream_kernel(Segme
 
 constexpr int kTileWaves = 8;      // 4 along the weight rows x 2 along the token rows
 constexpr int kTileThreads = kTileWaves * 64;
-constexpr int kTileN = 256;        // weight rows of a tile, 64 per wave
+constexpr int kWaveN = 48;         // weight rows of a wave: 3 operands of 16
+constexpr int kTileN = 4 * kWaveN;  // weight rows of a tile
 constexpr int kTileMost = 9;       // 16-row token tiles per wave
 constexpr int kTileTokens = 2 * 16 * kTileMost;
 constexpr int kScaleSlots = 6 * 64;  // 288 token scales (5 copies of 64), then the weights'
 
-// Copies 16 (4) bytes per lane from global memory to LDS at base + 16 (4) * lane
-// without passing registers.
-__device__ __forceinline__ void copy16_to_lds(const void *src, void *base) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                   (__attribute__((address_space(3))) void *)base, 16, 0, 0);
+// Copies 16 (4) bytes per lane from base + off (bytes, off per lane) to LDS at
+// byte `to` + 16 (4) * lane without passing registers. Written in asm because
+// the compiler, not knowing which buffer a copy in flight writes, would wait
+// for all copies before any LDS read; the loop below counts them itself. No
+// register is written, so nothing can be reused too early.
+__device__ __forceinline__ void copy16_to_lds(const void *base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(to), "v"(off), "s"(base) : "memory", "m0");
 }
-__device__ __forceinline__ void copy4_to_lds(const void *src, void *base) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                   (__attribute__((address_space(3))) void *)base, 4, 0, 0);
+__device__ __forceinline__ void copy4_to_lds(const void *base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :: "s"(to), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_byte(const void *p) {  // address of a shared object
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
+// Wave-uniform values, moved to scalar registers.
 __device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+template <class T>
+__device__ __forceinline__ T *scalar(T *x) {
+  const uint64_t v = (uint64_t)(uintptr_t)x;
+  return (T *)(uintptr_t)((uint64_t)(uint32_t)scalar((int)(uint32_t)v) |
+                          (uint64_t)(uint32_t)scalar((int)(uint32_t)(v >> 32)) << 32);
+}
 
 struct TilePos {
   int e, n0;
@@ -180,77 +194,91 @@ struct TilePos {
   int64_t row0, scale_base, r_stride, g_stride;
 };
 
-// One group of 128 channels of a tile in LDS: rows of 128 bytes, the 16-byte
+// Groups of 128 channels of a tile in LDS: rows of 128 bytes, the 16-byte
 // chunk c of row r at chunk c ^ (r & 7), so that the 16 rows a fragment reads
-// at one chunk fall on all banks.
-struct TileStage {
-  uint8_t w[kTileN * 128];
+// at one chunk fall on all banks. The weights come from HBM and are copied two
+// groups ahead into three buffers, the token rows (in L2 after the first tile
+// of an expert) one group ahead into two.
+struct TileRows {
   uint8_t a[kTileTokens * 128];
   uint32_t scale[kScaleSlots];
 };
+struct TileBuffers {
+  uint8_t w[3][kTileN * 128];
+  TileRows rows[2];
+};
 
 template <int TT, bool kWords>
-__device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &p, TileStage &st0,
-                                             TileStage &st1) {
+__device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &p,
+                                             TileBuffers &lds) {
   const int lane = threadIdx.x & 63, wave = scalar(threadIdx.x >> 6);
   const int wn = wave & 3, wt = wave >> 2;
   const int C = ga.C, G = C / kFp8Group;
   const int l16 = lane & 15, quad = lane >> 4;
-  const int nw = p.n0 + wn * 64;  // the wave's weight rows
+  const int nw = p.n0 + wn * kWaveN;  // the wave's weight rows
   // What the wave copies of a group: 8 rows per instruction, 8 lanes a row (a
   // whole 128-byte line; 16 lanes on 16 rows, as a fragment holds them, load
   // at a quarter of the rate). Uniform bases, 32-bit lane offsets.
   constexpr int kCopies = (TT * 4 + kTileWaves - 1) / kTileWaves;
-  const uint8_t *wbase = ga.w + ((int64_t)p.e * ga.N + p.n0) * C;
-  const uint8_t *tbase = ga.a + p.row0 * C;
+  const uint8_t *wbase = scalar(ga.w + ((int64_t)p.e * ga.N + p.n0) * C);
+  const uint8_t *tbase = scalar(ga.a + p.row0 * C);
   const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
-  uint32_t wo[4], to[kCopies];
+  uint32_t wo[3], to_off[kCopies];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 3; ++i) {
     const int r = (i * kTileWaves + wave) * 8 + (lane >> 3);
     wo[i] = (uint32_t)min(r, ga.N - 1 - p.n0) * (uint32_t)C + chunk;
   }
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) {
     const int r = (i * kTileWaves + wave) * 8 + (lane >> 3);
-    to[i] = (uint32_t)min(r, p.tokens - 1) * (uint32_t)C + chunk;
+    to_off[i] = (uint32_t)min(r, p.tokens - 1) * (uint32_t)C + chunk;
   }
-  // scales of a group: waves 0-4 copy the tokens', wave 5 those of the weight rows
-  const uint32_t *sbase = static_cast<const uint32_t *>(ga.a_scale) + p.scale_base;
-  const int64_t so = (int64_t)min(wave * 64 + lane, p.tokens - 1) * p.r_stride;
-  const float *wsbase = ga.w_scale + ((int64_t)p.e * ((ga.N + 127) / 128) + p.n0 / 128) * G;
-  const int ws = (min(p.n0 + (lane & 3) * 64, ga.N - 1) / 128 - p.n0 / 128) * G;
-  auto copy_group = [&](int g, TileStage &st) {
-    g = min(g, G - 1);
-    const int64_t k = (int64_t)g * kFp8Group;
+  // scales of a group: waves 0-4 copy the tokens', wave 5 those of the weight
+  // rows, one for each 16
+  const uint32_t *sbase = scalar(static_cast<const uint32_t *>(ga.a_scale) + p.scale_base);
+  const uint32_t so = (uint32_t)min(wave * 64 + lane, p.tokens - 1) * (uint32_t)p.r_stride * 4;
+  const float *wsbase =
+      scalar(ga.w_scale + ((int64_t)p.e * ((ga.N + 127) / 128) + p.n0 / 128) * G);
+  const uint32_t ws =
+      (uint32_t)(min(p.n0 + min(lane, 11) * 16, ga.N - 1) / 128 - p.n0 / 128) * (uint32_t)G * 4;
+  const uint32_t lds_w = lds_byte(lds.w) + wave * 1024, lds_a = lds_byte(lds.rows) + wave * 1024;
+  const uint32_t lds_s = lds_byte(lds.rows[0].scale) + min(wave, 5) * 256;
+  auto copy_weights = [&](int g, int to) {
+    const uint8_t *b = wbase + (int64_t)min(g, G - 1) * kFp8Group;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      copy16_to_lds(wbase + k + wo[i], st.w + (i * kTileWaves + wave) * 1024);
+    for (int i = 0; i < 3; ++i)
+      copy16_to_lds(b, wo[i], lds_w + to * (kTileN * 128) + i * kTileWaves * 1024);
+  };
+  auto copy_rows = [&](int g, int to) {
+    g = min(g, G - 1);
+    const uint8_t *b = tbase + (int64_t)g * kFp8Group;
+    const uint32_t at = lds_a + to * (uint32_t)sizeof(TileRows);
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
       if ((i + 1) * kTileWaves <= TT * 4 || i * kTileWaves + wave < TT * 4)
-        copy16_to_lds(tbase + k + to[i], st.a + (i * kTileWaves + wave) * 1024);
+        copy16_to_lds(b, to_off[i], at + i * kTileWaves * 1024);
+    const uint32_t st = lds_s + to * (uint32_t)sizeof(TileRows);
     if (wave < (TT + 1) / 2)
-      copy4_to_lds(sbase + (kWords ? g >> 2 : g) * p.g_stride + so, st.scale + wave * 64);
+      copy4_to_lds(sbase + (kWords ? g >> 2 : g) * p.g_stride, so, st);
     else if (wave == 5)
-      copy4_to_lds(wsbase + g + ws, st.scale + 5 * 64);
+      copy4_to_lds(wsbase + g, ws, st);
   };
 
-  f32x4 acc[4][TT];
+  f32x4 acc[3][TT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 3; ++i)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   // row l16's 16 bytes at chunk quad
   const int frag0 = l16 * 128 + ((quad ^ (l16 & 7)) * 16);
-  // Product q = 4 t + i (token tile t, weight rows i) is issued while product
+  // Product q = 3 t + i (token tile t, weight rows i) is issued while product
   // q - 2 is scaled and added. The empty asm orders the two: left alone, the
   // compiler issues all products first, and their results do not fit the
   // registers.
-  auto compute = [&](int g, const TileStage &st) {
-    const uint8_t *wbuf = st.w + wn * 8192, *buf = st.a + wt * TT * 2048;
-    const uint32_t *sc = st.scale + wt * TT * 16;
-    const float b = __uint_as_float(st.scale[5 * 64 + wn]);
+  auto compute = [&](int g, const uint8_t *sw, const TileRows &sa) {
+    const uint8_t *wbuf = sw + wn * kWaveN * 128, *buf = sa.a + wt * TT * 2048;
+    const uint32_t *sc = sa.scale + wt * TT * 16;
     auto rows16 = [&](const uint8_t *from, int t) {
       return frag(*reinterpret_cast<const ex_u32x4 *>(from + t * 2048 + frag0),
                   *reinterpret_cast<const ex_u32x4 *>(from + t * 2048 + (frag0 ^ 64)));
@@ -261,60 +289,67 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
       const uint32_t e = (x >> (8 * (g & 3))) & 255u;
       return __uint_as_float(e ? e << 23 : 0x00400000u);
     };
-    i32x8 w[4];
+    i32x8 w[3];
+    float b[3];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = rows16(wbuf, i);
+    for (int i = 0; i < 3; ++i) {
+      w[i] = rows16(wbuf, i);
+      b[i] = __uint_as_float(sa.scale[5 * 64 + wn * 3 + i]);
+    }
     f32x4 m[3];
     i32x8 a = rows16(buf, 0), next = a;
-    float s = scale(0) * b, s_next = s;
+    float s = scale(0), s_next = s;
 #pragma unroll
-    for (int q = 0; q < 4 * TT + 2; ++q) {
-      const int t = q >> 2, i = q & 3;
-      if (q < 4 * TT) {
+    for (int q = 0; q < 3 * TT + 2; ++q) {
+      const int t = q / 3, i = q % 3;
+      if (q < 3 * TT) {
         if (i == 0 && t > 0) a = next;
         if (i == 0 && t + 1 < TT) next = rows16(buf, t + 1);
         if (q >= 3) {
-          f32x4 &done = acc[(q - 3) & 3][(q - 3) >> 2];
+          f32x4 &done = acc[i][t - 1];
           asm volatile("" : "+v"(a), "+v"(done));
         }
-        m[q % 3] = mfma_group(w[i], a);
+        m[i] = mfma_group(w[i], a);
       }
       if (q >= 2) {
-        const int d = q - 2;
-        f32x4 &to_add = acc[d & 3][d >> 2];
-        if ((d & 3) == 0 && d > 0) s = s_next;
+        const int d = q - 2, dt = d / 3, di = d % 3;
+        if (di == 0 && d > 0) s = s_next;
+        const float f = s * b[di];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) to_add[c] = __builtin_fmaf(m[d % 3][c], s, to_add[c]);
-        if ((d & 3) == 0 && (d >> 2) + 1 < TT) s_next = scale((d >> 2) + 1) * b;
+        for (int c = 0; c < 4; ++c)
+          acc[di][dt][c] = __builtin_fmaf(m[di][c], f, acc[di][dt][c]);
+        if (di == 0 && dt + 1 < TT) s_next = scale(dt + 1);
       }
     }
   };
-  auto settle = [&]() {  // the copies of every wave have landed, the other stage is free
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  // While a group is computed, the next group's token rows and the weights of
+  // the group after that are on their way. At its end all copies but those
+  // last three of each wave have landed, for every wave. Groups past the last
+  // are copied again, not used.
+  copy_rows(0, 0);
+  copy_weights(0, 0);
+  copy_weights(1, 1);
+  __builtin_amdgcn_s_waitcnt(0x0f73);  // vmcnt(3)
+  lds_barrier();
+  int w_now = 0, w_free = 2;
+  for (int g = 0; g < G; ++g) {
+    copy_rows(g + 1, (g + 1) & 1);
+    copy_weights(g + 2, w_free);
+    compute(g, lds.w[w_now], lds.rows[g & 1]);
+    w_free = w_now;
+    w_now = w_now == 2 ? 0 : w_now + 1;
+    __builtin_amdgcn_s_waitcnt(0x0f73);
     lds_barrier();
-  };
-
-  copy_group(0, st0);
-  settle();
-  for (int g = 0; g + 1 < G; g += 2) {  // a group past the last is copied again, not used
-    copy_group(g + 1, st1);
-    compute(g, st0);
-    settle();
-    copy_group(g + 2, st0);
-    compute(g + 1, st1);
-    settle();
   }
-  if (G & 1) {
-    compute(G - 1, st0);
-    lds_barrier();
-  }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // the last copies land before the buffers are used again
+  lds_barrier();
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     const int r = (wt * TT + t) * 16 + l16;
     if (r >= p.tokens) continue;
     uint16_t *o = ga.out + (p.row0 + r) * ga.N + nw + quad * 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 3; ++i)
       if (nw + i * 16 + quad * 4 < ga.N)
         *reinterpret_cast<ex_u32x2 *>(o + i * 16) =
             ex_u32x2{ex_bf16x2(acc[i][t][0], acc[i][t][1]), ex_bf16x2(acc[i][t][2], acc[i][t][3])};
@@ -325,8 +360,7 @@ template <bool kWords>
 __global__ __launch_bounds__(kTileThreads, 2) void grouped_gemm_tile_kernel(Segments seg,
                                                                             GemmArgs ga) {
   __shared__ SegmentPlan plan;
-  __shared__ __align__(16) TileStage st0;
-  __shared__ __align__(16) TileStage st1;
+  __shared__ __align__(16) TileBuffers lds;
   const int pieces = plan_segments<kTileThreads>(seg, kTileTokens, plan, ga.status);
   const int G = ga.C / kFp8Group, SG = kWords ? G / 4 : G;  // scale entries of a row
   const int nblk = (ga.N + kTileN - 1) / kTileN;
@@ -340,7 +374,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void grouped_gemm_tile_kernel(Segm
     // wave-uniform values, kept in scalar registers
     p.e = scalar(plan_find(plan, seg.E, (int)(u / nblk)));
     const int first = scalar(plan.first[p.e]), np = scalar(plan.first[p.e + 1]) - first;
-    const int r = (int)(u - (int64_t)first * nblk);
+    const int r = scalar((int)(u - (int64_t)first * nblk));
     const int nb = scalar(r / np), piece = r - nb * np;
     const int count = scalar(seg.count[p.e]);
     const int per = scalar(((count + np - 1) / np + 31) & ~31);  // the pieces are even
@@ -357,14 +391,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void grouped_gemm_tile_kernel(Segm
       p.g_stride = 1;
     }
     switch (per >> 5) {
-      case 1: case 2: tile_product<2, kWords>(ga, p, st0, st1); break;
-      case 3: tile_product<3, kWords>(ga, p, st0, st1); break;
-      case 4: tile_product<4, kWords>(ga, p, st0, st1); break;
-      case 5: tile_product<5, kWords>(ga, p, st0, st1); break;
-      case 6: tile_product<6, kWords>(ga, p, st0, st1); break;
-      case 7: tile_product<7, kWords>(ga, p, st0, st1); break;
-      case 8: tile_product<8, kWords>(ga, p, st0, st1); break;
-      default: tile_product<9, kWords>(ga, p, st0, st1); break;
+      case 1: case 2: tile_product<2, kWords>(ga, p, lds); break;
+      case 3: tile_product<3, kWords>(ga, p, lds); break;
+      case 4: tile_product<4, kWords>(ga, p, lds); break;
+      case 5: tile_product<5, kWords>(ga, p, lds); break;
+      case 6: tile_product<6, kWords>(ga, p, lds); break;
+      case 7: tile_product<7, kWords>(ga, p, lds); break;
+      case 8: tile_product<8, kWords>(ga, p, lds); break;
+      default: tile_product<9, kWords>(ga, p, lds); break;
     }
   }
 }
