@@ -18,10 +18,6 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kRow16 = 16;          // rows of a matrix instruction's operand
-constexpr int kStreamTokens = 64;   // token rows of a unit
-constexpr int kStreamWaves = 4;
-
 __device__ __forceinline__ i32x8 frag(ex_u32x4 lo, ex_u32x4 hi) {
   return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,
                (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
@@ -31,124 +27,240 @@ __device__ __forceinline__ f32x4 mfma_group(i32x8 w, i32x8 a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, zero, 0, 0, 0, 0, 0, 0);
 }
 
-// A float scale, or exponent byte g % 4 of a packed word.
-template <bool kWords>
-__device__ __forceinline__ float row_scale(const void *p, int64_t base, int64_t g_stride, int g) {
-  if (kWords) {
-    const uint32_t w = static_cast<const uint32_t *>(p)[base + (g >> 2) * g_stride];
-    const uint32_t b = (w >> (8 * (g & 3))) & 255u;
-    return __uint_as_float(b ? b << 23 : 0x00400000u);
-  }
-  return static_cast<const float *>(p)[base + g * g_stride];
+// Wave-uniform values, moved to scalar registers.
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+template <class T>
+__device__ __forceinline__ T *scalar(T *x) {
+  const uint64_t v = (uint64_t)(uintptr_t)x;
+  return (T *)(uintptr_t)((uint64_t)(uint32_t)scalar((int)(uint32_t)v) |
+                          (uint64_t)(uint32_t)scalar((int)(uint32_t)(v >> 32)) << 32);
 }
 
+// Copies 16 (4) bytes per lane from base + off (bytes, off per lane) to LDS at
+// byte `to` + 16 (4) * lane without passing registers. Written in asm because
+// the compiler, not knowing which buffer a copy in flight writes, would wait
+// for all copies before any LDS read; the loop below counts them itself. No
+// register is written, so nothing can be reused too early.
+__device__ __forceinline__ void copy16_to_lds(const void *base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(scalar((int)to)), "v"(off), "s"(scalar(base)) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4_to_lds(const void *base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :: "s"(scalar((int)to)), "v"(off), "s"(scalar(base)) : "memory", "m0");
+}
+// The same with an address per lane.
+__device__ __forceinline__ void copy4_to_lds_at(const void *from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :: "s"(scalar((int)to)), "v"(from) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_byte(const void *p) {  // address of a shared object
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+
+// Rows of 128 bytes (a group) in LDS, the 16-byte chunk c of row r at chunk
+// c ^ (r & 7), so that the 16 rows a fragment reads at one chunk fall on all
+// banks. A copy moves 8 rows, 8 lanes a row: whole lines. (16 lanes on 16 rows,
+// as a fragment holds them, load at 16 bytes a clock and CU from L2 instead of
+// 55.) The lane's bytes of rows t * 16 ... t * 16 + 15:
+__device__ __forceinline__ i32x8 rows16(const uint8_t *rows, int t) {
+  const int lane = threadIdx.x & 63, l16 = lane & 15, quad = lane >> 4;
+  const int at = t * 2048 + l16 * 128 + ((quad ^ (l16 & 7)) * 16);
+  return frag(*reinterpret_cast<const ex_u32x4 *>(rows + at),
+              *reinterpret_cast<const ex_u32x4 *>(rows + (at ^ 64)));
+}
+// The value of exponent byte e of a UE8M0 word.
+__device__ __forceinline__ float byte_scale(uint32_t word, int e) {
+  const uint32_t b = (word >> (8 * e)) & 255u;
+  return __uint_as_float(b ? b << 23 : 0x00400000u);
+}
+
+// ---- stream: segments of few rows -------------------------------------------
+//
+// Few rows per expert make this a read of the weights. A unit is 32 weight rows
+// x up to 16 token rows, and every wave streams units of its own through a ring
+// of three groups in its own part of LDS, without a barrier: the copies of the
+// third group, also of the next unit, are in flight while the first is
+// multiplied. With fewer units than half the waves on the chip the eight waves
+// of a workgroup share a unit's groups out instead and join their sums in LDS.
+
+constexpr int kStreamTokens = 16;  // token rows of a unit
+constexpr int kStreamN = 32;       // weight rows of a unit
+constexpr int kStreamWaves = 8;
+constexpr int kStreamThreads = kStreamWaves * 64;
+constexpr int kStreamRing = 3;
+constexpr int kStreamCopies = kStreamN / 8 + kStreamTokens / 8 + 1;  // of a group
+
+struct StreamStage {
+  uint8_t w[kStreamN * 128];
+  uint8_t a[kStreamTokens * 128];
+  uint32_t scale[64];  // lanes 0-15: the tokens', lane 16: the weights'
+};
 struct StreamShared {
-  SegmentPlan plan;
-  float part[kStreamWaves][kStreamTokens][kRow16 + 1];
+  StreamStage ring[kStreamWaves][kStreamRing];
+  SegmentPlanRows plan;
+};
+static_assert(sizeof(float) * kStreamN * (kStreamTokens + 1) <= sizeof(StreamStage) * kStreamRing,
+              "a wave's partial sums take the place of its ring");
+
+struct StreamUnit {
+  int e, n0, tokens;
+  int64_t row0;
 };
 
-// One unit: 16 weight rows n0 ... n0 + 15, TT * 16 token rows. The waves share
-// the channels out, group by group, and join their sums in LDS.
-template <int TT, bool kWords>
-__device__ __forceinline__ void stream_unit(const GemmArgs &ga, StreamShared &sh, int e, int n0,
-                                            int64_t row0, int tokens, int64_t scale_base,
-                                            int64_t r_stride, int64_t g_stride) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int C = ga.C, G = C / kFp8Group;
-  const int l16 = lane & 15, c16 = (lane >> 4) * 16;
-  const int n = min(n0 + l16, ga.N - 1);
-  const uint8_t *wp = ga.w + ((int64_t)e * ga.N + n) * C + c16;
-  const float *sb = ga.w_scale + ((int64_t)e * ((ga.N + 127) / 128) + n0 / 128) * G;
-  const uint8_t *ap[TT];
-  int64_t as[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int64_t r = min(t * 16 + l16, tokens - 1);
-    ap[t] = ga.a + (row0 + r) * C + c16;
-    as[t] = scale_base + r * r_stride;
-  }
-  f32x4 acc[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int U = TT == 1 ? 4 : 2;  // groups in flight
-  for (int g0 = wave; g0 < G; g0 += U * kStreamWaves) {
-    ex_u32x4 w0[U], w1[U], a0[U][TT], a1[U][TT];
-    float s[U][TT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int g = min(g0 + u * kStreamWaves, G - 1);
-      const int64_t k = (int64_t)g * kFp8Group;
-      w0[u] = *reinterpret_cast<const ex_u32x4 *>(wp + k);
-      w1[u] = *reinterpret_cast<const ex_u32x4 *>(wp + k + 64);
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        a0[u][t] = *reinterpret_cast<const ex_u32x4 *>(ap[t] + k);
-        a1[u][t] = *reinterpret_cast<const ex_u32x4 *>(ap[t] + k + 64);
-        s[u][t] = row_scale<kWords>(ga.a_scale, as[t], g_stride, g);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int g = g0 + u * kStreamWaves;
-      if (g >= G) break;
-      const float b = sb[g];
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const f32x4 p = mfma_group(frag(w0[u], w1[u]), frag(a0[u][t], a1[u][t]));
-        const float sc = s[u][t] * b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(p[i], sc, acc[t][i]);
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < TT; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sh.part[wave][t * 16 + l16][(lane >> 4) * 4 + i] = acc[t][i];
-  __syncthreads();
-  for (int i = threadIdx.x; i < tokens * 8; i += kPlanThreads) {
-    const int t = i >> 3, c = (i & 7) * 2;
-    float v[2];
-#pragma unroll
-    for (int d = 0; d < 2; ++d)
-      v[d] = (sh.part[0][t][c + d] + sh.part[1][t][c + d]) +
-             (sh.part[2][t][c + d] + sh.part[3][t][c + d]);
-    if (n0 + c < ga.N)
-      *reinterpret_cast<uint32_t *>(ga.out + (row0 + t) * ga.N + n0 + c) = ex_bf16x2(v[0], v[1]);
-  }
-  __syncthreads();
-}
-
 template <bool kWords>
-__global__ __launch_bounds__(kPlanThreads) void grouped_gemm_stream_kernel(Segments seg,
-                                                                           GemmArgs ga) {
-  __shared__ StreamShared sh;
-  const int pieces = plan_segments(seg, kStreamTokens, sh.plan, ga.status);
-  const int G = ga.C / kFp8Group, SG = kWords ? G / 4 : G;  // scale entries of a row
-  const int nblk = (ga.N + kRow16 - 1) / kRow16;
+__global__ __launch_bounds__(kStreamThreads, 2) void grouped_gemm_stream_kernel(Segments seg,
+                                                                                GemmArgs ga) {
+  __shared__ __align__(16) StreamShared sh;
+  const int pieces = scalar(plan_segments<kStreamThreads>(seg, kStreamTokens, sh.plan, ga.status));
+  const int lane = threadIdx.x & 63, wave = scalar(threadIdx.x >> 6);
+  const int l16 = lane & 15, quad = lane >> 4;
+  const int C = ga.C, G = C / kFp8Group, SG = kWords ? G / 4 : G;  // scale entries of a row
+  const int nblk = (ga.N + kStreamN - 1) / kStreamN;
   const int64_t units = (int64_t)pieces * nblk;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int i = (int)(u / nblk), nb = (int)(u - (int64_t)i * nblk);
-    const int e = plan_find(sh.plan, seg.E, i);
-    const int t0 = (i - sh.plan.first[e]) * kStreamTokens;
-    const int tokens = min(seg.count[e] - t0, kStreamTokens);
-    const int64_t row0 = (int64_t)sh.plan.start[e] + t0;
-    int64_t base, rs, gs;
-    if (seg.per_expert > 0) {
-      base = (int64_t)e * SG * seg.per_expert + (row0 - (int64_t)e * seg.per_expert);
-      rs = 1;
-      gs = seg.per_expert;
+  if (units == 0) return;
+  const bool split = units * 2 <= (int64_t)gridDim.x * kStreamWaves;  // uniform
+  const int64_t u_first = split ? blockIdx.x : (int64_t)blockIdx.x * kStreamWaves + wave;
+  const int64_t u_step = split ? gridDim.x : (int64_t)gridDim.x * kStreamWaves;
+  const int g_first = split ? wave : 0, g_step = split ? kStreamWaves : 1;
+
+  // unit u: an expert's pieces of 16 rows side by side, then its next weight rows
+  auto unit = [&](int64_t u) {
+    StreamUnit x;
+    x.e = scalar(plan_find(sh.plan, seg.E, (int)(u / nblk)));
+    const int first = scalar(sh.plan.first[x.e]), np = scalar(sh.plan.first[x.e + 1]) - first;
+    const int r = scalar((int)(u - (int64_t)first * nblk));
+    const int nb = scalar(r / np), t0 = (r - nb * np) * kStreamTokens;
+    x.n0 = nb * kStreamN;
+    // (from LDS: a load from memory here would wait for every copy in flight)
+    x.tokens = min(scalar(sh.plan.rows[x.e]) - t0, kStreamTokens);
+    x.row0 = (int64_t)scalar(sh.plan.start[x.e]) + t0;
+    return x;
+  };
+
+  // where the next copies come from
+  const uint8_t *wbase = nullptr, *tbase = nullptr;
+  uint32_t wo[kStreamN / 8], to[kStreamTokens / 8];
+  const uint32_t *sp = nullptr;  // the lane's scale
+  int64_t s_step = 0;            // to the next group's (words: next four groups')
+  auto open = [&](int64_t u) {
+    const StreamUnit x = unit(u);
+    wbase = scalar(ga.w + ((int64_t)x.e * ga.N + x.n0) * C);
+    tbase = scalar(ga.a + x.row0 * C);
+    const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+#pragma unroll
+    for (int i = 0; i < kStreamN / 8; ++i)
+      wo[i] = (uint32_t)min(i * 8 + (lane >> 3), ga.N - 1 - x.n0) * (uint32_t)C + chunk;
+#pragma unroll
+    for (int i = 0; i < kStreamTokens / 8; ++i)
+      to[i] = (uint32_t)min(i * 8 + (lane >> 3), x.tokens - 1) * (uint32_t)C + chunk;
+    if (lane < 16) {
+      const int64_t r = x.row0 + min(lane, x.tokens - 1);
+      const int64_t at = seg.per_expert > 0
+                             ? (int64_t)x.e * SG * seg.per_expert +
+                                   (r - (int64_t)x.e * seg.per_expert)
+                             : r * SG;
+      sp = static_cast<const uint32_t *>(ga.a_scale) + at;
+      s_step = seg.per_expert > 0 ? seg.per_expert : 1;
     } else {
-      base = row0 * SG;
-      rs = SG;
-      gs = 1;
+      sp = reinterpret_cast<const uint32_t *>(ga.w_scale) +
+           ((int64_t)x.e * ((ga.N + 127) / 128) + x.n0 / 128) * G;
+      s_step = 1;
     }
-    if (tokens <= 16)
-      stream_unit<1, kWords>(ga, sh, e, nb * kRow16, row0, tokens, base, rs, gs);
-    else if (tokens <= 32)
-      stream_unit<2, kWords>(ga, sh, e, nb * kRow16, row0, tokens, base, rs, gs);
-    else
-      stream_unit<4, kWords>(ga, sh, e, nb * kRow16, row0, tokens, base, rs, gs);
+  };
+  const uint32_t ring0 = lds_byte(sh.ring[wave]);
+  auto issue = [&](int g, int slot) {
+    const uint32_t st = ring0 + slot * (uint32_t)sizeof(StreamStage);
+    const int64_t k = (int64_t)g * kFp8Group;
+#pragma unroll
+    for (int i = 0; i < kStreamN / 8; ++i) copy16_to_lds(wbase + k, wo[i], st + i * 1024);
+#pragma unroll
+    for (int i = 0; i < kStreamTokens / 8; ++i)
+      copy16_to_lds(tbase + k, to[i], st + kStreamN * 128 + i * 1024);
+    copy4_to_lds_at(sp + (kWords && lane < 16 ? g >> 2 : g) * s_step,
+                    st + (kStreamN + kStreamTokens) * 128);
+  };
+
+  f32x4 acc[2];
+  auto multiply = [&](int g, const StreamStage &st) {
+    const i32x8 a = rows16(st.a, 0);
+    const float b = __uint_as_float(st.scale[16]);
+    const float s = (kWords ? byte_scale(st.scale[l16], g & 3) : __uint_as_float(st.scale[l16])) * b;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4 m = mfma_group(rows16(st.w, i), a);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = __builtin_fmaf(m[c], s, acc[i][c]);
+    }
+  };
+
+  int64_t u_copy = u_first;  // next to copy: group g_copy of unit u_copy
+  int g_copy = g_first, slot_copy = 0, ahead = 0;
+  auto advance = [&]() {  // copies the next group, if there is one
+    if (u_copy >= units) return;
+    issue(g_copy, slot_copy);
+    slot_copy = slot_copy == kStreamRing - 1 ? 0 : slot_copy + 1;
+    ++ahead;
+    g_copy += g_step;
+    if (g_copy >= G) {
+      g_copy = g_first;
+      u_copy += u_step;
+      if (!split && u_copy < units) open(u_copy);
+    }
+  };
+  int slot = 0;
+  for (int64_t u = u_first; u < units; u += u_step) {
+    acc[0] = acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (u == u_first || split) {
+      open(u);
+      u_copy = g_first < G ? u : units;
+      g_copy = g_first;
+      slot_copy = slot = ahead = 0;
+      for (int i = 0; i < kStreamRing - 1; ++i)
+        if (!split || u_copy == u) advance();
+    }
+    for (int g = g_first; g < G; g += g_step) {
+      if (!split || u_copy == u) advance();
+      // `ahead` groups are in flight or landed; the first of them is needed
+      if (ahead == 3)
+        __builtin_amdgcn_s_waitcnt(0x0f7e);  // vmcnt(14): two groups' copies may be out
+      else if (ahead == 2)
+        __builtin_amdgcn_s_waitcnt(0x0f77);  // vmcnt(7)
+      else
+        __builtin_amdgcn_s_waitcnt(0x0f70);
+      asm volatile("" ::: "memory");
+      multiply(g, sh.ring[wave][slot]);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the slot is read, and free
+      asm volatile("" ::: "memory");
+      slot = slot == kStreamRing - 1 ? 0 : slot + 1;
+      --ahead;
+    }
+    const StreamUnit x = unit(u);
+    if (!split) {
+      uint16_t *o = ga.out + (x.row0 + l16) * ga.N + x.n0 + quad * 4;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (l16 < x.tokens && x.n0 + i * 16 + quad * 4 < ga.N)
+          *reinterpret_cast<ex_u32x2 *>(o + i * 16) =
+              ex_u32x2{ex_bf16x2(acc[i][0], acc[i][1]), ex_bf16x2(acc[i][2], acc[i][3])};
+      continue;
+    }
+    // the waves' sums, in the place of their rings (all copies have landed)
+    float *part = reinterpret_cast<float *>(sh.ring[wave]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        part[l16 * (kStreamN + 1) + i * 16 + quad * 4 + c] = acc[i][c];
+    __syncthreads();
+    const int t = threadIdx.x >> 5, n = threadIdx.x & 31;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kStreamWaves; ++w)
+      sum += reinterpret_cast<const float *>(sh.ring[w])[t * (kStreamN + 1) + n];
+    if (t < x.tokens && x.n0 + n < ga.N)
+      ga.out[(x.row0 + t) * ga.N + x.n0 + n] = (uint16_t)ex_bf16(sum);
+    __syncthreads();
   }
 }
 
@@ -160,33 +272,6 @@ constexpr int kWaveN = 48;         // weight rows of a wave: 3 operands of 16
 constexpr int kTileN = 4 * kWaveN;  // weight rows of a tile
 constexpr int kTileMost = 9;       // 16-row token tiles per wave
 constexpr int kTileTokens = 2 * 16 * kTileMost;
-constexpr int kScaleSlots = 6 * 64;  // 288 token scales (5 copies of 64), then the weights'
-
-// Copies 16 (4) bytes per lane from base + off (bytes, off per lane) to LDS at
-// byte `to` + 16 (4) * lane without passing registers. Written in asm because
-// the compiler, not knowing which buffer a copy in flight writes, would wait
-// for all copies before any LDS read; the loop below counts them itself. No
-// register is written, so nothing can be reused too early.
-__device__ __forceinline__ void copy16_to_lds(const void *base, uint32_t off, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(to), "v"(off), "s"(base) : "memory", "m0");
-}
-__device__ __forceinline__ void copy4_to_lds(const void *base, uint32_t off, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-               :: "s"(to), "v"(off), "s"(base) : "memory", "m0");
-}
-__device__ __forceinline__ uint32_t lds_byte(const void *p) {  // address of a shared object
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
-}
-
-// Wave-uniform values, moved to scalar registers.
-__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
-template <class T>
-__device__ __forceinline__ T *scalar(T *x) {
-  const uint64_t v = (uint64_t)(uintptr_t)x;
-  return (T *)(uintptr_t)((uint64_t)(uint32_t)scalar((int)(uint32_t)v) |
-                          (uint64_t)(uint32_t)scalar((int)(uint32_t)(v >> 32)) << 32);
-}
 
 struct TilePos {
   int e, n0;
@@ -199,16 +284,26 @@ struct TilePos {
 // at one chunk fall on all banks. The weights come from HBM and are copied two
 // groups ahead into three buffers, the token rows (in L2 after the first tile
 // of an expert) one group ahead into two.
-struct TileRows {
-  uint8_t a[kTileTokens * 128];
-  uint32_t scale[kScaleSlots];
+// Scales are kept for four groups at a time, and copied a block of four ahead:
+// the copies of one group's row-major scales touch a line per token, as many
+// lines as its 128 channels (1594 against 1175 us for the token copies alone of
+// 65536 rows, 7168 channels, 22 tiles wide).
+enum ScaleLayout {
+  kScaleWord,    // a UE8M0 word holds the token's four groups
+  kScaleVector,  // row-major floats, four of a token in one 16-byte copy
+  kScaleSingle,  // anything else: a copy per group
+};
+struct TileScales {
+  float tokens[4 * kTileTokens];  // kScaleVector: [token][4], else [group][token]
+  float weights[64];              // [16 weight rows][4]
 };
 struct TileBuffers {
   uint8_t w[3][kTileN * 128];
-  TileRows rows[2];
+  uint8_t a[2][kTileTokens * 128];
+  TileScales scale[2];
 };
 
-template <int TT, bool kWords>
+template <int TT, ScaleLayout kScale>
 __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &p,
                                              TileBuffers &lds) {
   const int lane = threadIdx.x & 63, wave = scalar(threadIdx.x >> 6);
@@ -220,6 +315,7 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
   // whole 128-byte line; 16 lanes on 16 rows, as a fragment holds them, load
   // at a quarter of the rate). Uniform bases, 32-bit lane offsets.
   constexpr int kCopies = (TT * 4 + kTileWaves - 1) / kTileWaves;
+  constexpr int kSlots = kCopies + 4;  // copies of a group: rows, weights, scales
   const uint8_t *wbase = scalar(ga.w + ((int64_t)p.e * ga.N + p.n0) * C);
   const uint8_t *tbase = scalar(ga.a + p.row0 * C);
   const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
@@ -234,35 +330,49 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
     const int r = (i * kTileWaves + wave) * 8 + (lane >> 3);
     to_off[i] = (uint32_t)min(r, p.tokens - 1) * (uint32_t)C + chunk;
   }
-  // scales of a group: waves 0-4 copy the tokens', wave 5 those of the weight
-  // rows, one for each 16
+  const uint32_t lds_w = lds_byte(lds.w) + wave * 1024, lds_a = lds_byte(lds.a) + wave * 1024;
+  // The i-th of a wave's three copies of a group's weights, and of its kCopies
+  // of the token rows.
+  auto copy_weights = [&](int g, int to, int i) {
+    copy16_to_lds(wbase + (int64_t)min(g, G - 1) * kFp8Group, wo[i],
+                  lds_w + to * (kTileN * 128) + i * kTileWaves * 1024);
+  };
+  auto copy_rows = [&](int g, int to, int i) {
+    if ((i + 1) * kTileWaves <= TT * 4 || i * kTileWaves + wave < TT * 4)
+      copy16_to_lds(tbase + (int64_t)min(g, G - 1) * kFp8Group, to_off[i],
+                    lds_a + to * (kTileTokens * 128) + i * kTileWaves * 1024);
+  };
+  // Scales: waves 0-4 copy those of 64 tokens each (the last of 32), wave 5
+  // those of the weights, a lane one of the twelve 16-row blocks and a group.
   const uint32_t *sbase = scalar(static_cast<const uint32_t *>(ga.a_scale) + p.scale_base);
-  const uint32_t so = (uint32_t)min(wave * 64 + lane, p.tokens - 1) * (uint32_t)p.r_stride * 4;
+  const int stok = wave * 64 + lane;
+  const uint32_t so = (uint32_t)min(stok, p.tokens - 1) * (uint32_t)p.r_stride * 4;
+  const bool scopy = wave < (TT + 1) / 2;  // uniform
   const float *wsbase =
       scalar(ga.w_scale + ((int64_t)p.e * ((ga.N + 127) / 128) + p.n0 / 128) * G);
-  const uint32_t ws =
-      (uint32_t)(min(p.n0 + min(lane, 11) * 16, ga.N - 1) / 128 - p.n0 / 128) * (uint32_t)G * 4;
-  const uint32_t lds_w = lds_byte(lds.w) + wave * 1024, lds_a = lds_byte(lds.rows) + wave * 1024;
-  const uint32_t lds_s = lds_byte(lds.rows[0].scale) + min(wave, 5) * 256;
-  auto copy_weights = [&](int g, int to) {
-    const uint8_t *b = wbase + (int64_t)min(g, G - 1) * kFp8Group;
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      copy16_to_lds(b, wo[i], lds_w + to * (kTileN * 128) + i * kTileWaves * 1024);
-  };
-  auto copy_rows = [&](int g, int to) {
-    g = min(g, G - 1);
-    const uint8_t *b = tbase + (int64_t)g * kFp8Group;
-    const uint32_t at = lds_a + to * (uint32_t)sizeof(TileRows);
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i)
-      if ((i + 1) * kTileWaves <= TT * 4 || i * kTileWaves + wave < TT * 4)
-        copy16_to_lds(b, to_off[i], at + i * kTileWaves * 1024);
-    const uint32_t st = lds_s + to * (uint32_t)sizeof(TileRows);
-    if (wave < (TT + 1) / 2)
-      copy4_to_lds(sbase + (kWords ? g >> 2 : g) * p.g_stride, so, st);
-    else if (wave == 5)
-      copy4_to_lds(wsbase + g, ws, st);
+  const uint32_t wblock =
+      (uint32_t)(min(p.n0 + min(lane >> 2, 11) * 16, ga.N - 1) / 128 - p.n0 / 128) * (uint32_t)G;
+  const uint32_t lds_s = lds_byte(lds.scale[0].tokens), lds_ws = lds_byte(lds.scale[0].weights);
+  // Part `part` of the scales of block b (groups 4 b ... 4 b + 3); the float
+  // layouts without whole vectors take a part per group, the others part 0.
+  // Returns whether this wave copied (uniform).
+  auto copy_scales = [&](int b, int part) {
+    const uint32_t to = (b & 1) * (uint32_t)sizeof(TileScales);
+    if (wave == 5 && part == 0) {
+      copy4_to_lds(wsbase, (wblock + (uint32_t)min(4 * b + (lane & 3), G - 1)) * 4, lds_ws + to);
+      return true;
+    }
+    if (!scopy || (kScale != kScaleSingle && part > 0)) return false;
+    if (stok < kTileTokens) {
+      if (kScale == kScaleVector)
+        copy16_to_lds(sbase + 4 * min(b, G / 4 - 1), so, lds_s + to + wave * 1024);
+      else if (kScale == kScaleWord)
+        copy4_to_lds(sbase + min(b, G / 4 - 1) * p.g_stride, so, lds_s + to + wave * 256);
+      else
+        copy4_to_lds(sbase + min(4 * b + part, G - 1) * p.g_stride, so,
+                     lds_s + to + (part * kTileTokens + wave * 64) * 4);
+    }
+    return true;
   };
 
   f32x4 acc[3][TT];
@@ -270,75 +380,87 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
   for (int i = 0; i < 3; ++i)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // row l16's 16 bytes at chunk quad
-  const int frag0 = l16 * 128 + ((quad ^ (l16 & 7)) * 16);
   // Product q = 3 t + i (token tile t, weight rows i) is issued while product
   // q - 2 is scaled and added. The empty asm orders the two: left alone, the
   // compiler issues all products first, and their results do not fit the
   // registers.
-  auto compute = [&](int g, const uint8_t *sw, const TileRows &sa) {
-    const uint8_t *wbuf = sw + wn * kWaveN * 128, *buf = sa.a + wt * TT * 2048;
-    const uint32_t *sc = sa.scale + wt * TT * 16;
-    auto rows16 = [&](const uint8_t *from, int t) {
-      return frag(*reinterpret_cast<const ex_u32x4 *>(from + t * 2048 + frag0),
-                  *reinterpret_cast<const ex_u32x4 *>(from + t * 2048 + (frag0 ^ 64)));
-    };
+  auto compute = [&](int g, const uint8_t *sw, const uint8_t *sa, const TileScales &sc,
+                     auto copy) {
+    const uint8_t *wbuf = sw + wn * kWaveN * 128, *buf = sa + wt * TT * 2048;
+    const int gi = g & 3;
     auto scale = [&](int t) {
-      const uint32_t x = sc[t * 16 + l16];
-      if (!kWords) return __uint_as_float(x);
-      const uint32_t e = (x >> (8 * (g & 3))) & 255u;
-      return __uint_as_float(e ? e << 23 : 0x00400000u);
+      const int r = (wt * TT + t) * 16 + l16;
+      if (kScale == kScaleVector) return sc.tokens[r * 4 + gi];
+      if (kScale == kScaleSingle) return sc.tokens[gi * kTileTokens + r];
+      return byte_scale(__float_as_uint(sc.tokens[r]), gi);
     };
-    i32x8 w[3];
-    float b[3];
+    i32x8 w[3], a[3];
+    float b[3], s[TT];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       w[i] = rows16(wbuf, i);
-      b[i] = __uint_as_float(sa.scale[5 * 64 + wn * 3 + i]);
+      if (i < 2 && i < TT) a[i] = rows16(buf, i);
     }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) b[i] = sc.weights[(wn * 3 + i) * 4 + gi];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) s[t] = scale(t);
     f32x4 m[3];
-    i32x8 a = rows16(buf, 0), next = a;
-    float s = scale(0), s_next = s;
 #pragma unroll
     for (int q = 0; q < 3 * TT + 2; ++q) {
       const int t = q / 3, i = q % 3;
       if (q < 3 * TT) {
-        if (i == 0 && t > 0) a = next;
-        if (i == 0 && t + 1 < TT) next = rows16(buf, t + 1);
+        if (i == 0 && t + 2 < TT) a[(t + 2) % 3] = rows16(buf, t + 2);
+        if (i == 1) {
+#pragma unroll
+          for (int c = t * kSlots / TT; c < (t + 1) * kSlots / TT; ++c) copy(c);
+        }
         if (q >= 3) {
           f32x4 &done = acc[i][t - 1];
-          asm volatile("" : "+v"(a), "+v"(done));
+          asm volatile("" : "+v"(a[t % 3]), "+v"(done));
         }
-        m[i] = mfma_group(w[i], a);
+        m[i] = mfma_group(w[i], a[t % 3]);
       }
       if (q >= 2) {
         const int d = q - 2, dt = d / 3, di = d % 3;
-        if (di == 0 && d > 0) s = s_next;
-        const float f = s * b[di];
+        const float f = s[dt] * b[di];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           acc[di][dt][c] = __builtin_fmaf(m[di][c], f, acc[di][dt][c]);
-        if (di == 0 && dt + 1 < TT) s_next = scale(dt + 1);
       }
     }
   };
-  // While a group is computed, the next group's token rows and the weights of
-  // the group after that are on their way. At its end all copies but those
-  // last three of each wave have landed, for every wave. Groups past the last
-  // are copied again, not used.
-  copy_rows(0, 0);
-  copy_weights(0, 0);
-  copy_weights(1, 1);
+  // While a group is computed, the next group's token rows, the weights of the
+  // group after that and the scales four groups on are on their way. At its end
+  // all copies but those last ones of the weights and scales have landed, for
+  // every wave. Groups past the last are copied again, not used.
+  // The copies are issued between the products: in one burst at the start they
+  // would hold the waves up until the address unit has taken them all.
+#pragma unroll
+  for (int i = 0; i < 4; ++i) copy_scales(0, i);
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) copy_rows(0, 0, i);
+#pragma unroll
+  for (int i = 0; i < 6; ++i) copy_weights(i / 3, i / 3, i % 3);
   __builtin_amdgcn_s_waitcnt(0x0f73);  // vmcnt(3)
   lds_barrier();
   int w_now = 0, w_free = 2;
   for (int g = 0; g < G; ++g) {
-    copy_rows(g + 1, (g + 1) & 1);
-    copy_weights(g + 2, w_free);
-    compute(g, lds.w[w_now], lds.rows[g & 1]);
+    bool more = false;
+    compute(g, lds.w[w_now], lds.a[g & 1], lds.scale[(g >> 2) & 1], [&](int c) {
+      if (c < kCopies)
+        copy_rows(g + 1, (g + 1) & 1, c);
+      else if (c < kCopies + 3)
+        copy_weights(g + 2, w_free, c - kCopies);
+      else
+        more = copy_scales((g >> 2) + 1, g & 3);
+    });
     w_free = w_now;
     w_now = w_now == 2 ? 0 : w_now + 1;
-    __builtin_amdgcn_s_waitcnt(0x0f73);
+    if (more)
+      __builtin_amdgcn_s_waitcnt(0x0f74);  // vmcnt(4)
+    else
+      __builtin_amdgcn_s_waitcnt(0x0f73);
     lds_barrier();
   }
   __builtin_amdgcn_s_waitcnt(0x0f70);  // the last copies land before the buffers are used again
@@ -356,13 +478,13 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
   }
 }
 
-template <bool kWords>
+template <ScaleLayout kScale>
 __global__ __launch_bounds__(kTileThreads, 2) void grouped_gemm_tile_kernel(Segments seg,
                                                                             GemmArgs ga) {
   __shared__ SegmentPlan plan;
   __shared__ __align__(16) TileBuffers lds;
-  const int pieces = plan_segments<kTileThreads>(seg, kTileTokens, plan, ga.status);
-  const int G = ga.C / kFp8Group, SG = kWords ? G / 4 : G;  // scale entries of a row
+  const int pieces = scalar(plan_segments<kTileThreads>(seg, kTileTokens, plan, ga.status));
+  const int G = ga.C / kFp8Group, SG = kScale == kScaleWord ? G / 4 : G;  // scale entries of a row
   const int nblk = (ga.N + kTileN - 1) / kTileN;
   // Workgroup b runs on XCD b % 8: each XCD takes one run of the tiles, so the
   // tiles in flight on it share weights and token rows in its L2.
@@ -379,7 +501,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void grouped_gemm_tile_kernel(Segm
     const int count = scalar(seg.count[p.e]);
     const int per = scalar(((count + np - 1) / np + 31) & ~31);  // the pieces are even
     p.tokens = min(count - piece * per, per);
-    p.row0 = (int64_t)scalar(plan.start[p.e]) + piece * per;
+    p.row0 = (int64_t)scalar(seg.start[p.e]) + piece * per;
     p.n0 = nb * kTileN;
     if (seg.per_expert > 0) {
       p.scale_base = (int64_t)p.e * SG * seg.per_expert + (p.row0 - (int64_t)p.e * seg.per_expert);
@@ -391,48 +513,55 @@ __global__ __launch_bounds__(kTileThreads, 2) void grouped_gemm_tile_kernel(Segm
       p.g_stride = 1;
     }
     switch (per >> 5) {
-      case 1: case 2: tile_product<2, kWords>(ga, p, lds); break;
-      case 3: tile_product<3, kWords>(ga, p, lds); break;
-      case 4: tile_product<4, kWords>(ga, p, lds); break;
-      case 5: tile_product<5, kWords>(ga, p, lds); break;
-      case 6: tile_product<6, kWords>(ga, p, lds); break;
-      case 7: tile_product<7, kWords>(ga, p, lds); break;
-      case 8: tile_product<8, kWords>(ga, p, lds); break;
-      default: tile_product<9, kWords>(ga, p, lds); break;
+      case 1: case 2: tile_product<2, kScale>(ga, p, lds); break;
+      case 3: tile_product<3, kScale>(ga, p, lds); break;
+      case 4: tile_product<4, kScale>(ga, p, lds); break;
+      case 5: tile_product<5, kScale>(ga, p, lds); break;
+      case 6: tile_product<6, kScale>(ga, p, lds); break;
+      case 7: tile_product<7, kScale>(ga, p, lds); break;
+      case 8: tile_product<8, kScale>(ga, p, lds); break;
+      default: tile_product<9, kScale>(ga, p, lds); break;
     }
   }
 }
 
 // Segments of up to this many rows are streamed, larger ones tiled.
 constexpr int kStreamMost = 32;
+static_assert(kStreamMost <= 255, "SegmentPlanRows::rows holds bytes");
 
 }  // namespace
 
 hipError_t launch_grouped_gemm(const Segments &seg, const GemmArgs &g, hipStream_t s) {
   const bool words = g.flags & kFp8Ue8m0;
-  const int64_t nblk = (g.N + kRow16 - 1) / kRow16;
+  const int64_t nblk = (g.N + kStreamN - 1) / kStreamN;
   const int64_t most = ((seg.rows + kStreamTokens - 1) / kStreamTokens + seg.E) * nblk;
-  const unsigned grid = (unsigned)(most < 2048 ? most : 2048);
+  const unsigned grid = (unsigned)(most < 256 ? most : 256);  // one workgroup per CU
   // how many rows a segment can have at most decides which kernels are needed
   const int64_t bound = seg.max_count > 0 ? seg.max_count
                                           : (seg.per_expert > 0 ? seg.per_expert : seg.rows);
   Segments part = seg;
   part.upto = kStreamMost;
   if (words)
-    hipLaunchKernelGGL((grouped_gemm_stream_kernel<true>), dim3(grid), dim3(kPlanThreads), 0, s,
+    hipLaunchKernelGGL((grouped_gemm_stream_kernel<true>), dim3(grid), dim3(kStreamThreads), 0, s,
                        part, g);
   else
-    hipLaunchKernelGGL((grouped_gemm_stream_kernel<false>), dim3(grid), dim3(kPlanThreads), 0, s,
+    hipLaunchKernelGGL((grouped_gemm_stream_kernel<false>), dim3(grid), dim3(kStreamThreads), 0, s,
                        part, g);
   if (bound > kStreamMost) {
     part.over = kStreamMost;
     part.upto = 0;
+    // row-major float scales in whole 16-byte vectors: every row starts on one
+    const bool vectors = seg.per_expert == 0 && (g.C / kFp8Group) % 4 == 0 &&
+                         (reinterpret_cast<uintptr_t>(g.a_scale) & 15u) == 0;
     if (words)
-      hipLaunchKernelGGL((grouped_gemm_tile_kernel<true>), dim3(256), dim3(kTileThreads), 0, s,
-                         part, g);
+      hipLaunchKernelGGL((grouped_gemm_tile_kernel<kScaleWord>), dim3(256), dim3(kTileThreads), 0,
+                         s, part, g);
+    else if (vectors)
+      hipLaunchKernelGGL((grouped_gemm_tile_kernel<kScaleVector>), dim3(256), dim3(kTileThreads), 0,
+                         s, part, g);
     else
-      hipLaunchKernelGGL((grouped_gemm_tile_kernel<false>), dim3(256), dim3(kTileThreads), 0, s,
-                         part, g);
+      hipLaunchKernelGGL((grouped_gemm_tile_kernel<kScaleSingle>), dim3(256), dim3(kTileThreads), 0,
+                         s, part, g);
   }
   return hipGetLastError();
 }

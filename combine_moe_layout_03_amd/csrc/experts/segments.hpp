@@ -2,6 +2,8 @@
 // knows the counts: the running sum of the experts' pieces in LDS.
 #pragma once
 
+#include <type_traits>
+
 #include "experts.hpp"
 
 namespace moe {
@@ -10,15 +12,18 @@ constexpr int kPlanThreads = 256;  // workgroup size of the stream kernels
 
 struct SegmentPlan {
   int32_t first[kMaxExperts + 1];  // pieces of the experts before e; first[E] = all
-  int32_t start[kMaxExperts];      // first buffer row of expert e
   int32_t wave[16];
+};
+struct SegmentPlanRows : SegmentPlan {
+  int32_t start[kMaxExperts];  // first buffer row of expert e
+  uint8_t rows[kMaxExperts];   // its rows, where a kernel's share has at most 255
 };
 
 // Cuts every segment into ceil(rows / piece) pieces and returns their number.
 // Every thread of the workgroup (kThreads) must call it. Bad segments are
 // reported by workgroup 0 alone.
-template <int kThreads = kPlanThreads>
-__device__ __forceinline__ int plan_segments(const Segments &seg, int piece, SegmentPlan &p,
+template <int kThreads = kPlanThreads, class Plan>
+__device__ __forceinline__ int plan_segments(const Segments &seg, int piece, Plan &p,
                                              int32_t *status) {
   constexpr int kMost = kMaxExperts / kThreads;
   const int per = (seg.E + kThreads - 1) / kThreads;  // consecutive experts per thread
@@ -34,7 +39,10 @@ __device__ __forceinline__ int plan_segments(const Segments &seg, int piece, Seg
       int r = segment_rows(seg, e0 + i, &st, &ok);
       coarse += (int)(((int64_t)r + 1023) >> 10);
       if (r <= seg.over || (seg.upto > 0 && r > seg.upto)) r = 0;
-      p.start[e0 + i] = st;
+      if constexpr (std::is_same_v<Plan, SegmentPlanRows>) {
+        p.start[e0 + i] = st;
+        p.rows[e0 + i] = (uint8_t)r;
+      }
       n[i] = (int)(((int64_t)r + piece - 1) / piece);
       bad = bad || !ok;
       mine += n[i];

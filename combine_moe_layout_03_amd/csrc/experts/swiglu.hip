@@ -24,7 +24,7 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
     Segments seg, const ex_u32x4 *__restrict__ x, ex_u32x2 *__restrict__ q,
     float *__restrict__ fscale, uint32_t *__restrict__ wscale, int32_t I, int32_t nchunk,
     int32_t *status) {
-  __shared__ SegmentPlan plan;
+  __shared__ SegmentPlanRows plan;
   const int total = plan_segments(seg, 1, plan, status);
   const int lane = threadIdx.x & 63;
   const int nv = I / 8;  // 16-byte vectors of gates in a row
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
 __global__ __launch_bounds__(kSwThreads) void swiglu_grad_kernel(
     Segments seg, const ex_u32x4 *x, const ex_u32x4 *__restrict__ dh, ex_u32x4 *dx, int32_t nv,
     int32_t nchunk, int32_t *status) {
-  __shared__ SegmentPlan plan;
+  __shared__ SegmentPlanRows plan;
   const int total = plan_segments(seg, 1, plan, status);
   const int lane = threadIdx.x & 63;
   const int64_t units = (int64_t)total * nchunk;
