@@ -590,16 +590,40 @@ _F32, _I32, _I64 = (torch.float32,), (torch.int32,), (torch.int64,)
 _BF16 = (torch.bfloat16,)
 
 
-def _here(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
-    """Refuses a call whose tensors do not all live on the current device, the
-    one the library launches on."""
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device} in one call")
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is "
+def _device(t: torch.Tensor, name: str) -> int:
+    """The index of the device a call runs on: its first tensor's, which has to
+    be the current one (the library launches there)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _ptr(t: Optional[torch.Tensor], name: str, dtypes, need: int, dev: int, optional=False):
+    """A tensor's address (None for an absent one). The checks are those of
+    ``_dev`` and that the tensor lives on device ``dev``; a small call's time is
+    mostly this marshalling, so they are one expression."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a GPU tensor" if not t.is_cuda else
+                         f"tensors on cuda:{dev} and {t.device} in one call")
+    if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < need:
+        _dev(t, name, dtypes, need)  # raises
+    return t.data_ptr() or None
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _logits(x: torch.Tensor, flags: int) -> int:
@@ -613,23 +637,25 @@ def moe_gate(T: int, E: int, K: int, logits: torch.Tensor, topk_idx: torch.Tenso
              topk_weights: torch.Tensor, flags: int = 0, scale: float = 1.0,
              status: Optional[torch.Tensor] = None, stream=None) -> int:
     """logits float32 or bfloat16 (MOE_GATE_BF16 follows from their dtype)."""
-    _here(logits, topk_idx, topk_weights, status)
+    dev = _device(logits, "logits")
     return _check("moe_gate", _lib.moe_gate(
-        T, E, K, _dev(logits, "logits", _F32 + _BF16, T * E),
-        _dev(topk_idx, "topk_idx", _I64, T * K), _dev(topk_weights, "topk_weights", _F32, T * K),
-        _logits(logits, flags), float(scale), _dev(status, "status", _I32, 1, optional=True),
-        _stream(stream)))
+        T, E, K, _ptr(logits, "logits", _F32 + _BF16, T * E, dev),
+        _ptr(topk_idx, "topk_idx", _I64, T * K, dev),
+        _ptr(topk_weights, "topk_weights", _F32, T * K, dev), _logits(logits, flags), float(scale),
+        _ptr(status, "status", _I32, 1, dev, True), _raw_stream(stream, dev)))
 
 
 def moe_gate_grad(T: int, E: int, K: int, logits: torch.Tensor, topk_idx: torch.Tensor,
                   d_weights: torch.Tensor, d_logits: torch.Tensor, flags: int = 0,
                   scale: float = 1.0, status: Optional[torch.Tensor] = None, stream=None) -> int:
-    _here(logits, topk_idx, d_weights, d_logits, status)
+    dev = _device(logits, "logits")
     return _check("moe_gate_grad", _lib.moe_gate_grad(
-        T, E, K, _dev(logits, "logits", _F32 + _BF16, T * E),
-        _dev(topk_idx, "topk_idx", _I64, T * K), _dev(d_weights, "d_weights", _F32, T * K),
-        _dev(d_logits, "d_logits", (logits.dtype,), T * E), _logits(logits, flags), float(scale),
-        _dev(status, "status", _I32, 1, optional=True), _stream(stream)))
+        T, E, K, _ptr(logits, "logits", _F32 + _BF16, T * E, dev),
+        _ptr(topk_idx, "topk_idx", _I64, T * K, dev),
+        _ptr(d_weights, "d_weights", _F32, T * K, dev),
+        _ptr(d_logits, "d_logits", (logits.dtype,), T * E, dev), _logits(logits, flags),
+        float(scale),
+        _ptr(status, "status", _I32, 1, dev, True), _raw_stream(stream, dev)))
 
 
 def moe_combine_grad(shape: moe_shape, d_out: torch.Tensor, y: Optional[torch.Tensor],
@@ -639,17 +665,17 @@ def moe_combine_grad(shape: moe_shape, d_out: torch.Tensor, y: Optional[torch.Te
                      rank_mask: Optional[torch.Tensor] = None,
                      status: Optional[torch.Tensor] = None, stream=None) -> int:
     T, H, K = shape.T, shape.H, shape.K
-    _here(d_out, y, slot, topk_weights, d_y, d_weights, topk_idx, rank_mask, status)
+    dev = _device(d_out, "d_out")
     return _check("moe_combine_grad", _lib.moe_combine_grad(
-        C.byref(shape), _dev(d_out, "d_out", _BF16_LIKE, T * H),
-        _dev(y, "y", _BF16_LIKE, int(recv_rows) * H, optional=d_weights is None), int(recv_rows),
-        _dev(slot, "slot", _I32, T * K),
-        _dev(topk_weights, "topk_weights", _F32, T * K, optional=True),
-        _dev(d_y, "d_y", _BF16_LIKE, int(recv_rows) * H),
-        _dev(d_weights, "d_weights", _F32, T * K, optional=True),
-        _dev(topk_idx, "topk_idx", _I64, T * K, optional=True),
-        _dev(rank_mask, "rank_mask", _I32, shape.R, optional=True),
-        _dev(status, "status", _I32, 1, optional=True), _stream(stream)))
+        C.byref(shape), _ptr(d_out, "d_out", _BF16_LIKE, T * H, dev),
+        _ptr(y, "y", _BF16_LIKE, int(recv_rows) * H, dev, d_weights is None), int(recv_rows),
+        _ptr(slot, "slot", _I32, T * K, dev),
+        _ptr(topk_weights, "topk_weights", _F32, T * K, dev, True),
+        _ptr(d_y, "d_y", _BF16_LIKE, int(recv_rows) * H, dev),
+        _ptr(d_weights, "d_weights", _F32, T * K, dev, True),
+        _ptr(topk_idx, "topk_idx", _I64, T * K, dev, True),
+        _ptr(rank_mask, "rank_mask", _I32, shape.R, dev, True),
+        _ptr(status, "status", _I32, 1, dev, True), _raw_stream(stream, dev)))
 
 
 def moe_grouped_gemm_fp8(E: int, N: int, C_: int, a: torch.Tensor, a_scale: torch.Tensor,
@@ -658,36 +684,39 @@ def moe_grouped_gemm_fp8(E: int, N: int, C_: int, a: torch.Tensor, a_scale: torc
                          flags: int = 0, max_count: int = 0,
                          status: Optional[torch.Tensor] = None, stream=None) -> int:
     rows = int(rows)
-    _here(a, a_scale, row_start, count, w, w_scale, out, status)
+    blocks = ((N + FP8_GROUP - 1) // FP8_GROUP) * (C_ // FP8_GROUP)
+    dev = _device(a, "a")
     return _check("moe_grouped_gemm_fp8", _lib.moe_grouped_gemm_fp8(
-        E, N, C_, _dev(a, "a", _FP8_CODES, rows * C_),
-        _dev(a_scale, "a_scale", _fp8_scale_dtypes(flags), rows * fp8_scale_cols(C_, flags)),
-        rows, _dev(row_start, "row_start", _I32, E), _dev(count, "count", _I32, E),
-        _dev(w, "w", _FP8_CODES, E * N * C_),
-        _dev(w_scale, "w_scale", _F32, E * ((N + FP8_GROUP - 1) // FP8_GROUP) * (C_ // FP8_GROUP)),
-        _dev(out, "out", _BF16_LIKE, rows * N), int(flags), int(max_count),
-        _dev(status, "status", _I32, 1, optional=True), _stream(stream)))
+        E, N, C_, _ptr(a, "a", _FP8_CODES, rows * C_, dev),
+        _ptr(a_scale, "a_scale", _fp8_scale_dtypes(flags), rows * fp8_scale_cols(C_, flags), dev),
+        rows, _ptr(row_start, "row_start", _I32, E, dev), _ptr(count, "count", _I32, E, dev),
+        _ptr(w, "w", _FP8_CODES, E * N * C_, dev),
+        _ptr(w_scale, "w_scale", _F32, E * blocks, dev),
+        _ptr(out, "out", _BF16_LIKE, rows * N, dev), int(flags), int(max_count),
+        _ptr(status, "status", _I32, 1, dev, True), _raw_stream(stream, dev)))
 
 
 def moe_swiglu_fp8(E: int, I: int, rows: int, x: torch.Tensor, row_start: torch.Tensor,
                    count: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, flags: int = 0,
                    status: Optional[torch.Tensor] = None, stream=None) -> int:
     rows = int(rows)
-    _here(x, row_start, count, q, scale, status)
+    dev = _device(x, "x")
     return _check("moe_swiglu_fp8", _lib.moe_swiglu_fp8(
-        E, I, rows, _dev(x, "x", _BF16_LIKE, rows * 2 * I), _dev(row_start, "row_start", _I32, E),
-        _dev(count, "count", _I32, E), _dev(q, "q", _FP8_CODES, rows * I),
-        _dev(scale, "scale", _fp8_scale_dtypes(flags), rows * fp8_scale_cols(I, flags)),
-        int(flags), _dev(status, "status", _I32, 1, optional=True), _stream(stream)))
+        E, I, rows, _ptr(x, "x", _BF16_LIKE, rows * 2 * I, dev),
+        _ptr(row_start, "row_start", _I32, E, dev), _ptr(count, "count", _I32, E, dev),
+        _ptr(q, "q", _FP8_CODES, rows * I, dev),
+        _ptr(scale, "scale", _fp8_scale_dtypes(flags), rows * fp8_scale_cols(I, flags), dev),
+        int(flags), _ptr(status, "status", _I32, 1, dev, True), _raw_stream(stream, dev)))
 
 
 def moe_swiglu_grad(E: int, I: int, rows: int, x: torch.Tensor, d_h: torch.Tensor,
                     row_start: torch.Tensor, count: torch.Tensor, d_x: torch.Tensor,
                     status: Optional[torch.Tensor] = None, stream=None) -> int:
     rows = int(rows)
-    _here(x, d_h, row_start, count, d_x, status)
+    dev = _device(x, "x")
     return _check("moe_swiglu_grad", _lib.moe_swiglu_grad(
-        E, I, rows, _dev(x, "x", _BF16_LIKE, rows * 2 * I), _dev(d_h, "d_h", _BF16_LIKE, rows * I),
-        _dev(row_start, "row_start", _I32, E), _dev(count, "count", _I32, E),
-        _dev(d_x, "d_x", _BF16_LIKE, rows * 2 * I),
-        _dev(status, "status", _I32, 1, optional=True), _stream(stream)))
+        E, I, rows, _ptr(x, "x", _BF16_LIKE, rows * 2 * I, dev),
+        _ptr(d_h, "d_h", _BF16_LIKE, rows * I, dev), _ptr(row_start, "row_start", _I32, E, dev),
+        _ptr(count, "count", _I32, E, dev),
+        _ptr(d_x, "d_x", _BF16_LIKE, rows * 2 * I, dev),
+        _ptr(status, "status", _I32, 1, dev, True), _raw_stream(stream, dev)))

@@ -16,8 +16,89 @@ namespace {
 constexpr int kSwThreads = kPlanThreads;
 
 __device__ __forceinline__ float keep_finite(float h) {
-  return fminf(fmaxf(h, -3.402823466e38f), 3.402823466e38f);
+  return __builtin_amdgcn_fmed3f(h, -3.402823466e38f, 3.402823466e38f);
 }
+
+// 1 / (1 + exp(-x)) within six half float steps for |x| <= 87 (one step each for
+// the exponential and the reciprocal, half for the sum and the correction);
+// beyond, 0 or 1. The exponent x log2(e) is carried in two floats: rounded
+// to one, its error would grow to 2^-24 |x| of the result. About 10 instructions
+// against 25 for exp and a correctly rounded quotient.
+__device__ __forceinline__ float sigmoid_of(float x) {
+#pragma clang fp contract(off)
+  constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147181f;
+  const float t = __builtin_amdgcn_fmed3f(x * -kLog2e, -128.0f, 128.0f);
+  const float low = __builtin_fmaf(x, -kLog2e, -t) - x * kLog2eLow;  // of the exact product
+  const float e0 = __builtin_amdgcn_exp2f(t);
+  const float e = fabsf(t) < 128.0f ? __builtin_fmaf(e0, low * kLn2, e0) : e0;
+  return __builtin_amdgcn_rcpf(1.0f + e);
+}
+
+// The rows of all segments, cut evenly into one run per workgroup; its waves
+// take the run's (row, 512-channel chunk) units in turn. A run's rows ascend,
+// so a wave finds the first one's expert by bisection and steps on from there.
+struct RowWalk {
+  int e, lo, hi;  // expert, its rows [lo, hi) among all rows
+  int64_t start;
+  __device__ __forceinline__ void at(const SegmentPlanRows &p, int i) {
+    if (i < hi) return;
+    while (i >= p.first[e + 1]) ++e;
+    set(p);
+  }
+  __device__ __forceinline__ void find(const SegmentPlanRows &p, int E, int i) {
+    e = plan_find(p, E, i);
+    set(p);
+  }
+  __device__ __forceinline__ void set(const SegmentPlanRows &p) {
+    e = __builtin_amdgcn_readfirstlane(e);
+    lo = __builtin_amdgcn_readfirstlane(p.first[e]);
+    hi = __builtin_amdgcn_readfirstlane(p.first[e + 1]);
+    start = __builtin_amdgcn_readfirstlane(p.start[e]);
+  }
+  __device__ __forceinline__ int64_t row(int i) const { return start + (i - lo); }
+};
+
+// Runs body(row, chunk of the row) for the wave's units; load(row, chunk) is
+// called one unit ahead and its result handed to body.
+template <class Load, class Body>
+__device__ __forceinline__ void for_rows(const Segments &seg, const SegmentPlanRows &plan,
+                                         int total, int nchunk, Load load, Body body) {
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  constexpr int kWaves = kSwThreads / 64;
+  const int r0 = (int)((int64_t)total * blockIdx.x / gridDim.x);
+  const int r1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+  int i = r0 + wave / nchunk, c = wave - wave / nchunk * nchunk;  // unit: row i, chunk c
+  if (i >= r1) return;
+  RowWalk walk;
+  walk.find(plan, seg.E, i);
+  int64_t row = walk.row(i);
+  auto v = load(row, c);
+  while (true) {
+    int ni = i, nc = c + kWaves;
+    while (nc >= nchunk) {
+      nc -= nchunk;
+      ++ni;
+    }
+    const bool more = ni < r1;
+    int64_t next = row;
+    auto nv = v;
+    if (more) {
+      walk.at(plan, ni);
+      next = walk.row(ni);
+      nv = load(next, nc);
+    }
+    body(row, c, v);
+    if (!more) return;
+    v = nv;
+    row = next;
+    i = ni;
+    c = nc;
+  }
+}
+
+struct GateUp {
+  ex_u32x4 g, u;
+};
 
 template <int kFlags>
 __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
@@ -28,23 +109,20 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
   const int total = plan_segments(seg, 1, plan, status);
   const int lane = threadIdx.x & 63;
   const int nv = I / 8;  // 16-byte vectors of gates in a row
-  const int64_t units = (int64_t)total * nchunk;
-  const int64_t waves = (int64_t)gridDim.x * (kSwThreads / 64);
-  for (int64_t u = (int64_t)blockIdx.x * (kSwThreads / 64) + (threadIdx.x >> 6); u < units;
-       u += waves) {
-    const int i = (int)(u / nchunk), c = (int)(u - (int64_t)i * nchunk);
-    const int e = plan_find(plan, seg.E, i);
-    const int64_t row = (int64_t)plan.start[e] + (i - plan.first[e]);
-    const int v = c * 64 + lane;
-    const bool in = v < nv;
+  auto load = [&](int64_t row, int c) {
+    const int v = min(c * 64 + lane, nv - 1);
     const ex_u32x4 *xr = x + row * 2 * nv;
-    const ex_u32x4 g = xr[in ? v : 0], up = xr[nv + (in ? v : 0)];
+    return GateUp{__builtin_nontemporal_load(xr + v), __builtin_nontemporal_load(xr + nv + v)};
+  };
+  for_rows(seg, plan, total, nchunk, load, [&](int64_t row, int c, const GateUp &in) {
+    const int v = c * 64 + lane;
+    const bool ok = v < nv;
     float h[8];
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      const float a = ex_lo(g[d]), b = ex_hi(g[d]);
-      h[2 * d] = keep_finite(a / (1.0f + expf(-a)) * ex_lo(up[d]));
-      h[2 * d + 1] = keep_finite(b / (1.0f + expf(-b)) * ex_hi(up[d]));
+      const float a = ex_lo(in.g[d]), b = ex_hi(in.g[d]);
+      h[2 * d] = keep_finite(a * sigmoid_of(a) * ex_lo(in.u[d]));
+      h[2 * d + 1] = keep_finite(b * sigmoid_of(b) * ex_hi(in.u[d]));
     }
     float am = 0.0f;
 #pragma unroll
@@ -60,18 +138,23 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
     const float y = 1.0f / s;
     float d8[8];
 #pragma unroll
-    for (int d = 0; d < 8; ++d) d8[d] = fminf(fmaxf(div_by_scale(h[d], s, y), -448.0f), 448.0f);
-    if (in)
+    for (int d = 0; d < 8; ++d)
+      d8[d] = __builtin_amdgcn_fmed3f(div_by_scale(h[d], s, y), -448.0f, 448.0f);
+    if (ok)
       q[row * nv + v] = ex_u32x2{e4m3x4(d8[0], d8[1], d8[2], d8[3]),
                                  e4m3x4(d8[4], d8[5], d8[6], d8[7])};
     if (kFlags & kFp8Ue8m0) {
       const uint32_t word = ue8m0_word(s);
       if (lane == 0) wscale[row * nchunk + c] = word;
-    } else if (in && (lane & 15) == 0) {
+    } else if (ok && (lane & 15) == 0) {
       fscale[row * (I / kFp8Group) + (v >> 4)] = s;
     }
-  }
+  });
 }
+
+struct GateUpGrad {
+  ex_u32x4 g, u, d;
+};
 
 __global__ __launch_bounds__(kSwThreads) void swiglu_grad_kernel(
     Segments seg, const ex_u32x4 *x, const ex_u32x4 *__restrict__ dh, ex_u32x4 *dx, int32_t nv,
@@ -79,34 +162,35 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_grad_kernel(
   __shared__ SegmentPlanRows plan;
   const int total = plan_segments(seg, 1, plan, status);
   const int lane = threadIdx.x & 63;
-  const int64_t units = (int64_t)total * nchunk;
-  const int64_t waves = (int64_t)gridDim.x * (kSwThreads / 64);
-  for (int64_t u = (int64_t)blockIdx.x * (kSwThreads / 64) + (threadIdx.x >> 6); u < units;
-       u += waves) {
-    const int i = (int)(u / nchunk), c = (int)(u - (int64_t)i * nchunk);
-    const int e = plan_find(plan, seg.E, i);
-    const int64_t row = (int64_t)plan.start[e] + (i - plan.first[e]);
+  // (x may be dx: a unit's vectors are read before they are written, and by no
+  // other wave)
+  auto load = [&](int64_t row, int c) {
+    const int v = min(c * 64 + lane, nv - 1);
+    const ex_u32x4 *xr = x + row * 2 * nv;
+    return GateUpGrad{__builtin_nontemporal_load(xr + v), __builtin_nontemporal_load(xr + nv + v),
+                      __builtin_nontemporal_load(dh + row * nv + v)};
+  };
+  for_rows(seg, plan, total, nchunk, load, [&](int64_t row, int c, const GateUpGrad &in) {
     const int v = c * 64 + lane;
-    if (v >= nv) continue;
-    const int64_t at = row * 2 * nv + v;
-    const ex_u32x4 g = x[at], up = x[at + nv], d = dh[row * nv + v];
+    if (v >= nv) return;
     ex_u32x4 dg, du;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float a[2] = {ex_lo(g[j]), ex_hi(g[j])}, b[2] = {ex_lo(up[j]), ex_hi(up[j])},
-            e[2] = {ex_lo(d[j]), ex_hi(d[j])}, p[2], r[2];
+      float a[2] = {ex_lo(in.g[j]), ex_hi(in.g[j])}, b[2] = {ex_lo(in.u[j]), ex_hi(in.u[j])},
+            e[2] = {ex_lo(in.d[j]), ex_hi(in.d[j])}, p[2], r[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float s = 1.0f / (1.0f + expf(-a[k]));
+        const float s = sigmoid_of(a[k]);
         p[k] = e[k] * b[k] * (s * (1.0f + a[k] * (1.0f - s)));
         r[k] = e[k] * (a[k] * s);
       }
       dg[j] = ex_bf16x2(p[0], p[1]);
       du[j] = ex_bf16x2(r[0], r[1]);
     }
-    dx[at] = dg;
-    dx[at + nv] = du;
-  }
+    const int64_t at = row * 2 * nv + v;
+    __builtin_nontemporal_store(dg, dx + at);
+    __builtin_nontemporal_store(du, dx + at + nv);
+  });
 }
 
 unsigned stream_blocks(const Segments &seg, int32_t nchunk) {

@@ -154,8 +154,8 @@ def test_binding_refusals(lib):
         lib.moe_swiglu_fp8(1, 128, 1, torch.zeros(1, 256, dtype=torch.bfloat16),
                            torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
                            torch.zeros(1, 128, dtype=torch.uint8), torch.zeros(1, 1))
-    with pytest.raises(ValueError, match="in one call"):
-        lib.moe_gate(4, 8, 2, x, idx.to("meta"), w)
+    with pytest.raises(ValueError, match="is required"):
+        lib.moe_gate(4, 8, 2, None, idx, w)
     with pytest.raises(TypeError, match="MOE_GATE_BF16"):
         lib._logits(x, lib.MOE_GATE_BF16)
     from combine_moe_layout_03_amd import ep
