@@ -49,14 +49,16 @@ __device__ __forceinline__ float wave_sum_f(float x) {
   return (lane_f(x, 0) + lane_f(x, 16)) + (lane_f(x, 32) + lane_f(x, 48));
 }
 
-// Maximum over the 64 lanes, wave-uniform.
+// Maximum over the 64 lanes, wave-uniform: each 16-lane row's in its last lane
+// (row_shr by 1, 2, 4, 8), handed on to the next row (row_bcast 15, 31).
 __device__ __forceinline__ uint32_t wave_max_u(uint32_t m) {
-  m = row16_max(m);
-  const uint32_t a = umax32((uint32_t)__builtin_amdgcn_readlane((int)m, 0),
-                            (uint32_t)__builtin_amdgcn_readlane((int)m, 16));
-  const uint32_t b = umax32((uint32_t)__builtin_amdgcn_readlane((int)m, 32),
-                            (uint32_t)__builtin_amdgcn_readlane((int)m, 48));
-  return umax32(a, b);
+  m = umax32(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x111, 0xf, 0xf, true));
+  m = umax32(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x112, 0xf, 0xf, true));
+  m = umax32(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x114, 0xf, 0xf, true));
+  m = umax32(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x118, 0xf, 0xf, true));
+  m = umax32(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x142, 0xa, 0xf, false));
+  m = umax32(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x143, 0xc, 0xf, false));
+  return (uint32_t)__builtin_amdgcn_readlane((int)m, 63);
 }
 
 // Expert e's rows: row_start[e] ... row_start[e] + count[e] - 1, inside

@@ -4,12 +4,14 @@
 // One wave holds one token's E <= 1024 logits, expert e = lane + 64 * j in
 // register j, as unsigned keys whose integer order is the float order (the sign
 // bit flipped, negatives complemented), 0 for an expert that cannot be
-// selected. K times: the largest key of the wave (a maximum per lane, then four
-// DPP steps and four readlanes), and the lowest expert holding it (a ballot per
-// register, lowest register and lane first), which is taken out. Selection thus
-// compares the logits themselves: sigmoid and softmax keep their order, and two
-// logits that a rounded score would merge still rank as they stand. -0 is
-// turned into +0 first, so that the two tie.
+// selected. A lane sorts its keys once (for up to four of them); then K times:
+// the largest head of the 64 lanes (six DPP steps), the lane that holds it (a
+// ballot), whose list moves up. Several lanes with the same key, rare but for
+// bf16 logits and masks, go by the lowest expert id. Selection thus compares the
+// logits themselves: sigmoid and softmax keep their order, and two logits that
+// a rounded score would merge still rank as they stand. -0 is turned into +0
+// first, so that the two tie. What bounds the kernel is instructions, not the
+// logits' bytes: MEASURED
 //
 // Lane k then holds the k-th logit, and the weights of a token are computed in
 // its lanes at once. All statistics are float; the renormalised weights come
@@ -45,6 +47,13 @@ __device__ __forceinline__ uint32_t gate_key(float x, bool *bad) {
 __device__ __forceinline__ float key_logit(uint32_t k) {  // 0 -> -infinity
   if (k <= kKeyNegInf) return -INFINITY;
   return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);
+}
+
+// exp(d) for d <= 0: the exponent d log2(e) is rounded once, so the result is off
+// by 2^-24 |d| and one step. For the sum over all experts, where the terms of
+// large |d| are small against the first, which is 1.
+__device__ __forceinline__ float exp_below(float d) {
+  return __builtin_amdgcn_exp2f(d * 1.44269504f);
 }
 
 __device__ __forceinline__ float log_sigmoid(float x) {  // x may be -infinity
@@ -91,30 +100,70 @@ __global__ __launch_bounds__(256) void gate_kernel(const void *__restrict__ x, i
     key[j] = e < E ? gate_key(gate_load(x, (int64_t)t * E + e, bf16), &bad) : 0u;
   }
   uint32_t k0[V];
+  int slot[V];  // the register a key came from
 #pragma unroll
-  for (int j = 0; j < V; ++j) k0[j] = key[j];
+  for (int j = 0; j < V; ++j) {
+    k0[j] = key[j];
+    slot[j] = j;
+  }
+  constexpr bool kSorted = V <= 4;
+  if (kSorted) {  // larger first, equal keys as they were
+#pragma unroll
+    for (int a = 0; a < V - 1; ++a)
+#pragma unroll
+      for (int b = 0; b < V - 1 - a; ++b) {
+        const bool up = key[b + 1] > key[b];
+        const uint32_t k1 = up ? key[b + 1] : key[b], k2 = up ? key[b] : key[b + 1];
+        const int s1 = up ? slot[b + 1] : slot[b], s2 = up ? slot[b] : slot[b + 1];
+        key[b] = k1;
+        key[b + 1] = k2;
+        slot[b] = s1;
+        slot[b + 1] = s2;
+      }
+  }
   int my_id = -1;
   uint32_t my_key = 0, top_key = 0;
   for (int k = 0; k < K; ++k) {
-    uint32_t m = key[0];
+    uint32_t head = key[0];
+    int at = slot[0];
+    if (!kSorted) {
 #pragma unroll
-    for (int j = 1; j < V; ++j) m = umax32(m, key[j]);
-    m = wave_max_u(m);
+      for (int j = 1; j < V; ++j) {
+        const bool up = key[j] > head;
+        head = up ? key[j] : head;
+        at = up ? j : at;
+      }
+    }
+    const uint32_t m = wave_max_u(head);
     if (k == 0) top_key = m;
     if (m == 0) break;  // no selectable expert is left (uniform)
-    int id = -1;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint64_t b = __ballot(key[j] == m);
-      if (id < 0 && b) {  // uniform
-        const int l = __ffsll((unsigned long long)b) - 1;
-        id = l + 64 * j;
-        if (lane == l) key[j] = 0;
+    uint64_t tied = __ballot(head == m);
+    int l = __ffsll((unsigned long long)tied) - 1;
+    int id = l + 64 * __builtin_amdgcn_readlane(at, l);
+    while (tied &= tied - 1) {  // uniform
+      const int l2 = __ffsll((unsigned long long)tied) - 1;
+      const int id2 = l2 + 64 * __builtin_amdgcn_readlane(at, l2);
+      if (id2 < id) {
+        id = id2;
+        l = l2;
       }
     }
     if (lane == k) {
       my_id = id;
       my_key = m;
+    }
+    if (lane == l) {
+      if (kSorted) {
+#pragma unroll
+        for (int j = 0; j + 1 < V; ++j) {
+          key[j] = key[j + 1];
+          slot[j] = slot[j + 1];
+        }
+        key[V - 1] = 0;
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = j == at ? 0u : key[j];
+      }
     }
   }
   const float top = key_logit(top_key);
@@ -122,7 +171,7 @@ __global__ __launch_bounds__(256) void gate_kernel(const void *__restrict__ x, i
   if (!(kMode & (kGateSigmoid | kGateRenorm))) {
     float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) s += k0[j] ? expf(key_logit(k0[j]) - top) : 0.0f;
+    for (int j = 0; j < V; ++j) s += k0[j] ? exp_below(key_logit(k0[j]) - top) : 0.0f;
     sum = wave_sum_f(s);
   }
   const float p = gate_score<kMode>(key_logit(my_key), top, sum);
@@ -174,7 +223,7 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      v[j] = key[j] ? expf(key_logit(key[j]) - top) : 0.0f;
+      v[j] = key[j] ? exp_below(key_logit(key[j]) - top) : 0.0f;
       s += v[j];
     }
     sum = wave_sum_f(s);

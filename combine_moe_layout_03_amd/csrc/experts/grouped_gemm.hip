@@ -293,8 +293,9 @@ enum ScaleLayout {
   kScaleVector,  // row-major floats, four of a token in one 16-byte copy
   kScaleSingle,  // anything else: a copy per group
 };
+constexpr int kScaleTokens = (kTileTokens + 63) / 64 * 64;  // whole copies of 64
 struct TileScales {
-  float tokens[4 * kTileTokens];  // kScaleVector: [token][4], else [group][token]
+  float tokens[4 * kScaleTokens];  // kScaleVector: [token][4], else [group][token]
   float weights[64];              // [16 weight rows][4]
 };
 struct TileBuffers {
@@ -342,11 +343,10 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
       copy16_to_lds(tbase + (int64_t)min(g, G - 1) * kFp8Group, to_off[i],
                     lds_a + to * (kTileTokens * 128) + i * kTileWaves * 1024);
   };
-  // Scales: waves 0-4 copy those of 64 tokens each (the last of 32), wave 5
+  // Scales: waves 0-4 copy those of 64 tokens each, wave 5
   // those of the weights, a lane one of the twelve 16-row blocks and a group.
   const uint32_t *sbase = scalar(static_cast<const uint32_t *>(ga.a_scale) + p.scale_base);
-  const int stok = wave * 64 + lane;
-  const uint32_t so = (uint32_t)min(stok, p.tokens - 1) * (uint32_t)p.r_stride * 4;
+  const uint32_t so = (uint32_t)min(wave * 64 + lane, p.tokens - 1) * (uint32_t)p.r_stride * 4;
   const bool scopy = wave < (TT + 1) / 2;  // uniform
   const float *wsbase =
       scalar(ga.w_scale + ((int64_t)p.e * ((ga.N + 127) / 128) + p.n0 / 128) * G);
@@ -363,15 +363,13 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
       return true;
     }
     if (!scopy || (kScale != kScaleSingle && part > 0)) return false;
-    if (stok < kTileTokens) {
-      if (kScale == kScaleVector)
-        copy16_to_lds(sbase + 4 * min(b, G / 4 - 1), so, lds_s + to + wave * 1024);
-      else if (kScale == kScaleWord)
-        copy4_to_lds(sbase + min(b, G / 4 - 1) * p.g_stride, so, lds_s + to + wave * 256);
-      else
-        copy4_to_lds(sbase + min(4 * b + part, G - 1) * p.g_stride, so,
-                     lds_s + to + (part * kTileTokens + wave * 64) * 4);
-    }
+    if (kScale == kScaleVector)
+      copy16_to_lds(sbase + 4 * min(b, G / 4 - 1), so, lds_s + to + wave * 1024);
+    else if (kScale == kScaleWord)
+      copy4_to_lds(sbase + min(b, G / 4 - 1) * p.g_stride, so, lds_s + to + wave * 256);
+    else
+      copy4_to_lds(sbase + min(4 * b + part, G - 1) * p.g_stride, so,
+                   lds_s + to + (part * kScaleTokens + wave * 64) * 4);
     return true;
   };
 
@@ -391,7 +389,7 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
     auto scale = [&](int t) {
       const int r = (wt * TT + t) * 16 + l16;
       if (kScale == kScaleVector) return sc.tokens[r * 4 + gi];
-      if (kScale == kScaleSingle) return sc.tokens[gi * kTileTokens + r];
+      if (kScale == kScaleSingle) return sc.tokens[gi * kScaleTokens + r];
       return byte_scale(__float_as_uint(sc.tokens[r]), gi);
     };
     i32x8 w[3], a[3];
@@ -486,12 +484,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void grouped_gemm_tile_kernel(Segm
   const int pieces = scalar(plan_segments<kTileThreads>(seg, kTileTokens, plan, ga.status));
   const int G = ga.C / kFp8Group, SG = kScale == kScaleWord ? G / 4 : G;  // scale entries of a row
   const int nblk = (ga.N + kTileN - 1) / kTileN;
-  // Workgroup b runs on XCD b % 8: each XCD takes one run of the tiles, so the
-  // tiles in flight on it share weights and token rows in its L2.
+  // Workgroup b runs on XCD b % 8. In every round the XCD's workgroups take
+  // neighbouring tiles, which share weights and token rows in its L2; the rounds
+  // go through the experts together, so that one with many rows does not stay
+  // with one XCD.
   const int64_t tiles = (int64_t)pieces * nblk;
-  const int xcd = blockIdx.x & 7, lanes = gridDim.x >> 3;
-  const int64_t lo = tiles * xcd / 8, hi = tiles * (xcd + 1) / 8;
-  for (int64_t u = lo + (blockIdx.x >> 3); u < hi; u += lanes) {
+  const int lanes = gridDim.x >> 3;
+  for (int64_t u = (int64_t)(blockIdx.x & 7) * lanes + (blockIdx.x >> 3); u < tiles; u += gridDim.x) {
     TilePos p;
     // wave-uniform values, kept in scalar registers
     p.e = scalar(plan_find(plan, seg.E, (int)(u / nblk)));
