@@ -84,7 +84,7 @@ __device__ __forceinline__ float byte_scale(uint32_t word, int e) {
 // multiplied. With fewer units than half the waves on the chip the eight waves
 // of a workgroup share a unit's groups out instead and join their sums in LDS.
 
-constexpr int kStreamTokens = 16;  // token rows of a unit
+constexpr int kStreamTokens = 16;  // most token rows of a unit
 constexpr int kStreamN = 32;       // weight rows of a unit
 constexpr int kStreamWaves = 8;
 constexpr int kStreamThreads = kStreamWaves * 64;
@@ -124,17 +124,13 @@ __global__ __launch_bounds__(kStreamThreads, 2) void grouped_gemm_stream_kernel(
   const int64_t u_step = split ? gridDim.x : (int64_t)gridDim.x * kStreamWaves;
   const int g_first = split ? wave : 0, g_step = split ? kStreamWaves : 1;
 
-  // unit u: an expert's pieces of 16 rows side by side, then its next weight rows
-  auto unit = [&](int64_t u) {
+  auto unit = [&](int64_t u) {  // one piece per segment: its blocks of weight rows in turn
     StreamUnit x;
     x.e = scalar(plan_find(sh.plan, seg.E, (int)(u / nblk)));
-    const int first = scalar(sh.plan.first[x.e]), np = scalar(sh.plan.first[x.e + 1]) - first;
-    const int r = scalar((int)(u - (int64_t)first * nblk));
-    const int nb = scalar(r / np), t0 = (r - nb * np) * kStreamTokens;
-    x.n0 = nb * kStreamN;
+    x.n0 = scalar((int)(u - (int64_t)scalar(sh.plan.first[x.e]) * nblk)) * kStreamN;
     // (from LDS: a load from memory here would wait for every copy in flight)
-    x.tokens = min(scalar(sh.plan.rows[x.e]) - t0, kStreamTokens);
-    x.row0 = (int64_t)scalar(sh.plan.start[x.e]) + t0;
+    x.tokens = scalar(sh.plan.rows[x.e]);
+    x.row0 = scalar(sh.plan.start[x.e]);
     return x;
   };
 
@@ -524,16 +520,18 @@ __global__ __launch_bounds__(kTileThreads, 2) void grouped_gemm_tile_kernel(Segm
   }
 }
 
-// Segments of up to this many rows are streamed, larger ones tiled.
-constexpr int kStreamMost = 32;
-static_assert(kStreamMost <= 255, "SegmentPlanRows::rows holds bytes");
+// A segment of one stream unit's rows is streamed, a larger one tiled. (With
+// the border at 32 or 64 rows, streamed in pieces of 16 that read the weights
+// again: 1024 x 8 rows over 256 experts, 7168 x 4096, 4.3 or 3.0 TB/s of weights
+// against 5.4; 128 x 8 rows over 32 experts 3.3 or 3.1 against 4.8.)
+constexpr int kStreamMost = kStreamTokens;
 
 }  // namespace
 
 hipError_t launch_grouped_gemm(const Segments &seg, const GemmArgs &g, hipStream_t s) {
   const bool words = g.flags & kFp8Ue8m0;
   const int64_t nblk = (g.N + kStreamN - 1) / kStreamN;
-  const int64_t most = ((seg.rows + kStreamTokens - 1) / kStreamTokens + seg.E) * nblk;
+  const int64_t most = seg.E * nblk;
   const unsigned grid = (unsigned)(most < 256 ? most : 256);  // one workgroup per CU
   // how many rows a segment can have at most decides which kernels are needed
   const int64_t bound = seg.max_count > 0 ? seg.max_count

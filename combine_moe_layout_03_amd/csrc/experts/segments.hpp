@@ -16,7 +16,7 @@ struct SegmentPlan {
 };
 struct SegmentPlanRows : SegmentPlan {
   int32_t start[kMaxExperts];  // first buffer row of expert e
-  uint8_t rows[kMaxExperts];   // its rows, where a kernel's share has at most 255
+  uint8_t rows[kMaxExperts];   // its rows, for a kernel whose share has at most 255
 };
 
 // Cuts every segment into ceil(rows / piece) pieces and returns their number.

@@ -141,8 +141,9 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
     for (int d = 0; d < 8; ++d)
       d8[d] = __builtin_amdgcn_fmed3f(div_by_scale(h[d], s, y), -448.0f, 448.0f);
     if (ok)
-      q[row * nv + v] = ex_u32x2{e4m3x4(d8[0], d8[1], d8[2], d8[3]),
-                                 e4m3x4(d8[4], d8[5], d8[6], d8[7])};
+      __builtin_nontemporal_store(ex_u32x2{e4m3x4(d8[0], d8[1], d8[2], d8[3]),
+                                           e4m3x4(d8[4], d8[5], d8[6], d8[7])},
+                                  q + row * nv + v);
     if (kFlags & kFp8Ue8m0) {
       const uint32_t word = ue8m0_word(s);
       if (lane == 0) wscale[row * nchunk + c] = word;
