@@ -10,8 +10,8 @@
 // bf16 logits and masks, go by the lowest expert id. Selection thus compares the
 // logits themselves: sigmoid and softmax keep their order, and two logits that
 // a rounded score would merge still rank as they stand. -0 is turned into +0
-// first, so that the two tie. What bounds the kernel is instructions, not the
-// logits' bytes: MEASURED
+// first, so that the two tie. What bounds the kernel is instructions
+// (about 400 per token of 256 experts and eight places), not the logits' bytes.
 //
 // Lane k then holds the k-th logit, and the weights of a token are computed in
 // its lanes at once. All statistics are float; the renormalised weights come
@@ -29,24 +29,45 @@
 namespace moe {
 namespace {
 
-constexpr uint32_t kKeyNegInf = 0x007fffffu;  // the key of -infinity
+constexpr uint32_t kKeyNegInf = 0x007fffffu;  // the keys of the infinities
+constexpr uint32_t kKeyPosInf = 0xff800000u;
 
 __device__ __forceinline__ float gate_load(const void *x, int64_t i, bool bf16) {
   return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(x)[i] << 16)
               : static_cast<const float *>(x)[i];
 }
+// A token's logits lane + 64 j, all loads in flight together (past the last
+// expert the last one's again, which the callers leave out).
+template <int V>
+__device__ __forceinline__ void gate_row(const void *x, int64_t row, int E, bool bf16,
+                                         float (&v)[V]) {
+  const int lane = threadIdx.x & 63;
+  if (bf16) {
+    const uint16_t *p = static_cast<const uint16_t *>(x) + row;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      v[j] = __uint_as_float((uint32_t)p[min(lane + 64 * j, E - 1)] << 16);
+  } else {
+    const float *p = static_cast<const float *>(x) + row;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = p[min(lane + 64 * j, E - 1)];
+  }
+}
 
-// Key of a selectable logit, 0 for -infinity; NaN and +infinity also give 0 and set bad.
+// Key of a selectable logit, 0 for -infinity; NaN and +infinity also give 0 and
+// set bad. The keys of the finite floats are those between the infinities',
+// which NaN of either sign fall outside of.
 __device__ __forceinline__ uint32_t gate_key(float x, bool *bad) {
-  const uint32_t u = __float_as_uint(x + 0.0f);
-  const uint32_t k = (u >> 31) ? ~u : (u | 0x80000000u);
-  const bool fin = (u & 0x7f800000u) != 0x7f800000u;
-  *bad = *bad || (!fin && u != 0xff800000u);
+  const int32_t u = (int32_t)__float_as_uint(x + 0.0f);
+  const uint32_t k = (uint32_t)(u ^ ((u >> 31) | (int32_t)0x80000000));
+  const bool fin = k - (kKeyNegInf + 1u) < kKeyPosInf - (kKeyNegInf + 1u);
+  *bad = *bad || (!fin && k != kKeyNegInf);
   return fin ? k : 0u;
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {  // 0 -> -infinity
-  if (k <= kKeyNegInf) return -INFINITY;
-  return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);
+  const int32_t u = (int32_t)k;
+  const float f = __uint_as_float((uint32_t)(u ^ (~(u >> 31) | (int32_t)0x80000000)));
+  return k ? f : -INFINITY;
 }
 
 // exp(d) for d <= 0: the exponent d log2(e) is rounded once, so the result is off
@@ -94,10 +115,12 @@ __global__ __launch_bounds__(256) void gate_kernel(const void *__restrict__ x, i
   if (t >= T) return;
   uint32_t key[V];
   bool bad = false;
+  float logit[V];
+  gate_row<V>(x, (int64_t)t * E, E, bf16, logit);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int e = lane + 64 * j;
-    key[j] = e < E ? gate_key(gate_load(x, (int64_t)t * E + e, bf16), &bad) : 0u;
+    const uint32_t k = gate_key(logit[j], &bad);
+    key[j] = lane + 64 * j < E ? k : 0u;
   }
   uint32_t k0[V];
   int slot[V];  // the register a key came from
@@ -166,12 +189,13 @@ __global__ __launch_bounds__(256) void gate_kernel(const void *__restrict__ x, i
       }
     }
   }
-  const float top = key_logit(top_key);
+  // (a token without a selectable expert: every term is 0, no difference of infinities)
+  const float top = top_key ? key_logit(top_key) : 0.0f;
   float sum = 1.0f;
   if (!(kMode & (kGateSigmoid | kGateRenorm))) {
     float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) s += k0[j] ? exp_below(key_logit(k0[j]) - top) : 0.0f;
+    for (int j = 0; j < V; ++j) s += exp_below(key_logit(k0[j]) - top);
     sum = wave_sum_f(s);
   }
   const float p = gate_score<kMode>(key_logit(my_key), top, sum);
@@ -193,6 +217,9 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(
   const int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (blockDim.x >> 6) +
                                                      (threadIdx.x >> 6)));
   if (t >= T) return;
+  constexpr bool kAll = !kSig && !kRenorm;  // softmax over all experts
+  float logit[V];
+  if (kAll) gate_row<V>(x, (int64_t)t * E, E, bf16, logit);
   int id = -1;
   float d = 0.0f, xs = -INFINITY;
   int st = 0;
@@ -209,21 +236,21 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(
   }
   if (xs == -INFINITY) id = -1;  // masked: contributes nothing
   float v[V], top = -INFINITY, sum = 1.0f;
-  constexpr bool kAll = !kSig && !kRenorm;  // softmax over all experts
   uint32_t key[V];
   if (kAll) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int e = lane + 64 * j;
-      key[j] = e < E ? gate_key(gate_load(x, (int64_t)t * E + e, bf16), &bad) : 0u;
+      const uint32_t k = gate_key(logit[j], &bad);
+      key[j] = lane + 64 * j < E ? k : 0u;
       m = umax32(m, key[j]);
     }
-    top = key_logit(wave_max_u(m));
+    const uint32_t tk = wave_max_u(m);
+    top = tk ? key_logit(tk) : 0.0f;
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      v[j] = key[j] ? exp_below(key_logit(key[j]) - top) : 0.0f;
+      v[j] = exp_below(key_logit(key[j]) - top);
       s += v[j];
     }
     sum = wave_sum_f(s);
@@ -254,15 +281,16 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] += (ik == lane + 64 * j) ? gk : 0.0f;
   }
+  if (bf16) {
+    uint16_t *o = static_cast<uint16_t *>(dx) + (int64_t)t * E;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane + 64 * j;
-    if (e >= E) continue;
-    const int64_t o = (int64_t)t * E + e;
-    if (bf16)
-      static_cast<uint16_t *>(dx)[o] = (uint16_t)ex_bf16(v[j]);
-    else
-      static_cast<float *>(dx)[o] = v[j];
+    for (int j = 0; j < V; ++j)
+      if (lane + 64 * j < E) o[lane + 64 * j] = (uint16_t)ex_bf16(v[j]);
+  } else {
+    float *o = static_cast<float *>(dx) + (int64_t)t * E;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (lane + 64 * j < E) o[lane + 64 * j] = v[j];
   }
   const uint64_t be = __ballot(st != 0), bl = __ballot(bad);
   if (status && lane == 0 && (be | bl))

@@ -45,6 +45,11 @@ __device__ __forceinline__ void copy16_to_lds(const void *base, uint32_t off, ui
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :: "s"(scalar((int)to)), "v"(off), "s"(scalar(base)) : "memory", "m0");
 }
+// The same for bytes that nobody reads again: marked to leave L2 first.
+__device__ __forceinline__ void copy16_once(const void *base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+               :: "s"(scalar((int)to)), "v"(off), "s"(scalar(base)) : "memory", "m0");
+}
 __device__ __forceinline__ void copy4_to_lds(const void *base, uint32_t off, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                :: "s"(scalar((int)to)), "v"(off), "s"(scalar(base)) : "memory", "m0");
@@ -169,7 +174,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void grouped_gemm_stream_kernel(
     const uint32_t st = ring0 + slot * (uint32_t)sizeof(StreamStage);
     const int64_t k = (int64_t)g * kFp8Group;
 #pragma unroll
-    for (int i = 0; i < kStreamN / 8; ++i) copy16_to_lds(wbase + k, wo[i], st + i * 1024);
+    for (int i = 0; i < kStreamN / 8; ++i) copy16_once(wbase + k, wo[i], st + i * 1024);
 #pragma unroll
     for (int i = 0; i < kStreamTokens / 8; ++i)
       copy16_to_lds(tbase + k, to[i], st + kStreamN * 128 + i * 1024);
@@ -405,9 +410,10 @@ __device__ __forceinline__ void tile_product(const GemmArgs &ga, const TilePos &
       const int t = q / 3, i = q % 3;
       if (q < 3 * TT) {
         if (i == 0 && t + 2 < TT) a[(t + 2) % 3] = rows16(buf, t + 2);
-        if (i == 1) {
+        if (i == 1) {  // two at a time, or what it takes
+          constexpr int kPer = kSlots > 2 * TT ? (kSlots + TT - 1) / TT : 2;
 #pragma unroll
-          for (int c = t * kSlots / TT; c < (t + 1) * kSlots / TT; ++c) copy(c);
+          for (int c = t * kPer; c < (t + 1) * kPer && c < kSlots; ++c) copy(c);
         }
         if (q >= 3) {
           f32x4 &done = acc[i][t - 1];
