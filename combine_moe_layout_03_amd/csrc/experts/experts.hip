@@ -45,6 +45,10 @@ bool on(const void *p, uintptr_t bytes) {  // aligned to that many bytes (a powe
 
 int launched(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
 
+// A launch holds fewer than 2^32 threads: at most this many waves, with a
+// workgroup to spare.
+constexpr int64_t kMaxWaveRows = (1 << 26) - 64;
+
 // The FP8 flags and the channel counts they need.
 int fp8_flags_ok(int32_t channels, int32_t flags) {
   constexpr int kCast = MOE_FP8_ROUND_SCALE | MOE_FP8_UE8M0;
@@ -56,7 +60,7 @@ int fp8_flags_ok(int32_t channels, int32_t flags) {
 
 int gate_ok(int32_t T, int32_t E, int32_t K, int32_t flags, float scale) {
   if (T < 0 || E < 1 || E > kMaxExperts || K < 1 || K > 64 || K > E) return MOE_ERR_SHAPE;
-  if ((int64_t)T * K >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
+  if (T > kMaxWaveRows) return MOE_ERR_SHAPE;
   if (flags & ~(MOE_GATE_BF16 | MOE_GATE_SIGMOID | MOE_GATE_RENORM)) return MOE_ERR_FLAGS;
   if (!std::isfinite(scale)) return MOE_ERR_SHAPE;
   return MOE_OK;
@@ -109,8 +113,8 @@ MOE_API int moe_combine_grad(const moe_shape *s, const uint16_t *d_out, const ui
       s->E % s->R != 0 || s->A < 1 || s->A > (1 << 16) || s->H < 8 || s->H > (1 << 20) ||
       s->H % 8 != 0)
     return MOE_ERR_SHAPE;
-  // one workgroup per pair, tokens rounded up to eights
-  if (((int64_t)s->T + 7) * s->K >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
+  // one workgroup of four waves per pair, tokens rounded up to eights
+  if (((int64_t)s->T + 7) * s->K * 4 > kMaxWaveRows) return MOE_ERR_SHAPE;
   if (recv_rows < 0) return MOE_ERR_CAPACITY;
   if (!topk_idx != !rank_mask) return MOE_ERR_NULL;
   if (s->T == 0) return MOE_OK;

@@ -12,7 +12,9 @@
  *   moe_grouped_gemm_fp8 (down) -> moe_combine
  * and backward: moe_combine_grad (rows and weights), moe_swiglu_grad,
  * moe_combine with topk_weights = NULL (the gradient of the dispatch is the
- * plain sum of a token's rows), moe_gate_grad.
+ * plain sum of a token's rows), moe_gate_grad. The gradient of a product with
+ * respect to its rows is the product with the transposed weights; the gradient
+ * with respect to the weights is not part of this library.
  *
  * The conventions of moe_ep.h hold: caller-owned device pointers, nothing
  * allocated, freed or kept between calls, every call enqueues on the caller's
@@ -59,7 +61,7 @@ extern "C" {
  *     sigmoid + renorm:  w_k = scale * s_k / sum over the selected j of s_j
  *   (the renormalised sigmoids from log s, so that sums which would underflow
  *   do not divide by zero).
- * 1 <= E <= 1024, 1 <= K <= min(E, 64), scale finite. logits and topk_weights
+ * 0 <= T <= 2^26 - 64, 1 <= E <= 1024, 1 <= K <= min(E, 64), scale finite. logits and topk_weights
  * 4-byte aligned (bf16 logits: 2), topk_idx 8-byte. status may be NULL. */
 int moe_gate(int32_t T, int32_t E, int32_t K, const void *logits, int64_t *topk_idx,
              float *topk_weights, int32_t flags, float scale, int32_t *status,
@@ -88,8 +90,8 @@ int moe_gate_grad(int32_t T, int32_t E, int32_t K, const void *logits, const int
  *   (one of the two products is left in the row). A slot outside
  *   [-1, recv_rows) sets MOE_STATUS_BAD_SLOT (also on a masked rank: its row
  *   would be written), gets d_weights 0 and no row.
- * Needs T*K < 2^31 and the shape limits of moe_combine. d_out, y and d_y
- * 16-byte aligned, d_y must not overlap d_out or y. The gradient of the
+ * Needs (T + 7) * K <= 2^24 - 16 and the shape limits of moe_combine. d_out, y
+ * and d_y 16-byte aligned, d_y must not overlap d_out or y. The gradient of the
  * dispatch is moe_combine with topk_weights = NULL. */
 int moe_combine_grad(const moe_shape *shape, const uint16_t *d_out, const uint16_t *y,
                      int64_t recv_rows, const int32_t *slot, const float *topk_weights,

@@ -41,7 +41,7 @@ def test_exports_every_declared_symbol(lib):
 @pytest.mark.parametrize("T,E,K,flags,scale,code", [
     (-1, 8, 2, 0, 1.0, SHAPE), (4, 0, 1, 0, 1.0, SHAPE), (4, 1025, 1, 0, 1.0, SHAPE),
     (4, 8, 0, 0, 1.0, SHAPE), (4, 8, 9, 0, 1.0, SHAPE), (4, 128, 65, 0, 1.0, SHAPE),
-    (1 << 30, 8, 2, 0, 1.0, SHAPE), (4, 8, 2, 8, 1.0, FLAGS), (4, 8, 2, -1, 1.0, FLAGS),
+    ((1 << 26) - 63, 8, 2, 0, 1.0, SHAPE), (4, 8, 2, 8, 1.0, FLAGS), (4, 8, 2, -1, 1.0, FLAGS),
     (4, 8, 2, 0, float("nan"), SHAPE), (4, 8, 2, 0, float("inf"), SHAPE)])
 def test_gate_shapes(lib, T, E, K, flags, scale, code):
     raw = lib.lib()
@@ -78,7 +78,7 @@ def test_combine_grad_checks(lib):
     ok = lib.make_shape(4, 16, 16, 4, 2)
     assert call(None) == NULL
     for bad in ((-1, 16, 16, 4, 2), (4, 12, 16, 4, 2), (4, 0, 16, 4, 2), (4, 16, 16, 3, 2),
-                (4, 16, 1025, 1, 2), (4, 16, 16, 4, 0), (4, 16, 16, 4, 65), (1 << 30, 16, 16, 4, 2)):
+                (4, 16, 1025, 1, 2), (4, 16, 16, 4, 0), (4, 16, 16, 4, 65), (1 << 23, 16, 16, 4, 2)):
         assert call(lib.make_shape(*bad)) == SHAPE
     assert call(ok, rows=-1) == CAPACITY
     for kw in (dict(do=None), dict(slot=None), dict(dy=None), dict(y=None), dict(idx=D),

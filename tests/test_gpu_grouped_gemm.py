@@ -279,6 +279,76 @@ def test_large_beside_small_products(capi):
     assert np.all(got[k.live] == want)
 
 
+@pytest.mark.parametrize("counts", [[3, 2], [70, 20]], ids=["streamed", "tiled"])
+def test_nan_stays_in_its_row_and_column(capi, counts):
+    """A NaN code or scale of a row spoils that row, one of a weight row its
+    column, for that expert alone."""
+    k = Case(61, counts, 200, 512, ROWS)
+    k.a[k.start[0] + 1, 300] = 0x7F
+    k.scale[k.start[1], 2] = np.nan
+    k.w[1, 77, 5] = 0xFF
+    got = mi.bf16_bits_to_f32(k.run(capi)).astype(np.float64)
+    nan = np.zeros(got.shape, bool)
+    nan[k.start[0] + 1] = True
+    nan[k.start[1]] = True
+    nan[k.start[1]:k.start[1] + counts[1], 77] = True
+    assert np.array_equal(np.isnan(got), nan & (np.isin(np.arange(k.rows), k.live)[:, None]))
+    # a zero scale gives +-0 or nothing, an infinite one NaN or infinities, in its row alone
+    k = Case(62, counts, 40, 256, ROWS)
+    k.scale[k.start[0]] = 0.0
+    k.scale[k.start[1]] = np.inf
+    got = mi.bf16_bits_to_f32(k.run(capi)).astype(np.float64)
+    assert np.all(got[k.start[0]] == 0) and not np.isfinite(got[k.start[1]]).any()
+    rest = np.setdiff1d(k.live, [k.start[0], k.start[1]])
+    assert np.isfinite(got[rest]).all()
+
+
+def test_byte_scales_of_every_exponent(capi):
+    """UE8M0 bytes 0 ... 254 as the powers of two they stand for."""
+    for counts in ([16], [64]):
+        k = Case(63, counts, 8, 512, ROWS | ROUND | WORDS)
+        n = counts[0]
+        k.a[k.live], k.w[:], k.ws[:] = 0x38, 0x38, 1.0  # ones
+        byte = (np.arange(n) * 4 % 255).astype(np.int64)
+        k.scale[k.live, 0] = byte.astype(np.int32)  # the first group's; the others' 2^-127
+        got = mi.bf16_bits_to_f32(k.run(capi)).astype(np.float64)[k.live]
+        want = 128 * (np.exp2(byte - 127.0) + 3 * np.exp2(-127.0))
+        fin = want < 3.3e38
+        assert np.all(np.abs(got - want[:, None])[fin] <= ref.HALF_BF16 * want[fin, None])
+        assert np.all(np.isinf(got[~fin]))
+
+
+def test_graph_of_both_kernels(capi):
+    """A captured product whose segments are streamed and tiled, replayed on new
+    rows and counts with eager calls between: every replay equals the eager one."""
+    k = Case(71, [40, 3, 0, 100], 264, 512, ROWS)
+    d = [to_dev(v) for v in (k.a, k.scale, k.start, np.array(k.counts, np.int32), k.w, k.ws)]
+    out = torch.zeros(k.rows, k.N, dtype=torch.int16, device=dev())
+    other = torch.zeros_like(out)
+    cnt = [[40, 3, 0, 100], [0, 3, 0, 17], [1, 0, 0, 0], [40, 1, 0, 99]]
+
+    def step(o, s):
+        capi.moe_grouped_gemm_fp8(k.E, k.N, k.C, d[0], d[1], k.rows, d[2], d[3], d[4], d[5], o,
+                                  k.flags, 0, None, s)
+
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    step(out, stream)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        step(out, stream)
+    for c in cnt:
+        d[3].copy_(torch.tensor(c, dtype=torch.int32))
+        out.fill_(5)
+        other.fill_(5)
+        step(other, None)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, other)
+
+
 def test_streams_and_repeat(capi):
     """Two calls at once on two streams, then again: the same bits."""
     ks = [Case(41, [90, 3, 0, 40], 264, 512, ROWS), Case(42, [1, 2, 3, 200], 128, 1024, ROWS)]
