@@ -322,6 +322,9 @@ def gate_grad(logits: torch.Tensor, topk_idx: torch.Tensor, d_weights: torch.Ten
               status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of ``gate``'s weights: d_logits [T, E] in the logits' type."""
     T, E = logits.shape
+    if topk_idx.shape != d_weights.shape or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx {tuple(topk_idx.shape)} and d_weights "
+                         f"{tuple(d_weights.shape)} for {T} tokens")
     x = logits.contiguous()
     d = torch.empty_like(x)
     capi.moe_gate_grad(T, E, topk_idx.shape[1], x, topk_idx.contiguous(), d_weights.contiguous(),
@@ -337,6 +340,9 @@ def combine_grad(d_out: torch.Tensor, y: torch.Tensor, handle: Handle,
     written. rank_mask as in low_latency_combine (it needs the handle of a
     low-latency dispatch, which carries the routing)."""
     T, H = d_out.shape
+    if T != handle.shape.T or y.shape[-1] != H:
+        raise ValueError(f"d_out {tuple(d_out.shape)} for {handle.shape.T} tokens and expert "
+                         f"rows of {y.shape[-1]}")
     shape = capi.make_shape(T, H, handle.shape.E, handle.shape.R, handle.shape.K, handle.shape.A)
     if rank_mask is not None and handle.topk_idx is None:
         raise ValueError("rank_mask needs a handle that carries topk_idx")
@@ -371,6 +377,11 @@ def expert_gemm(x: Tuple[torch.Tensor, torch.Tensor], weight: Tuple[torch.Tensor
     q, sc = x
     w, ws = weight
     E, N, Cc = w.shape
+    if E != handle.shape.E or q.shape[-1] != Cc:
+        raise ValueError(f"weights {tuple(w.shape)} for {handle.shape.E} experts and rows of "
+                         f"{q.shape[-1]}")
+    if ws.shape != (E, -(-N // capi.FP8_GROUP), Cc // capi.FP8_GROUP):
+        raise ValueError(f"scales {tuple(ws.shape)} for weights {tuple(w.shape)}")
     rows = handle.recv_rows
     flags = capi.MOE_FP8_SCALE_ROWS
     if sc.dtype == torch.int32:
@@ -390,13 +401,19 @@ def expert_gemm(x: Tuple[torch.Tensor, torch.Tensor], weight: Tuple[torch.Tensor
     return out
 
 
+def _half(x: torch.Tensor) -> int:
+    if x.shape[1] % 2:
+        raise ValueError(f"rows of {x.shape[1]} are not gates and ups")
+    return x.shape[1] // 2
+
+
 def swiglu_fp8(x: torch.Tensor, handle: Handle, round_scale: bool = False,
                use_ue8m0: bool = False):
     """silu(gate) * up of the receive rows x [rows, 2I] bf16, cast to FP8:
     (codes [rows, I], row-major scales [rows, I/128] float32, or [rows, I/512]
     int32 with use_ue8m0), as ``expert_gemm`` takes them."""
     x = x.reshape(-1, x.shape[-1]).contiguous()
-    I = x.shape[1] // 2
+    I = _half(x)
     rows = handle.recv_rows
     flags = ((capi.MOE_FP8_ROUND_SCALE if round_scale or use_ue8m0 else 0)
              | (capi.MOE_FP8_UE8M0 if use_ue8m0 else 0))
@@ -413,7 +430,9 @@ def swiglu_grad(x: torch.Tensor, d_h: torch.Tensor, handle: Handle) -> torch.Ten
     """Gradient of the activation: d_x [rows, 2I] bf16 from x [rows, 2I] and
     d_h [rows, I]; rows of no expert are not written."""
     x = x.reshape(-1, x.shape[-1]).contiguous()
-    I = x.shape[1] // 2
+    I = _half(x)
+    if d_h.shape[-1] != I:
+        raise ValueError(f"d_h has rows of {d_h.shape[-1]}, not {I}")
     d_x = torch.empty_like(x)
     lay = handle.layout
     capi.moe_swiglu_grad(handle.shape.E, I, handle.recv_rows, x,

@@ -162,3 +162,37 @@ def test_binding_refusals(lib):
 
     with pytest.raises(ValueError, match="score"):
         ep.gate(x, 2, score="tanh")
+
+
+def test_wrapper_refusals(lib):
+    """Shapes that do not belong together, which the element counts alone would
+    let through: fewer experts, narrower rows, fewer tokens, transposed scales."""
+    from combine_moe_layout_03_amd import ep
+
+    shape = lib.make_shape(6, 256, 8, 2, 2, 1)
+    h = ep.Handle(shape, lib.LayoutBuffers.empty(shape, "cpu"), 12)
+    q, sc = torch.zeros(12, 256, dtype=torch.float8_e4m3fn), torch.ones(12, 2)
+
+    def gemm(E=8, C=256, blocks=(3, 2)):
+        return ep.expert_gemm((q, sc), (torch.zeros(E, 384, C, dtype=torch.float8_e4m3fn),
+                                        torch.ones(E, *blocks)), h)
+
+    with pytest.raises(ValueError, match="GPU tensor"):  # as it should be, but for the device
+        gemm()
+    with pytest.raises(ValueError, match="for 8 experts"):
+        gemm(E=4)
+    with pytest.raises(ValueError, match="rows of 256"):
+        gemm(C=128, blocks=(3, 1))
+    with pytest.raises(ValueError, match="scales"):
+        gemm(blocks=(2, 3))
+    x = torch.zeros(12, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="not gates and ups"):
+        ep.swiglu_fp8(x[:, :255], h)
+    with pytest.raises(ValueError, match="rows of 64"):
+        ep.swiglu_grad(x, x[:, :64], h)
+    with pytest.raises(ValueError, match="for 6 tokens"):
+        ep.combine_grad(x[:4], x, h)
+    with pytest.raises(ValueError, match="expert rows of 128"):
+        ep.combine_grad(x[:6], x[:, :128], h)
+    with pytest.raises(ValueError, match="for 6 tokens"):
+        ep.gate_grad(torch.zeros(6, 8), torch.zeros(6, 2, dtype=torch.int64), torch.zeros(6, 3))

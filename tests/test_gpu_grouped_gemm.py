@@ -119,6 +119,28 @@ def test_column_scales(capi, counts, N, C, flags):
     c.check(c.run(capi))
 
 
+@pytest.mark.parametrize("flags", [ROWS, ROWS | ROUND | WORDS])
+def test_scales_at_any_word(capi, flags):
+    """Row-major scales that start on a word, not on 16 bytes, and 16-byte
+    aligned operands that start inside their allocation."""
+    c = Case(71, [9, 40, 0, 130], 200, 1024, flags)
+    want = c.run(capi)
+    c.check(want)
+
+    def moved(x, n):  # the same values n elements into a larger buffer
+        t = to_dev(x).reshape(-1)
+        buf = torch.zeros(t.numel() + n, dtype=t.dtype, device=dev())
+        buf[n:] = t
+        return buf[n:]
+
+    out = torch.full((c.rows, c.N), SENTINEL, dtype=torch.int16, device=dev())
+    capi.moe_grouped_gemm_fp8(
+        c.E, c.N, c.C, moved(c.a, 16), moved(c.scale, 1), c.rows, moved(c.start, 1),
+        moved(np.array(c.counts, np.int32), 3), moved(c.w, 48), moved(c.ws, 1), out, c.flags)
+    torch.cuda.synchronize()
+    assert np.array_equal(out.cpu().numpy().view(np.uint16), want)
+
+
 @pytest.mark.parametrize("c", [1, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 79, 80, 96, 97,
                                112, 113, 127, 128, 129, 143, 144, 159, 160, 161, 255, 256, 257,
                                511, 513])
