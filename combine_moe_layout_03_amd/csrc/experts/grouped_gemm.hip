@@ -88,6 +88,12 @@ __device__ __forceinline__ float byte_scale(uint32_t word, int e) {
 // third group, also of the next unit, are in flight while the first is
 // multiplied. With fewer units than half the waves on the chip the eight waves
 // of a workgroup share a unit's groups out instead and join their sums in LDS.
+//
+// Bound by the weights' bytes, which every unit reads once. 16 tokens x 8 of 256
+// experts, 7168 channels to 4096: 451 us for 2996 MB (6.6 TB/s; a copy, half
+// reads and half writes, reaches 6.1); 128 tokens x 8, 2048 to 7168: 583 us
+// for 3711 MB (6.4 TB/s). The weights' copies marked to leave L2 first took these
+// from 506 and 670 us. A token alone (8 experts, 7168 to 4096): 47 us, 5.0 TB/s.
 
 constexpr int kStreamTokens = 16;  // most token rows of a unit
 constexpr int kStreamN = 32;       // weight rows of a unit
@@ -266,6 +272,24 @@ __global__ __launch_bounds__(kStreamThreads, 2) void grouped_gemm_stream_kernel(
 }
 
 // ---- tiles: segments of many rows -------------------------------------------
+//
+// A tile is 192 weight rows x up to 288 token rows: its float sums (3 x 9 of
+// 16 x 16 per wave) and operands fill 256 registers, its buffers LDS. The larger
+// the tile, the fewer bytes a product copies; 288 rows also take an expert of
+// average size of 8192 tokens x 8 over 256 experts in one piece, so that its
+// weights are read once (counted there, 7168 channels to 4096: 8.6 GB read, 8.0 at
+// least).
+// What bounds it (that product: 2420 us, 1590 TFLOP/s): the copies without the
+// products take 2230 us, the products without the copies 1670, all without memory
+// (rows and weights from L2) 1965. The matrix units are busy 45% of the clocks, at
+// 1.7 to 2.1 GHz: under this load the GPU's power holds the clock down, so that the
+// products cost as much as the overlap would win. The skewed batch (4096 tokens
+// x 6 over 64 experts, 4096 to 2824): 400 us, 1420 TFLOP/s, from pieces of 32 rows'
+// steps and a last round of tiles that does not fill the chip.
+// Tried and slower: 256 weight rows with two buffers (2884 us with the copies
+// of that time); weights copied by four waves and rows by the others (+9%); the
+// weights' buffer given back at a barrier of its own (+14%); the next tile's
+// lines fetched into L2 ahead (+35%); raised priority around the products (+3%).
 
 constexpr int kTileWaves = 8;      // 4 along the weight rows x 2 along the token rows
 constexpr int kTileThreads = kTileWaves * 64;

@@ -8,6 +8,15 @@
 // channels of h: a lane reads 8 gates and 8 ups (16 bytes each), and the 128
 // channels of a scale are one 16-lane DPP row, as in the dispatch's cast. h
 // stays in float up to the E4M3 code.
+//
+// Bound by bytes: 65536 rows of 2 x 2048, the cast 675 MB and the gradient 1342 MB,
+// together 381 us (5.3 TB/s; a large copy reaches 6.1). The cast was bound by
+// instructions (268 per unit of 512 channels) until the walk's addresses were
+// left to the scalar unit and the sigmoid and the codes' quotient were cut to what
+// their error allows (162 now). Rows in runs, because a wave then looks a segment
+// up only when it leaves one: units strided over the whole grid take 394 us;
+// twice or half the grid, or two units' registers in turn, change nothing; loads
+// or stores not marked nontemporal cost 3%.
 #include "segments.hpp"
 
 namespace moe {
@@ -19,20 +28,22 @@ __device__ __forceinline__ float keep_finite(float h) {
   return __builtin_amdgcn_fmed3f(h, -3.402823466e38f, 3.402823466e38f);
 }
 
-// 1 / (1 + exp(-x)) within six half float steps for |x| <= 87 (one step each for
-// the exponential and the reciprocal, half for the sum and the correction);
-// beyond, 0 or 1. The exponent x log2(e) is carried in two floats: rounded
-// to one, its error would grow to 2^-24 |x| of the result. About 10 instructions
-// against 25 for exp and a correctly rounded quotient.
+// 1 / (1 + exp(-x)) of a bf16 value within six half float steps for |x| <= 87
+// (one step each for the exponential and the reciprocal, half for the sum and the
+// correction); beyond, 0 or 1. 2^t with t = -x log2(e) rounded to one float would
+// be off by 2^-24 |x|: what t ln2 differs from -x (ln2 in two floats; exact to
+// 2^-40) is added back. At the bound -89 the power is infinite and the correction
+// positive, so the result is 0; a bf16 value inside has a finite power.
 __device__ __forceinline__ float sigmoid_of(float x) {
-#pragma clang fp contract(off)
-  constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147181f;
-  const float t = __builtin_amdgcn_fmed3f(x * -kLog2e, -128.0f, 128.0f);
-  const float low = __builtin_fmaf(x, -kLog2e, -t) - x * kLog2eLow;  // of the exact product
+  constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147182f, kLn2Low = -1.90465430e-9f;
+  x = __builtin_amdgcn_fmed3f(x, -89.0f, 89.0f);
+  const float t = x * -kLog2e;
+  const float d = __builtin_fmaf(-t, kLn2Low, __builtin_fmaf(-t, kLn2, -x));
   const float e0 = __builtin_amdgcn_exp2f(t);
-  const float e = fabsf(t) < 128.0f ? __builtin_fmaf(e0, low * kLn2, e0) : e0;
-  return __builtin_amdgcn_rcpf(1.0f + e);
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e0, d, e0));
 }
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // The rows of all segments, cut evenly into one run per workgroup; its waves
 // take the run's (row, 512-channel chunk) units in turn. A run's rows ascend,
@@ -42,7 +53,7 @@ struct RowWalk {
   int64_t start;
   __device__ __forceinline__ void at(const SegmentPlanRows &p, int i) {
     if (i < hi) return;
-    while (i >= p.first[e + 1]) ++e;
+    while (i >= uniform(p.first[e + 1])) ++e;
     set(p);
   }
   __device__ __forceinline__ void find(const SegmentPlanRows &p, int E, int i) {
@@ -50,10 +61,10 @@ struct RowWalk {
     set(p);
   }
   __device__ __forceinline__ void set(const SegmentPlanRows &p) {
-    e = __builtin_amdgcn_readfirstlane(e);
-    lo = __builtin_amdgcn_readfirstlane(p.first[e]);
-    hi = __builtin_amdgcn_readfirstlane(p.first[e + 1]);
-    start = __builtin_amdgcn_readfirstlane(p.start[e]);
+    e = uniform(e);
+    lo = uniform(p.first[e]);
+    hi = uniform(p.first[e + 1]);
+    start = uniform(p.start[e]);
   }
   __device__ __forceinline__ int64_t row(int i) const { return start + (i - lo); }
 };
@@ -63,11 +74,15 @@ struct RowWalk {
 template <class Load, class Body>
 __device__ __forceinline__ void for_rows(const Segments &seg, const SegmentPlanRows &plan,
                                          int total, int nchunk, Load load, Body body) {
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  // All of the walk is the same in every lane. Divisions are done in vector
+  // registers: read back, they leave it and every address it makes to the scalar
+  // unit.
+  const int wave = uniform(threadIdx.x >> 6);
   constexpr int kWaves = kSwThreads / 64;
-  const int r0 = (int)((int64_t)total * blockIdx.x / gridDim.x);
-  const int r1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
-  int i = r0 + wave / nchunk, c = wave - wave / nchunk * nchunk;  // unit: row i, chunk c
+  const int r0 = uniform((int64_t)total * blockIdx.x / gridDim.x);
+  const int r1 = uniform((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+  const int skip = uniform(wave / nchunk);
+  int i = r0 + skip, c = wave - skip * nchunk;  // unit: row i, chunk c
   if (i >= r1) return;
   RowWalk walk;
   walk.find(plan, seg.E, i);
@@ -106,11 +121,11 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
     float *__restrict__ fscale, uint32_t *__restrict__ wscale, int32_t I, int32_t nchunk,
     int32_t *status) {
   __shared__ SegmentPlanRows plan;
-  const int total = plan_segments(seg, 1, plan, status);
+  const int total = uniform(plan_segments(seg, 1, plan, status));
   const int lane = threadIdx.x & 63;
   const int nv = I / 8;  // 16-byte vectors of gates in a row
   auto load = [&](int64_t row, int c) {
-    const int v = min(c * 64 + lane, nv - 1);
+    const uint32_t v = (uint32_t)min(c * 64 + lane, nv - 1);
     const ex_u32x4 *xr = x + row * 2 * nv;
     return GateUp{__builtin_nontemporal_load(xr + v), __builtin_nontemporal_load(xr + nv + v)};
   };
@@ -129,17 +144,22 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
     for (int d = 0; d < 8; ++d) am = fmaxf(am, fabsf(h[d]));
     am = __uint_as_float(row16_max(__float_as_uint(am)));
     if (am < 1e-4f) am = 1e-4f;
-    float s = am / 448.0f;
+    // am / 448, correctly rounded (product, remainder, correction)
+    const float s0 = am * (1.0f / 448.0f);
+    float s = __builtin_fmaf(__builtin_fmaf(-448.0f, s0, am), 1.0f / 448.0f, s0);
     if (kFlags & kFp8RoundScale) {
       uint32_t b = __float_as_uint(s);
       if (b & 0x7fffffu) b = (b & 0xff800000u) + 0x800000u;
       s = __uint_as_float(b);
     }
-    const float y = 1.0f / s;
+    // The codes are those of h * (1 / s), within two half float steps of h / s
+    // (one for a power of two); the cast of bf16 rows divides exactly, but h
+    // itself is only good to eight. None passes 448 by more than those steps,
+    // which round to 448.
+    const float r = __builtin_amdgcn_rcpf(s), y = __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
     float d8[8];
 #pragma unroll
-    for (int d = 0; d < 8; ++d)
-      d8[d] = __builtin_amdgcn_fmed3f(div_by_scale(h[d], s, y), -448.0f, 448.0f);
+    for (int d = 0; d < 8; ++d) d8[d] = h[d] * y;
     if (ok)
       __builtin_nontemporal_store(ex_u32x2{e4m3x4(d8[0], d8[1], d8[2], d8[3]),
                                            e4m3x4(d8[4], d8[5], d8[6], d8[7])},
@@ -161,12 +181,12 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_grad_kernel(
     Segments seg, const ex_u32x4 *x, const ex_u32x4 *__restrict__ dh, ex_u32x4 *dx, int32_t nv,
     int32_t nchunk, int32_t *status) {
   __shared__ SegmentPlanRows plan;
-  const int total = plan_segments(seg, 1, plan, status);
+  const int total = uniform(plan_segments(seg, 1, plan, status));
   const int lane = threadIdx.x & 63;
   // (x may be dx: a unit's vectors are read before they are written, and by no
   // other wave)
   auto load = [&](int64_t row, int c) {
-    const int v = min(c * 64 + lane, nv - 1);
+    const uint32_t v = (uint32_t)min(c * 64 + lane, nv - 1);
     const ex_u32x4 *xr = x + row * 2 * nv;
     return GateUpGrad{__builtin_nontemporal_load(xr + v), __builtin_nontemporal_load(xr + nv + v),
                       __builtin_nontemporal_load(dh + row * nv + v)};
