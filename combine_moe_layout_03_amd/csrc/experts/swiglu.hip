@@ -15,8 +15,8 @@
 // left to the scalar unit and the sigmoid and the codes' quotient were cut to what
 // their error allows (162 now). Rows in runs, because a wave then looks a segment
 // up only when it leaves one: units strided over the whole grid take 394 us;
-// twice or half the grid, or two units' registers in turn, change nothing; loads
-// or stores not marked nontemporal cost 3%.
+// twice the grid, or two units' registers in turn, change nothing, half the grid
+// costs 2%, loads or stores not marked nontemporal 3%.
 #include "segments.hpp"
 
 namespace moe {
