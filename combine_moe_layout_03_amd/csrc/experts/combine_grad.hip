@@ -30,10 +30,9 @@ __global__ __launch_bounds__(kCgThreads) void combine_grad_kernel(
     int32_t *status) {
   __shared__ float part[kCgThreads / 64];
   // pair of this workgroup: tokens in groups of 8, the group's token fastest
-  const int64_t b = blockIdx.x;
-  const int64_t grp = b / (8 * K);
-  const int r = (int)(b - grp * 8 * K);
-  const int64_t t = grp * 8 + (r & 7);
+  const uint32_t b = blockIdx.x, grp = b / (8u * K);
+  const int r = (int)(b - grp * 8u * K);
+  const int64_t t = (int64_t)grp * 8 + (r & 7);
   const int k = r >> 3;
   if (t >= T) return;
   const int64_t pair = t * K + k;

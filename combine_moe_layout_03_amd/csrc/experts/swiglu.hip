@@ -79,8 +79,9 @@ __device__ __forceinline__ void for_rows(const Segments &seg, const SegmentPlanR
   // unit.
   const int wave = uniform(threadIdx.x >> 6);
   constexpr int kWaves = kSwThreads / 64;
-  const int r0 = uniform((int64_t)total * blockIdx.x / gridDim.x);
-  const int r1 = uniform((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+  const int each = uniform((uint32_t)total / gridDim.x), rest = total - each * (int)gridDim.x;
+  const int r0 = uniform(each * (int)blockIdx.x + min((int)blockIdx.x, rest));
+  const int r1 = uniform(r0 + each + ((int)blockIdx.x < rest ? 1 : 0));
   const int skip = uniform(wave / nchunk);
   int i = r0 + skip, c = wave - skip * nchunk;  // unit: row i, chunk c
   if (i >= r1) return;

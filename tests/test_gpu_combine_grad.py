@@ -185,3 +185,33 @@ def test_on_another_stream_and_repeat(capi, orc):
         st.synchronize()
         got.append((dy, dw))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_offsets_past_32_bits(capi):
+    """Expert rows of more than 2^32 elements, slots at both ends and between."""
+    T, H, E, R, K, rows = 3, 8192, 8, 2, 2, (1 << 19) + 5
+    shape = capi.make_shape(T, H, E, R, K, 1)
+    slot = torch.tensor([0, rows - 1, (1 << 18) + 1, rows - 3, -1, 7], dtype=torch.int32,
+                        device=dev())
+    g = torch.Generator(device="cuda").manual_seed(3)
+    y = torch.zeros(rows, H, dtype=torch.bfloat16, device=dev())
+    live = slot[slot >= 0].long()
+    y[live] = torch.randn(5, H, generator=g, device=dev()).to(torch.bfloat16)
+    d_out = torch.randn(T, H, generator=g, device=dev()).to(torch.bfloat16)
+    w = torch.rand(T, K, generator=g, device=dev())
+    d_y = torch.zeros(rows, H, dtype=torch.bfloat16, device=dev())
+    d_w = torch.zeros(T, K, device=dev())
+    capi.moe_combine_grad(shape, d_out, y, rows, slot, w, d_y, d_w)
+    torch.cuda.synchronize()
+    for p in range(T * K):
+        t, k, s = p // K, p % K, int(slot[p])
+        if s < 0:
+            assert float(d_w[t, k]) == 0
+            continue
+        assert torch.equal(d_y[s], (w[t, k] * d_out[t].float()).to(torch.bfloat16))
+        prod = d_out[t].double() * y[s].double()
+        # H products added in float: half a step of the running sum each
+        tol = H * 2.0 ** -24 * float(prod.abs().sum())
+        assert abs(float(d_w[t, k]) - float(prod.sum())) <= tol
+    d_y[live] = 0
+    assert all(not bool(c.any()) for c in d_y.split(1 << 16))

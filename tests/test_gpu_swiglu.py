@@ -175,3 +175,34 @@ def test_bad_segments(capi):
     q, sc = fp8(capi, [0, -3, 2], np.array([-9, 99, 1], np.int32), rows, x, I, 0, st)
     assert int(st.item()) == 0  # empty segments may point anywhere
     check_fp8(np.arange(1, 3), x, q, sc, I, 0)
+
+
+def test_offsets_past_32_bits(capi):
+    """A buffer of more than 2^32 elements, segments at both ends: the same rows
+    as in a small buffer, bit for bit."""
+    I, rows, counts = 2048, (1 << 20) + 40, [3, 37]
+    start = np.array([1, rows - 38], np.int32)
+    small = np.array([0, 3], np.int32)
+    rng = np.random.default_rng(8)
+    part = to_dev(mi.to_bf16_bits(rng.standard_normal((40, 2 * I)).astype(np.float32)))
+    dpart = to_dev(mi.to_bf16_bits(rng.standard_normal((40, I)).astype(np.float32)))
+    far = torch.cat([torch.arange(1, 4), torch.arange(rows - 38, rows - 1)]).to(dev())
+    cnt = to_dev(np.array(counts, np.int32))
+    got = []
+    for n, st, at in ((40, small, torch.arange(40, device=dev())), (rows, start, far)):
+        x = torch.zeros(n, 2 * I, dtype=torch.int16, device=dev())
+        dh = torch.zeros(n, I, dtype=torch.int16, device=dev())
+        x[at], dh[at] = part.view(torch.int16), dpart.view(torch.int16)
+        q = torch.zeros(n, I, dtype=torch.uint8, device=dev())
+        sc = torch.zeros(n, I // 128, device=dev())
+        dx = torch.zeros(n, 2 * I, dtype=torch.int16, device=dev())
+        capi.moe_swiglu_fp8(2, I, n, x, to_dev(st), cnt, q, sc)
+        capi.moe_swiglu_grad(2, I, n, x, dh, to_dev(st), cnt, dx)
+        torch.cuda.synchronize()
+        got.append((q[at].clone(), sc[at].clone(), dx[at].clone()))
+        if n == rows:  # nothing else was written
+            for t in (q, sc, dx):
+                t[at] = 0
+                assert all(not bool(c.any()) for c in t.split(1 << 18))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
