@@ -128,17 +128,18 @@ __global__ __launch_bounds__(kStreamThreads, 2) void grouped_gemm_stream_kernel(
   const int l16 = lane & 15, quad = lane >> 4;
   const int C = ga.C, G = C / kFp8Group, SG = kWords ? G / 4 : G;  // scale entries of a row
   const int nblk = (ga.N + kStreamN - 1) / kStreamN;
-  const int64_t units = (int64_t)pieces * nblk;
+  // (at most a piece per expert and 2^15 blocks: 32 bits, also with a step on top)
+  const uint32_t units = (uint32_t)pieces * nblk;
   if (units == 0) return;
-  const bool split = units * 2 <= (int64_t)gridDim.x * kStreamWaves;  // uniform
-  const int64_t u_first = split ? blockIdx.x : (int64_t)blockIdx.x * kStreamWaves + wave;
-  const int64_t u_step = split ? gridDim.x : (int64_t)gridDim.x * kStreamWaves;
+  const bool split = units * 2 <= gridDim.x * kStreamWaves;  // uniform
+  const uint32_t u_first = split ? blockIdx.x : blockIdx.x * kStreamWaves + wave;
+  const uint32_t u_step = split ? gridDim.x : gridDim.x * kStreamWaves;
   const int g_first = split ? wave : 0, g_step = split ? kStreamWaves : 1;
 
-  auto unit = [&](int64_t u) {  // one piece per segment: its blocks of weight rows in turn
+  auto unit = [&](uint32_t u) {  // one piece per segment: its blocks of weight rows in turn
     StreamUnit x;
     x.e = scalar(plan_find(sh.plan, seg.E, (int)(u / nblk)));
-    x.n0 = scalar((int)(u - (int64_t)scalar(sh.plan.first[x.e]) * nblk)) * kStreamN;
+    x.n0 = scalar((int)(u - (uint32_t)scalar(sh.plan.first[x.e]) * nblk)) * kStreamN;
     // (from LDS: a load from memory here would wait for every copy in flight)
     x.tokens = scalar(sh.plan.rows[x.e]);
     x.row0 = scalar(sh.plan.start[x.e]);
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void grouped_gemm_stream_kernel(
   uint32_t wo[kStreamN / 8], to[kStreamTokens / 8];
   const uint32_t *sp = nullptr;  // the lane's scale
   int64_t s_step = 0;            // to the next group's (words: next four groups')
-  auto open = [&](int64_t u) {
+  auto open = [&](uint32_t u) {
     const StreamUnit x = unit(u);
     wbase = scalar(ga.w + ((int64_t)x.e * ga.N + x.n0) * C);
     tbase = scalar(ga.a + x.row0 * C);
@@ -201,7 +202,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void grouped_gemm_stream_kernel(
     }
   };
 
-  int64_t u_copy = u_first;  // next to copy: group g_copy of unit u_copy
+  uint32_t u_copy = u_first;  // next to copy: group g_copy of unit u_copy
   int g_copy = g_first, slot_copy = 0, ahead = 0;
   auto advance = [&]() {  // copies the next group, if there is one
     if (u_copy >= units) return;
@@ -216,7 +217,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void grouped_gemm_stream_kernel(
     }
   };
   int slot = 0;
-  for (int64_t u = u_first; u < units; u += u_step) {
+  for (uint32_t u = u_first; u < units; u += u_step) {
     acc[0] = acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (u == u_first || split) {
       open(u);
@@ -514,14 +515,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void grouped_gemm_tile_kernel(Segm
   // neighbouring tiles, which share weights and token rows in its L2; the rounds
   // go through the experts together, so that one with many rows does not stay
   // with one XCD.
-  const int64_t tiles = (int64_t)pieces * nblk;
-  const int lanes = gridDim.x >> 3;
-  for (int64_t u = (int64_t)(blockIdx.x & 7) * lanes + (blockIdx.x >> 3); u < tiles; u += gridDim.x) {
+  // (32 bits: more tiles than that would have results past any memory)
+  const uint32_t tiles = (uint32_t)pieces * nblk;
+  const uint32_t lanes = gridDim.x >> 3;
+  for (uint32_t u = (blockIdx.x & 7) * lanes + (blockIdx.x >> 3); u < tiles; u += gridDim.x) {
     TilePos p;
     // wave-uniform values, kept in scalar registers
     p.e = scalar(plan_find(plan, seg.E, (int)(u / nblk)));
     const int first = scalar(plan.first[p.e]), np = scalar(plan.first[p.e + 1]) - first;
-    const int r = scalar((int)(u - (int64_t)first * nblk));
+    const int r = scalar((int)(u - (uint32_t)first * nblk));
     const int nb = scalar(r / np), piece = r - nb * np;
     const int count = scalar(seg.count[p.e]);
     const int per = scalar(((count + np - 1) / np + 31) & ~31);  // the pieces are even
