@@ -93,7 +93,7 @@ __device__ __forceinline__ float byte_scale(uint32_t word, int e) {
 // experts, 7168 channels to 4096: 451 us for 2996 MB (6.6 TB/s; a copy, half
 // reads and half writes, reaches 6.1); 128 tokens x 8, 2048 to 7168: 583 us
 // for 3711 MB (6.4 TB/s). The weights' copies marked to leave L2 first took these
-// from 506 and 670 us. A token alone (8 experts, 7168 to 4096): 47 us, 5.0 TB/s.
+// from 506 and 670 us. A token alone (8 experts, 7168 to 4096): 43 us, 5.5 TB/s.
 
 constexpr int kStreamTokens = 16;  // most token rows of a unit
 constexpr int kStreamN = 32;       // weight rows of a unit
