@@ -205,7 +205,11 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_grad_kernel(
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float s = sigmoid_of(a[k]);
-        p[k] = e[k] * b[k] * (s * (1.0f + a[k] * (1.0f - s)));
+        // the larger factor first: d_h * u can pass the float range, and u times a
+        // small slope fall below it, where the product of the three does not
+        const bool up = fabsf(b[k]) > fabsf(e[k]);
+        const float big = up ? b[k] : e[k], small = up ? e[k] : b[k];
+        p[k] = small * (big * (s * (1.0f + a[k] * (1.0f - s))));
         r[k] = e[k] * (a[k] * s);
       }
       dg[j] = ex_bf16x2(p[0], p[1]);

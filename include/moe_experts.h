@@ -116,7 +116,8 @@ int moe_combine_grad(const moe_shape *shape, const uint16_t *d_out, const uint16
  *   M), 0 if unknown. It lets a small batch run as one launch; a segment with
  *   more rows is skipped and sets MOE_STATUS_BAD_SLOT.
  * C % 128 == 0 (512 with UE8M0), N % 8 == 0, 8 <= N, C <= 2^20, E <= 1024.
- * a, w and out 16-byte aligned, scales 4-byte aligned. The gradient with
+ * a, w and out 16-byte aligned, scales 4-byte aligned. A row's scale times a
+ * block's must be a finite float (the two are multiplied first). The gradient with
  * respect to the rows is the same call on weights stored transposed (the
  * blocks of w_scale transpose with them). */
 int moe_grouped_gemm_fp8(int32_t E, int32_t N, int32_t C, const uint8_t *a, const void *a_scale,

@@ -160,6 +160,29 @@ def test_swiglu_grad(capi, counts, I):
     assert np.array_equal(xin.cpu().numpy().view(np.uint16)[live], got[live])
 
 
+def test_gradient_of_large_factors(capi):
+    """d_h * u past the float range where the sigmoid brings the product back, or
+    to zero: the gradient is the formula's, not an infinity or NaN."""
+    I = 64
+    g = np.zeros((4, I), np.float32)
+    g[0], g[1], g[2] = -1e30, np.linspace(-80, -30, I), -3.3e38
+    g[3] = np.linspace(-85, 85, I)
+    u = np.full((4, I), 3e38, np.float32)
+    d = np.full((4, I), -10.0, np.float32)
+    d[3] = 1e-3
+    x, dh = mi.to_bf16_bits(np.concatenate([g, u], 1)), mi.to_bf16_bits(d)
+    dx = torch.zeros(4, 2 * I, dtype=torch.int16, device=dev())
+    capi.moe_swiglu_grad(1, I, 4, to_dev(x), to_dev(dh), to_dev(np.array([0], np.int32)),
+                         to_dev(np.array([4], np.int32)), dx)
+    torch.cuda.synchronize()
+    have = mi.bf16_bits_to_f32(dx.cpu().numpy().view(np.uint16)).astype(np.float64)
+    gg, uu, s, _ = ref.silu_mul(mi.bf16_bits_to_f32(x))
+    dd = mi.bf16_bits_to_f32(dh).astype(np.float64)
+    want = np.concatenate([dd * uu * s * (1 + gg * (1 - s)), dd * gg * s], 1)
+    assert np.isfinite(want).all() and np.isfinite(have).all()
+    assert np.all(np.abs(have - want) <= grad_tol(gg, uu, s, dd, want))
+
+
 def test_bad_segments(capi):
     """Segments outside the buffer are skipped and reported, the others done."""
     I, rows = 128, 32
