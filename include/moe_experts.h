@@ -141,8 +141,8 @@ int moe_swiglu_fp8(int32_t E, int32_t I, int64_t rows, const uint16_t *x,
  * row of a segment, with s = 1 / (1 + exp(-g)),
  *   d_x[r][0..I)  = bf16_rne( d_h * u * s * (1 + g * (1 - s)) )
  *   d_x[r][I..2I) = bf16_rne( d_h * g * s )
- * x [rows*2I], d_h [rows*I], d_x [rows*2I] bf16, 16-byte aligned; d_x may be x
- * itself. I % 8 == 0, I <= 2^20. */
+ * x [rows*2I], d_h [rows*I] (both finite), d_x [rows*2I] bf16, 16-byte aligned;
+ * d_x may be x itself. I % 8 == 0, I <= 2^20. */
 int moe_swiglu_grad(int32_t E, int32_t I, int64_t rows, const uint16_t *x, const uint16_t *d_h,
                     const int32_t *row_start, const int32_t *count, uint16_t *d_x,
                     int32_t *status, hipStream_t stream);
