@@ -205,11 +205,13 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_grad_kernel(
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float s = sigmoid_of(a[k]);
-        // the larger factor first: d_h * u can pass the float range, and u times a
-        // small slope fall below it, where the product of the three does not
+        // The larger factor first: d_h * u can pass the float range, and u times a
+        // small slope fall below it, where the product of the three does not. The
+        // slope is at most 1.1, so half of it keeps the first product in range
+        // too; a power of two, it changes no rounding.
         const bool up = fabsf(b[k]) > fabsf(e[k]);
         const float big = up ? b[k] : e[k], small = up ? e[k] : b[k];
-        p[k] = small * (big * (s * (1.0f + a[k] * (1.0f - s))));
+        p[k] = 2.0f * (small * (big * (0.5f * s * (1.0f + a[k] * (1.0f - s)))));
         r[k] = e[k] * (a[k] * s);
       }
       dg[j] = ex_bf16x2(p[0], p[1]);

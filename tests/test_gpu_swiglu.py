@@ -229,3 +229,35 @@ def test_offsets_past_32_bits(capi):
                 assert all(not bool(c.any()) for c in t.split(1 << 18))
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_gradient_of_a_steep_gate(capi):
+    """The gate's slope s (1 + g (1 - s)) passes 1 between g = 0 and its tail: a
+    factor near the largest bf16 times it leaves the float range where the other
+    factor, being small, brings the product back."""
+    I = 64
+    slopes = np.linspace(0.01, 12.0, I)
+    g = np.tile(slopes, (4, 1)).astype(np.float32)
+    u, d = np.empty((4, I), np.float32), np.empty((4, I), np.float32)
+    u[0], d[0] = 1e-10, 3.38e38
+    u[1], d[1] = 3.38e38, -1e-10
+    u[2], d[2] = -0.75, 3.38e38   # the product itself in the top binade
+    u[3], d[3] = 1e-30, 1e-8      # and far below
+    x, dh = mi.to_bf16_bits(np.concatenate([g, u], 1)), mi.to_bf16_bits(d)
+    dx = torch.zeros(4, 2 * I, dtype=torch.int16, device=dev())
+    capi.moe_swiglu_grad(1, I, 4, to_dev(x), to_dev(dh), to_dev(np.array([0], np.int32)),
+                         to_dev(np.array([4], np.int32)), dx)
+    torch.cuda.synchronize()
+    have = mi.bf16_bits_to_f32(dx.cpu().numpy().view(np.uint16)).astype(np.float64)
+    gg, uu, s, _ = ref.silu_mul(mi.bf16_bits_to_f32(x))
+    dd = mi.bf16_bits_to_f32(dh).astype(np.float64)
+    want = np.concatenate([dd * uu * s * (1 + gg * (1 - s)), dd * gg * s], 1)
+    # the largest bf16 is (2 - 2^-7) 2^127; from half a step above, a value rounds
+    # to infinity
+    top, edge = (2 - 2.0 ** -7) * 2.0 ** 127, (2 - 2.0 ** -8) * 2.0 ** 127
+    tol = grad_tol(gg, uu, s, dd, want)
+    fits = np.abs(want) + tol < top
+    assert fits[:, :I].all() and fits[1].all() and fits[3].all()
+    assert np.all(np.abs(have - want)[fits] <= tol[fits])
+    past = np.abs(want) - tol > edge
+    assert np.all(have[past] == np.copysign(np.inf, want[past]))
