@@ -25,9 +25,19 @@ namespace moe {
 namespace {
 
 constexpr int kSwThreads = kPlanThreads;
+constexpr uint32_t kInfBits = 0x7f800000u, kNanBits = 0x7fc00000u;
 
 __device__ __forceinline__ float keep_finite(float h) {
   return __builtin_amdgcn_fmed3f(h, -3.402823466e38f, 3.402823466e38f);
+}
+
+// Whether one of a vector's eight bf16 values is infinite or NaN.
+__device__ __forceinline__ bool any_not_finite(ex_u32x4 v) {
+  bool r = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    r = r || (v[j] & 0x7f80u) == 0x7f80u || (v[j] & 0x7f800000u) == 0x7f800000u;
+  return r;
 }
 
 // 1 / (1 + exp(-x)) of a bf16 value within six half float steps for |x| <= 87
@@ -139,13 +149,31 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       const float a = ex_lo(in.g[d]), b = ex_hi(in.g[d]);
-      h[2 * d] = keep_finite(a * sigmoid_of(a) * ex_lo(in.u[d]));
-      h[2 * d + 1] = keep_finite(b * sigmoid_of(b) * ex_hi(in.u[d]));
+      h[2 * d] = a * sigmoid_of(a) * ex_lo(in.u[d]);
+      h[2 * d + 1] = b * sigmoid_of(b) * ex_hi(in.u[d]);
     }
-    float am = 0.0f;
+    // |h| as bit patterns, whose integer order puts infinities and NaN on top: a
+    // gate or up that is not finite leaves an h that is not
+    uint32_t top = 0;
 #pragma unroll
-    for (int d = 0; d < 8; ++d) am = fmaxf(am, fabsf(h[d]));
-    am = __uint_as_float(row16_max(__float_as_uint(am)));
+    for (int d = 0; d < 8; ++d) top = umax32(top, __float_as_uint(h[d]) & 0x7fffffffu);
+    top = row16_max(top);
+    bool spoilt = false;
+    if (__ballot(top >= kInfBits)) {  // uniform, and rare
+      // A product of finite values past the float range is kept at the largest
+      // float; a group with an input that is not finite gets the scale NaN and, by
+      // the quotients with it, NaN codes.
+      const bool mine = any_not_finite(in.g) || any_not_finite(in.u);
+      top = mine ? kInfBits : 0u;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        h[d] = keep_finite(h[d]);
+        top = umax32(top, __float_as_uint(h[d]) & 0x7fffffffu);
+      }
+      top = row16_max(top);
+      spoilt = top >= kInfBits;
+    }
+    float am = __uint_as_float(top);
     if (am < 1e-4f) am = 1e-4f;
     // am / 448, correctly rounded (product, remainder, correction)
     const float s0 = am * (1.0f / 448.0f);
@@ -155,6 +183,7 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
       if (b & 0x7fffffu) b = (b & 0xff800000u) + 0x800000u;
       s = __uint_as_float(b);
     }
+    s = spoilt ? __uint_as_float(kNanBits) : s;
     // The codes are those of h * (1 / s), within two half float steps of h / s
     // (one for a power of two); the cast of bf16 rows divides exactly, but h
     // itself is only good to eight. None passes 448 by more than those steps,

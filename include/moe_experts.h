@@ -131,8 +131,10 @@ int moe_grouped_gemm_fp8(int32_t E, int32_t N, int32_t C, const uint8_t *a, cons
  * cast as moe_quantize_fp8 casts a row (flags as there; the code is that of
  * h * (1 / scale), within two half float steps of the quotient): q [rows*I] codes,
  * scale [rows][I/128] float or [rows][I/512] words, row-major. x [rows*2I]
- * bf16 must be finite. I % 128 == 0 (512 with MOE_FP8_UE8M0). x and q 16-byte
- * aligned, scale 4-byte. */
+ * bf16; a NaN or infinity in it gives its group of 128 channels the scale NaN
+ * (UE8M0: byte 255) and NaN codes, so that it shows in every result of its row's
+ * product, and touches no other group. I % 128 == 0 (512 with MOE_FP8_UE8M0). x
+ * and q 16-byte aligned, scale 4-byte. */
 int moe_swiglu_fp8(int32_t E, int32_t I, int64_t rows, const uint16_t *x,
                    const int32_t *row_start, const int32_t *count, uint8_t *q, void *scale,
                    int32_t flags, int32_t *status, hipStream_t stream);
@@ -141,8 +143,9 @@ int moe_swiglu_fp8(int32_t E, int32_t I, int64_t rows, const uint16_t *x,
  * row of a segment, with s = 1 / (1 + exp(-g)),
  *   d_x[r][0..I)  = bf16_rne( d_h * u * s * (1 + g * (1 - s)) )
  *   d_x[r][I..2I) = bf16_rne( d_h * g * s )
- * x [rows*2I], d_h [rows*I] (both finite), d_x [rows*2I] bf16, 16-byte aligned;
- * d_x may be x itself. I % 8 == 0, I <= 2^20. */
+ * x [rows*2I], d_h [rows*I], d_x [rows*2I] bf16, 16-byte aligned;
+ * d_x may be x itself. NaN and infinities go as the formulas take them, each to
+ * its own channel. I % 8 == 0, I <= 2^20. */
 int moe_swiglu_grad(int32_t E, int32_t I, int64_t rows, const uint16_t *x, const uint16_t *d_h,
                     const int32_t *row_start, const int32_t *count, uint16_t *d_x,
                     int32_t *status, hipStream_t stream);

@@ -240,3 +240,25 @@ def test_layer_in_a_graph(ep):
         torch.cuda.synchronize()
         for i, (a, b) in enumerate(zip(held, want)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (seed, i)
+
+
+@pytest.mark.parametrize("words", [False, True])
+@pytest.mark.parametrize("T", [6, 90])
+def test_a_diverged_row_stays_visible(ep, T, words):
+    """One NaN and one infinity behind the first product: the rows they are in
+    come out of the second as NaN throughout, all others as without them."""
+    H, E, R, K, I, M = 256, 4, 2, 2, 512, 96
+    rng = np.random.default_rng(T)
+    w2 = weights(rng, E, H, I)
+    idx = torch.from_numpy(mi._uniform_subsets(rng, T, E, K)).to(dev())
+    x = torch.randn(T, H, device=dev()).to(torch.bfloat16)
+    recv, _, h = ep.low_latency_dispatch(x, idx, M, E, R, 1)
+    y1 = torch.randn(h.recv_rows, 2 * I, device=dev()).to(torch.bfloat16)
+    slot = h.layout.slot.long()
+    bad = slot[torch.tensor([3, len(slot) - 2], device=dev())]
+    spoilt = y1.clone()
+    spoilt[bad[0], 77], spoilt[bad[1], I + 500] = float("nan"), float("inf")
+    out = [ep.expert_gemm(ep.swiglu_fp8(v, h, use_ue8m0=words), w2, h) for v in (y1, spoilt)]
+    assert bool(out[1][bad].isnan().all())
+    rest = slot[~torch.isin(slot, bad)]
+    assert torch.equal(out[0][rest], out[1][rest]) and bool(out[0][slot].isfinite().all())

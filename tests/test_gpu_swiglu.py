@@ -261,3 +261,78 @@ def test_gradient_of_a_steep_gate(capi):
     assert np.all(np.abs(have - want)[fits] <= tol[fits])
     past = np.abs(want) - tol > edge
     assert np.all(have[past] == np.copysign(np.inf, want[past]))
+
+
+@pytest.mark.parametrize("flags", [0, ROUND, ROUND | WORDS])
+def test_values_that_are_not_finite_stay_visible(capi, flags):
+    """A NaN or infinite gate or up gives its group of 128 channels the scale NaN
+    (UE8M0: the byte 255) and NaN codes; every other group is as without it."""
+    I, n = 1024, 9
+    rng = np.random.default_rng(31)
+    clean = mi.to_bf16_bits(rng.standard_normal((n, 2 * I)).astype(np.float32))
+    x = clean.copy()
+    nan, neg_nan, inf, neg_inf = 0x7FC0, 0xFFFF, 0x7F80, 0xFF80
+    bad = {1: (300, nan), 2: (I + 5, inf), 3: (700, neg_inf), 4: (I + 1023, neg_nan),
+           5: (128, inf), 6: (I + 130, neg_inf), 7: (127, 0x7F81)}
+    for r, (c, v) in bad.items():
+        x[r, c] = v
+    x[5, I + 128] = 0            # an infinite gate on an up of zero
+    x[6, 130] = 0                # and the other way round
+    x[8, 0], x[8, I] = 0x7F7F, 0x7F7F  # the product of two finite values is kept finite
+    start = np.array([0], np.int32)
+    q, sc = fp8(capi, [n], start, n, x, I, flags)
+    x[8, 0], x[8, I] = clean[8, 0], clean[8, I]
+    q0, sc0 = fp8(capi, [n], start, n, clean, I, flags)
+
+    def groups(s):
+        if not flags & WORDS:
+            return s
+        return np.stack([(s.astype(np.int64) >> k) & 255 for k in (0, 8, 16, 24)],
+                        -1).reshape(n, -1)
+
+    s, s0 = groups(sc), groups(sc0)
+    q, q0 = q.reshape(n, I // 128, 128), q0.reshape(n, I // 128, 128)
+    hit = np.zeros((n, I // 128), bool)
+    for r, (c, _) in bad.items():
+        hit[r, c % I // 128] = True
+    over = np.zeros_like(hit)
+    over[8, 0] = True
+    assert np.all((q[hit] & 0x7F) == 0x7F)
+    assert np.all(s[hit] == 255) if flags & WORDS else np.isnan(s[hit]).all()
+    assert np.array_equal(q[~hit & ~over], q0[~hit & ~over])
+    assert np.array_equal(s[~hit & ~over], s0[~hit & ~over])
+    assert np.all((q[8, 0] & 0x7F) < 0x7F) and (flags or q[8, 0, 0] == 0x7E)
+    assert s[8, 0] < 255 if flags & WORDS else np.isfinite(s[8, 0])
+
+
+def test_gradient_of_values_that_are_not_finite(capi):
+    """NaN where the formulas give NaN, an infinity where they give one, and the
+    other channels as without them."""
+    I = 64
+    rng = np.random.default_rng(37)
+    g, u, d = (rng.standard_normal((7, I)).astype(np.float32) for _ in range(3))
+    clean = [mi.to_bf16_bits(v) for v in (g, u, d)]
+    at = np.arange(0, I, 3)
+    g, u, d = g.copy(), u.copy(), d.copy()
+    g[0, at], u[1, at], d[2, at] = np.nan, np.nan, np.nan
+    g[3, at], u[4, at], d[5, at] = np.inf, -np.inf, np.inf
+    g[6, at] = -np.inf
+    bits = [mi.to_bf16_bits(v) for v in (g, u, d)]
+    start, cnt = to_dev(np.array([0], np.int32)), to_dev(np.array([7], np.int32))
+    got = []
+    for b in (bits, clean):
+        dx = torch.zeros(7, 2 * I, dtype=torch.int16, device=dev())
+        capi.moe_swiglu_grad(1, I, 7, to_dev(np.concatenate(b[:2], 1)), to_dev(b[2]), start, cnt,
+                             dx)
+        torch.cuda.synchronize()
+        got.append(dx.cpu().numpy().view(np.uint16))
+    have = mi.bf16_bits_to_f32(got[0])
+    g, u, d = (mi.bf16_bits_to_f32(b).astype(np.float64) for b in bits)
+    with np.errstate(all="ignore"):
+        s = 1 / (1 + np.exp(-g))
+        want = np.concatenate([d * u * s * (1 + g * (1 - s)), d * g * s], 1)
+    assert np.array_equal(np.isnan(have), np.isnan(want))
+    assert np.array_equal(have[np.isinf(want)], want[np.isinf(want)])
+    assert not np.isfinite(want[:, at]).all() and np.isinf(want).any()
+    rest = np.setdiff1d(np.arange(2 * I), np.concatenate([at, at + I]))
+    assert np.array_equal(got[0][:, rest], got[1][:, rest])
