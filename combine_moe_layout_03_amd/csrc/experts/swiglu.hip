@@ -40,19 +40,21 @@ __device__ __forceinline__ bool any_not_finite(ex_u32x4 v) {
   return r;
 }
 
-// 1 / (1 + exp(-x)) of a bf16 value within six half float steps for |x| <= 87
+// 4 / (1 + exp(-x)) of a bf16 value within six half float steps for |x| <= 88.5
 // (one step each for the exponential and the reciprocal, half for the sum and the
-// correction); beyond, 0 or 1. 2^t with t = -x log2(e) rounded to one float would
+// correction); beyond, 0 or 4. 2^t with t = -x log2(e) rounded to one float would
 // be off by 2^-24 |x|: what t ln2 differs from -x (ln2 in two floats; exact to
 // 2^-40) is added back. At the bound -89 the power is infinite and the correction
-// positive, so the result is 0; a bf16 value inside has a finite power.
-__device__ __forceinline__ float sigmoid_of(float x) {
+// positive, so the result is 0; a bf16 value inside has a finite power. Four times
+// the sigmoid, because the reciprocal flushes subnormals, which the sigmoid of
+// -87.5 to -88.5 is and its product with x is not; callers take x / 4 or such.
+__device__ __forceinline__ float sigmoid4_of(float x) {
   constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147182f, kLn2Low = -1.90465430e-9f;
   x = __builtin_amdgcn_fmed3f(x, -89.0f, 89.0f);
   const float t = x * -kLog2e;
   const float d = __builtin_fmaf(-t, kLn2Low, __builtin_fmaf(-t, kLn2, -x));
   const float e0 = __builtin_amdgcn_exp2f(t);
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e0, d, e0));
+  return __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fmaf(e0, d, e0), 0.25f, 0.25f));
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -149,8 +151,8 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       const float a = ex_lo(in.g[d]), b = ex_hi(in.g[d]);
-      h[2 * d] = a * sigmoid_of(a) * ex_lo(in.u[d]);
-      h[2 * d + 1] = b * sigmoid_of(b) * ex_hi(in.u[d]);
+      h[2 * d] = 0.25f * a * sigmoid4_of(a) * ex_lo(in.u[d]);
+      h[2 * d + 1] = 0.25f * b * sigmoid4_of(b) * ex_hi(in.u[d]);
     }
     // |h| as bit patterns, whose integer order puts infinities and NaN on top: a
     // gate or up that is not finite leaves an h that is not
@@ -233,15 +235,16 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_grad_kernel(
             e[2] = {ex_lo(in.d[j]), ex_hi(in.d[j])}, p[2], r[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float s = sigmoid_of(a[k]);
+        const float s4 = sigmoid4_of(a[k]), a4 = 0.25f * a[k];
+        const float slope = s4 * __builtin_fmaf(a4, __builtin_fmaf(s4, -0.25f, 1.0f), 0.25f);
         // The larger factor first: d_h * u can pass the float range, and u times a
         // small slope fall below it, where the product of the three does not. The
         // slope is at most 1.1, so half of it keeps the first product in range
         // too; a power of two, it changes no rounding.
         const bool up = fabsf(b[k]) > fabsf(e[k]);
         const float big = up ? b[k] : e[k], small = up ? e[k] : b[k];
-        p[k] = 2.0f * (small * (big * (0.5f * s * (1.0f + a[k] * (1.0f - s)))));
-        r[k] = e[k] * (a[k] * s);
+        p[k] = 2.0f * (small * (big * (0.5f * slope)));
+        r[k] = e[k] * (a4 * s4);
       }
       dg[j] = ex_bf16x2(p[0], p[1]);
       du[j] = ex_bf16x2(r[0], r[1]);

@@ -127,7 +127,8 @@ int moe_grouped_gemm_fp8(int32_t E, int32_t N, int32_t C, const uint8_t *a, cons
 
 /* The activation between an expert's two products, cast to FP8: for every row
  * of a segment, with g = x[r][0..I) and u = x[r][I..2I),
- *   h = g / (1 + exp(-g)) * u   (float, kept within the finite floats)
+ *   h = g / (1 + exp(-g)) * u   (float, kept within the finite floats; 0 where
+ *                                exp(-g) passes them)
  * cast as moe_quantize_fp8 casts a row (flags as there; the code is that of
  * h * (1 / scale), within two half float steps of the quotient): q [rows*I] codes,
  * scale [rows][I/128] float or [rows][I/512] words, row-major. x [rows*2I]

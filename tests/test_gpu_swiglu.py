@@ -336,3 +336,35 @@ def test_gradient_of_values_that_are_not_finite(capi):
     assert not np.isfinite(want[:, at]).all() and np.isinf(want).any()
     rest = np.setdiff1d(np.arange(2 * I), np.concatenate([at, at + I]))
     assert np.array_equal(got[0][:, rest], got[1][:, rest])
+
+
+def test_gates_whose_sigmoid_is_subnormal(capi):
+    """From -87.5 to -88.5 exp(-g) is finite, but its reciprocal is below the
+    smallest normal float; times a large up, value and gradient are not."""
+    I = 384
+    g = np.repeat(np.array([-87.0, -87.5, -88.0, -88.5, -86.5], np.float32), 3)
+    g = np.tile(g, I // 15 + 1)[:I][None].repeat(4, 0)
+    u = np.empty((4, I), np.float32)
+    u[0], u[1] = 3.3e38, -1e38
+    u[2] = np.linspace(1e36, 3e38, I)
+    u[3] = -np.geomspace(1e34, 1e38, I)
+    x = mi.to_bf16_bits(np.concatenate([g, u], 1))
+    start = np.array([0], np.int32)
+    q, sc = fp8(capi, [4], start, 4, x, I, 0)
+    check_fp8(np.arange(4), x, q, sc, I, 0)
+    d = np.where(np.arange(I) % 2, 3e38, -7.0).astype(np.float32)[None].repeat(4, 0)
+    d[0], d[1] = 10.0, -1e-3
+    dh = mi.to_bf16_bits(d)
+    dx = torch.zeros(4, 2 * I, dtype=torch.int16, device=dev())
+    capi.moe_swiglu_grad(1, I, 4, to_dev(x), to_dev(dh), to_dev(start),
+                         to_dev(np.array([4], np.int32)), dx)
+    torch.cuda.synchronize()
+    have = mi.bf16_bits_to_f32(dx.cpu().numpy().view(np.uint16)).astype(np.float64)
+    gg, uu, s, _ = ref.silu_mul(mi.bf16_bits_to_f32(x))
+    dd = mi.bf16_bits_to_f32(dh).astype(np.float64)
+    want = np.concatenate([dd * uu * s * (1 + gg * (1 - s)), dd * gg * s], 1)
+    # results past the largest bf16 are infinite
+    over = np.abs(want) > 3.38e38
+    assert not over[:2].any() and not over[:, I:].any()
+    tol = grad_tol(gg, uu, s, dd, want)
+    assert np.all(np.abs(have - want)[~over] <= tol[~over])
