@@ -186,14 +186,12 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
       s = __uint_as_float(b);
     }
     s = spoilt ? __uint_as_float(kNanBits) : s;
-    // The codes are those of h * (1 / s), within two half float steps of h / s
-    // (one for a power of two); the cast of bf16 rows divides exactly, but h
-    // itself is only good to eight. None passes 448 by more than those steps,
-    // which round to 448.
-    const float r = __builtin_amdgcn_rcpf(s), y = __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
+    // codes of the correctly rounded h / s, as the cast of bf16 rows divides (none
+    // passes 448 by more than half a float step, which rounds to 448)
+    const float y = 1.0f / s;
     float d8[8];
 #pragma unroll
-    for (int d = 0; d < 8; ++d) d8[d] = h[d] * y;
+    for (int d = 0; d < 8; ++d) d8[d] = div_by_scale(h[d], s, y);
     if (ok)
       __builtin_nontemporal_store(ex_u32x2{e4m3x4(d8[0], d8[1], d8[2], d8[3]),
                                            e4m3x4(d8[4], d8[5], d8[6], d8[7])},

@@ -129,8 +129,7 @@ int moe_grouped_gemm_fp8(int32_t E, int32_t N, int32_t C, const uint8_t *a, cons
  * of a segment, with g = x[r][0..I) and u = x[r][I..2I),
  *   h = g / (1 + exp(-g)) * u   (float, kept within the finite floats; 0 where
  *                                exp(-g) passes them)
- * cast as moe_quantize_fp8 casts a row (flags as there; the code is that of
- * h * (1 / scale), within two half float steps of the quotient): q [rows*I] codes,
+ * cast as moe_quantize_fp8 casts a row (flags as there): q [rows*I] codes,
  * scale [rows][I/128] float or [rows][I/512] words, row-major. x [rows*2I]
  * bf16; a NaN or infinity in it gives its group of 128 channels the scale NaN
  * (UE8M0: byte 255) and NaN codes, so that it shows in every result of its row's

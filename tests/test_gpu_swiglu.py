@@ -368,3 +368,38 @@ def test_gates_whose_sigmoid_is_subnormal(capi):
     assert not over[:2].any() and not over[:, I:].any()
     tol = grad_tol(gg, uu, s, dd, want)
     assert np.all(np.abs(have - want)[~over] <= tol[~over])
+
+
+@pytest.mark.parametrize("flags", [0, ROUND, ROUND | WORDS])
+def test_codes_are_those_of_the_cast_of_rows(capi, flags):
+    """With gates of 128 the sigmoid is 1 and h = 128 u a bf16 value, so the cast
+    has to give what moe_quantize_fp8 gives for the same rows, bit for bit: every
+    significand of a group's largest value against every one below it, over the
+    E4M3 range. Among them are 76 quotients that fall on the middle of two codes,
+    which a product with the scale's reciprocal misses."""
+    sig = np.arange(128, 256, dtype=np.float32) / 128
+    I = 128 * 128                   # a group per significand of its largest value
+    binades = 2.0 ** -np.arange(0, 18, dtype=np.float32)
+    rows = len(binades) * 2         # 64 of the significands below it in each row's group
+    h = np.empty((rows, 128, 128), np.float32)
+    for b, two in enumerate(binades):
+        for half in range(2):
+            v = sig[64 * half:64 * half + 64] * two
+            h[2 * b + half, :, :64] = v
+            h[2 * b + half, :, 64:] = -v[::-1]
+    h = np.minimum(h, sig[None, :, None])
+    h = np.maximum(h, -sig[None, :, None])
+    h[:, :, 0] = sig
+    h = h.reshape(rows, I)
+    u = mi.to_bf16_bits(h)
+    assert np.array_equal(mi.bf16_bits_to_f32(u), h)
+    g = np.full((rows, I), 0x4300, np.uint16)
+    start = np.array([0], np.int32)
+    q, sc = fp8(capi, [rows], start, rows, np.concatenate([g, u], 1), I, flags)
+    want = torch.zeros(rows, I, dtype=torch.uint8, device=dev())
+    ws = torch.zeros(sc.shape, device=dev(),
+                     dtype=torch.int32 if flags & WORDS else torch.float32)
+    capi.moe_quantize_fp8(rows, I, to_dev(mi.to_bf16_bits(128 * h)), want, ws, flags)
+    torch.cuda.synchronize()
+    assert np.array_equal(sc, ws.cpu().numpy())
+    assert np.array_equal(q, want.cpu().numpy()), np.count_nonzero(q != want.cpu().numpy())
