@@ -77,8 +77,9 @@ __device__ __forceinline__ float key_logit(uint32_t k) {  // 0 -> -infinity
 }
 
 // exp(d) for d <= 0: the exponent d log2(e) is rounded once, so the result is off
-// by 2^-24 |d| and one step. For the sum over all experts, where the terms of
-// large |d| are small against the first, which is 1.
+// by 2^-24 |d| and one step. Only for a sum over all experts, where the terms of
+// large |d| are small against the first, which is 1; the gradient, where a term
+// is an expert's own result, takes expf.
 __device__ __forceinline__ float exp_below(float d) {
   return __builtin_amdgcn_exp2f(d * 1.44269504f);
 }
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      v[j] = exp_below(key_logit(key[j]) - top);
+      v[j] = expf(key_logit(key[j]) - top);
       s += v[j];
     }
     sum = wave_sum_f(s);

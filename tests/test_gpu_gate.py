@@ -206,3 +206,24 @@ def test_empty_batch_and_repeat(capi):
         got.append((idx.clone(), w.clone(), d.clone()))
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_gradient_of_unselected_experts(capi):
+    """An unselected expert's own gradient is -p_e times a number: its p_e has to
+    be good by itself, also where it is a small part of the sum. The differences
+    to the largest logit are whole numbers, so nothing is lost in them. In half
+    float steps: the exponential 2, the sum over E = 64 terms 2 + 9 + 1, which
+    counts for the selected p and for the quotient (24), two quotients and three
+    products 5: 31. (The smallest of them is still a normal float.)"""
+    E = 64
+    x = np.full((24, E), -90.0, np.float32)
+    x[:, 5] = 0.0
+    x[:, 20:47] = -np.arange(60, 87)  # 27 distances
+    x[12:] += 64.0
+    ids = np.full((24, 1), 5, np.int64)
+    dw = (np.linspace(1, 3, 24) * np.tile([1, -1], 12)).astype(np.float32)[:, None]
+    _, _, dx, st = run(capi, torch.from_numpy(x), 1, 0, 1.0, dw, ids)
+    want = ref.gate_grad(x, ids, dw, False, False, 1.0)
+    assert st == 0
+    off = np.abs(dx - want)[:, 20:47] / np.abs(want)[:, 20:47]
+    assert off.max() <= 31 * ref.EPS24, off.max() / ref.EPS24
