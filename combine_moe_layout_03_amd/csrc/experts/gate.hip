@@ -268,8 +268,9 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(
     g = id < 0 ? 0.0f : d * p;
     const float dot = wave_sum_f(g);
     const float r = sum > 0.0f ? dot / sum : 0.0f;
+    // (a masked logit's 0 stays 0 where d_weights makes r infinite or NaN)
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = -v[j] * r;
+    for (int j = 0; j < V; ++j) v[j] = key[j] ? -v[j] * r : 0.0f;
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = 0.0f;

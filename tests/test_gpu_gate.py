@@ -227,3 +227,24 @@ def test_gradient_of_unselected_experts(capi):
     assert st == 0
     off = np.abs(dx - want)[:, 20:47] / np.abs(want)[:, 20:47]
     assert off.max() <= 31 * ref.EPS24, off.max() / ref.EPS24
+
+
+@pytest.mark.parametrize("E", [40, 200, 700])
+@pytest.mark.parametrize("flags", [0, SIG, REN, SIG | REN])
+def test_masked_logits_get_zero_from_any_weight_gradient(capi, flags, E):
+    """NaN and infinities among d_weights reach unmasked logits only, of their
+    own token."""
+    K = 4
+    rng = np.random.default_rng(E)
+    x = rng.standard_normal((6, E)).astype(np.float32)
+    x[:, ::3] = -np.inf
+    x[5, 1] = np.nan
+    dw = rng.standard_normal((6, K)).astype(np.float32)
+    clean = dw.copy()
+    dw[0, 1], dw[1, 0], dw[2, 3], dw[3, 2], dw[5, 0] = (np.nan, np.inf, -np.inf, 3.4e38, np.nan)
+    d = torch.from_numpy(x)
+    _, _, dx, _ = run(capi, d, K, flags, 2.0, dw)
+    _, _, want, _ = run(capi, d, K, flags, 2.0, clean)
+    assert np.all(dx[~np.isfinite(x)] == 0)
+    assert np.array_equal(dx[4], want[4])
+    assert np.isnan(dx[0]).any() and np.isnan(dx[5]).any()
