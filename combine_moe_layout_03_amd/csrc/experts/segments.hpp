@@ -53,9 +53,9 @@ __device__ __forceinline__ int plan_segments(const Segments &seg, int piece, Pla
     // Segments that overlap against the rules could overflow the 32-bit sums
     // (up to 1024 segments of up to 2^31 rows): a coarse sum of all of them
     // first, in units of 1024 rows, and no pieces at all if it passes the
-    // buffer's rows.
+    // buffer's rows. What remains is less than 2^31 + 2^21.
     block_exclusive_scan(coarse, p.wave, kThreads / 64, &total);
-    if (total > (int)(seg.rows >> 10) + 1 + seg.E) {
+    if ((uint32_t)total > (uint32_t)((seg.rows >> 10) + 1 + seg.E)) {
       mine = 0;
       bad = true;
 #pragma unroll
@@ -63,6 +63,12 @@ __device__ __forceinline__ int plan_segments(const Segments &seg, int piece, Pla
     }
   }
   int at = block_exclusive_scan(mine, p.wave, kThreads / 64, &total);
+  if (total < 0) {  // uniform: pieces of one row each past 2^31 - 1 after all
+    total = at = 0;
+    bad = true;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) n[i] = 0;
+  }
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
     if (i < per && e0 + i < seg.E) {

@@ -403,3 +403,28 @@ def test_codes_are_those_of_the_cast_of_rows(capi, flags):
     torch.cuda.synchronize()
     assert np.array_equal(sc, ws.cpu().numpy())
     assert np.array_equal(q, want.cpu().numpy()), np.count_nonzero(q != want.cpu().numpy())
+
+
+def test_rows_that_pass_32_bits_together(capi):
+    """Overlapping segments of a buffer near 2^31 rows, whose rows together do not
+    fit 31 bits: against the rules, reported, and nothing is read or written.
+    (Their sum in units of 1024 rows still fits the buffer.)"""
+    I, rows = 8, (1 << 31) - 1
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 110 << 30:
+        pytest.skip("needs 96 GiB for the buffers")
+    extra = 1000
+    counts = np.ones(1 + extra, np.int32)
+    counts[0] = rows
+    start = np.zeros(1 + extra, np.int32)
+    start[1:] = np.arange(extra)
+    x = torch.empty(rows * 2 * I, dtype=torch.int16, device=dev())
+    dh = torch.empty(rows * I, dtype=torch.int16, device=dev())
+    ends = (x[:1 << 20], x[-(1 << 20):], x[rows * I:rows * I + (1 << 20)])
+    for t in ends:
+        t.fill_(0x1234)
+    st = torch.zeros(1, dtype=torch.int32, device=dev())
+    capi.moe_swiglu_grad(1 + extra, I, rows, x, dh, to_dev(start), to_dev(counts), x, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == capi.MOE_STATUS_BAD_SLOT
+    assert all(bool((t == 0x1234).all()) for t in ends)
