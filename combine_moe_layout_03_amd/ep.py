@@ -358,8 +358,11 @@ def combine_grad(d_out: torch.Tensor, y: torch.Tensor, handle: Handle,
 
 def dispatch_grad(d_recv: torch.Tensor, handle: Handle) -> torch.Tensor:
     """Gradient of the dispatch: each token's rows summed back, [T, H] bf16
-    (the combine without weights)."""
-    return combine(d_recv.reshape(-1, d_recv.shape[-1]), handle)
+    (the combine without weights), H being the width of d_recv."""
+    d_recv = d_recv.reshape(-1, d_recv.shape[-1])
+    s = handle.shape
+    shape = capi.make_shape(s.T, d_recv.shape[1], s.E, s.R, s.K, s.A)
+    return combine(d_recv, Handle(shape, handle.layout, handle.recv_rows))
 
 
 def _most_rows(handle: Handle) -> int:

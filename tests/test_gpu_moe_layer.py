@@ -262,3 +262,21 @@ def test_a_diverged_row_stays_visible(ep, T, words):
     assert bool(out[1][bad].isnan().all())
     rest = slot[~torch.isin(slot, bad)]
     assert torch.equal(out[0][rest], out[1][rest]) and bool(out[0][slot].isfinite().all())
+
+
+def test_dispatch_gradient_of_another_width(ep):
+    """dispatch_grad sums rows of the width it is given, whatever the width the
+    handle was made for."""
+    T, E, R, K = 19, 8, 2, 3
+    rng = np.random.default_rng(3)
+    idx = torch.from_numpy(mi._uniform_subsets(rng, T, E, K)).to(dev())
+    for made, H in ((8, 256), (64, 128), (512, 64)):
+        _, _, _, _, h = ep.get_dispatch_layout(idx, E, R, 4, made)
+        rows = to_dev(mi.to_bf16_bits(rng.standard_normal((h.recv_rows, H)).astype(
+            np.float32))).view(torch.bfloat16)
+        d_x = ep.dispatch_grad(rows, h)
+        assert h.shape.H == made  # the handle is as it was
+        t = host(rows.float()).numpy().astype(np.float64)[
+            host(h.layout.slot).numpy().reshape(T, K)]
+        assert np.all(np.abs(host(d_x.float()).numpy() - t.sum(1))
+                      <= ref.HALF_BF16 * np.abs(t.sum(1)) + K * ref.EPS24 * np.abs(t).sum(1))
