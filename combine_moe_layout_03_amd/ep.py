@@ -389,12 +389,17 @@ def expert_gemm(x: Tuple[torch.Tensor, torch.Tensor], weight: Tuple[torch.Tensor
     flags = capi.MOE_FP8_SCALE_ROWS
     if sc.dtype == torch.int32:
         flags |= capi.MOE_FP8_ROUND_SCALE | capi.MOE_FP8_UE8M0
+    if sc.shape[-1] != capi.fp8_scale_cols(Cc, flags):
+        raise ValueError(f"scales {tuple(sc.shape)} ({sc.dtype}) for rows of {Cc} codes")
     if not sc.is_contiguous():  # the page's view of a column-major tensor
         sc = sc.transpose(-1, -2)
         flags &= ~capi.MOE_FP8_SCALE_ROWS
         if handle.ll_M is None or not sc.is_contiguous():
             raise ValueError("scales are neither row-major nor a low-latency dispatch's "
                              "column-major tensor")
+        if sc.shape[-1] * E != rows:  # stripes of another length
+            raise ValueError(f"column-major scales of {sc.shape[-1]} rows per expert for "
+                             f"{rows} rows of {E} experts")
     if out is None:
         out = torch.empty(max(rows, 1), N, dtype=torch.bfloat16, device=q.device)
     lay = handle.layout

@@ -196,3 +196,30 @@ def test_wrapper_refusals(lib):
         ep.combine_grad(x[:6], x[:, :128], h)
     with pytest.raises(ValueError, match="for 6 tokens"):
         ep.gate_grad(torch.zeros(6, 8), torch.zeros(6, 2, dtype=torch.int64), torch.zeros(6, 3))
+
+
+def test_scales_have_to_match_the_rows(lib):
+    """Row scales of another width or layout than the codes', which hold enough
+    elements: refused, not read as something else."""
+    from combine_moe_layout_03_amd import ep
+
+    shape = lib.make_shape(6, 256, 4, 2, 2, 1)
+    lay = lib.LayoutBuffers.empty(shape, "cpu")
+    h = ep.Handle(shape, lay, 4 * 8, ll_M=4)  # stripes of 8 rows for each of 4 experts
+    q = torch.zeros(32, 256, dtype=torch.float8_e4m3fn)
+    w = (torch.zeros(4, 128, 256, dtype=torch.float8_e4m3fn), torch.ones(4, 1, 2))
+
+    def gemm(sc):
+        return ep.expert_gemm((q, sc), w, h)
+
+    columns = torch.ones(4, 2, 8)  # as the dispatch stores them
+    for good in (torch.ones(32, 2), torch.ones(2, 2, 8, 2), columns.transpose(1, 2),
+                 columns.view(2, 2, 2, 8).transpose(2, 3)):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            gemm(good)
+    for bad in (torch.ones(32, 4),                          # of rows twice as wide
+                columns,                                    # column-major, but not the view
+                torch.ones(32, 1),
+                torch.ones(4, 2, 16).transpose(1, 2)):      # stripes of another length
+        with pytest.raises(ValueError, match="scales"):
+            gemm(bad)
