@@ -14,6 +14,7 @@ no host synchronisation.
 """
 from __future__ import annotations
 
+import warnings
 from dataclasses import dataclass
 from typing import Optional, Tuple, Union
 
@@ -376,7 +377,13 @@ def expert_gemm(x: Tuple[torch.Tensor, torch.Tensor], weight: Tuple[torch.Tensor
     of an FP8 dispatch or of ``swiglu_fp8`` (float or UE8M0 scales, row-major or
     the low-latency dispatch's column-major), weight the (codes [E, N, C],
     scales [E, ceil(N/128), C/128] float32) tuple. Returns [rows, N] bf16; rows
-    of no expert are not written."""
+    of no expert are not written.
+
+    The product's gradient with respect to its rows is this call on d_out (cast
+    by ``capi.moe_quantize_fp8``) and the transposed weights, codes and scales
+    both, which takes N % 128 == 0. Store those once: weights that are not
+    contiguous, such as a transposed view, are copied by every call, with a
+    warning."""
     q, sc = x
     w, ws = weight
     E, N, Cc = w.shape
@@ -400,6 +407,9 @@ def expert_gemm(x: Tuple[torch.Tensor, torch.Tensor], weight: Tuple[torch.Tensor
         if sc.shape[-1] * E != rows:  # stripes of another length
             raise ValueError(f"column-major scales of {sc.shape[-1]} rows per expert for "
                              f"{rows} rows of {E} experts")
+    if not w.is_contiguous():
+        warnings.warn("expert_gemm copies weights that are not contiguous on every call: store "
+                      "transposed weights once", stacklevel=2)
     if out is None:
         out = torch.empty(max(rows, 1), N, dtype=torch.bfloat16, device=q.device)
     lay = handle.layout

@@ -13,8 +13,9 @@
  * and backward: moe_combine_grad (rows and weights), moe_swiglu_grad,
  * moe_combine with topk_weights = NULL (the gradient of the dispatch is the
  * plain sum of a token's rows), moe_gate_grad. The gradient of a product with
- * respect to its rows is the product with the transposed weights; the gradient
- * with respect to the weights is not part of this library.
+ * respect to its rows is the product of the cast gradient (moe_quantize_fp8) with
+ * the transposed weights; the gradient with respect to the weights is not part
+ * of this library.
  *
  * The conventions of moe_ep.h hold: caller-owned device pointers, nothing
  * allocated, freed or kept between calls, every call enqueues on the caller's
@@ -117,9 +118,12 @@ int moe_combine_grad(const moe_shape *shape, const uint16_t *d_out, const uint16
  *   more rows is skipped and sets MOE_STATUS_BAD_SLOT.
  * C % 128 == 0 (512 with UE8M0), N % 8 == 0, 8 <= N, C <= 2^20, E <= 1024.
  * a, w and out 16-byte aligned, scales 4-byte aligned. A row's scale times a
- * block's must be a finite float (the two are multiplied first). The gradient with
- * respect to the rows is the same call on weights stored transposed (the
- * blocks of w_scale transpose with them). */
+ * block's must be a finite float (the two are multiplied first; below 2^-126 the
+ * product loses bits). The gradient with respect to the rows is the same call on
+ * d_out, cast by moe_quantize_fp8, and on weights stored transposed: w [E*C*N],
+ * w_scale with its blocks changed over. N is the channel count there, so it
+ * takes N % 128 == 0 (512 with UE8M0); for another N both are stored with N
+ * rounded up, the added channels 0. */
 int moe_grouped_gemm_fp8(int32_t E, int32_t N, int32_t C, const uint8_t *a, const void *a_scale,
                          int64_t rows, const int32_t *row_start, const int32_t *count,
                          const uint8_t *w, const float *w_scale, uint16_t *out, int32_t flags,

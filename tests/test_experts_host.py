@@ -4,6 +4,7 @@ arguments before a device is touched."""
 import ctypes as C
 import os
 import re
+import warnings
 
 import pytest
 import torch
@@ -223,3 +224,25 @@ def test_scales_have_to_match_the_rows(lib):
                 torch.ones(4, 2, 16).transpose(1, 2)):      # stripes of another length
         with pytest.raises(ValueError, match="scales"):
             gemm(bad)
+
+
+def test_weights_that_would_be_copied_are_reported(lib):
+    """Weights that are not contiguous still run, but the copy of all of them
+    that each call makes is not silent; nor is a transposed product whose width
+    is no whole number of groups of 128 accepted."""
+    from combine_moe_layout_03_amd import ep
+
+    shape = lib.make_shape(6, 256, 4, 2, 2, 1)
+    h = ep.Handle(shape, lib.LayoutBuffers.empty(shape, "cpu"), 12)
+    q, sc = torch.zeros(12, 256, dtype=torch.float8_e4m3fn), torch.ones(12, 2)
+    w = torch.zeros(4, 256, 128, dtype=torch.float8_e4m3fn)
+    with pytest.warns(UserWarning, match="contiguous"):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            ep.expert_gemm((q, sc), (w.transpose(1, 2), torch.ones(4, 1, 2)), h)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(ValueError, match="GPU tensor"):
+            ep.expert_gemm((q, sc), (w.transpose(1, 2).contiguous(), torch.ones(4, 1, 2)), h)
+    raw = lib.lib()  # N = 200 forwards, so C = 200 back
+    assert raw.moe_grouped_gemm_fp8(4, 200, 256, D, D, 0, D, D, D, D, D, 4, 0, None, None) == 0
+    assert raw.moe_grouped_gemm_fp8(4, 256, 200, D, D, 0, D, D, D, D, D, 4, 0, None, None) == SHAPE
