@@ -280,3 +280,191 @@ def test_dispatch_gradient_of_another_width(ep):
             host(h.layout.slot).numpy().reshape(T, K)]
         assert np.all(np.abs(host(d_x.float()).numpy() - t.sum(1))
                       <= ref.HALF_BF16 * np.abs(t.sum(1)) + K * ref.EPS24 * np.abs(t).sum(1))
+
+
+def transposed(w):
+    """Weights stored for the product's gradient: rows and columns changed over,
+    the scales' blocks with them (N has to be a multiple of 128)."""
+    codes, scale = w
+    return (codes.view(torch.uint8).transpose(1, 2).contiguous().view(torch.float8_e4m3fn),
+            scale.transpose(1, 2).contiguous())
+
+
+def cast_rows(x, flags=0):
+    from combine_moe_layout_03_amd import capi
+
+    rows, width = x.shape
+    q = torch.empty(rows, width, dtype=torch.float8_e4m3fn, device=x.device)
+    sc = torch.empty(rows, capi.fp8_scale_cols(width, flags), device=x.device,
+                     dtype=torch.int32 if flags & capi.MOE_FP8_UE8M0 else torch.float32)
+    capi.moe_quantize_fp8(rows, width, x, q, sc, flags)
+    return q, sc
+
+
+def check_cast(x, h, rows):
+    """Codes and scales of the live rows against their definition."""
+    v = host(x.float()).numpy()[rows].astype(np.float64).reshape(len(rows), -1, 128)
+    s = scales64(h[1])[rows]
+    got = ref.e4m3_values(host(h[0].view(torch.uint8)).numpy()[rows]).reshape(v.shape)
+    assert np.all(np.abs(got * s[..., None] - v) <= 2.0 ** -4 * np.abs(v) * (1 + 2.0 ** -20)
+                  + 2.0 ** -10 * s[..., None])
+
+
+@pytest.mark.parametrize("mode", ["contiguous", "ll", "ll_words"])
+def test_backward_of_the_experts(ep, orc, mode):
+    """The whole way back, each step on what the one before it hands on: combine's
+    gradient, cast, product with the transposed weights, activation's gradient,
+    cast, the other transposed product, sum of a token's rows. Held to 64 bits
+    step by step, rows of no segment being whatever the buffers held."""
+    T, H, E, R, K, I, M = 37, 512, 16, 4, 4, 256, 64
+    rng = np.random.default_rng(41)
+    flags = 3 if mode == "ll_words" else 0
+    if flags:
+        I = 512
+    logits = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).to(dev())
+    x = to_dev(mi.to_bf16_bits(rng.standard_normal((T, H)).astype(np.float32))).view(torch.bfloat16)
+    d_out = to_dev(mi.to_bf16_bits(rng.standard_normal((T, H)).astype(np.float32))).view(
+        torch.bfloat16)
+    w1, w2 = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+    w1t, w2t = transposed(w1), transposed(w2)
+    idx, wt = ep.gate(logits, K, renormalize=True)
+    if mode == "contiguous":
+        _, _, _, _, handle = ep.get_dispatch_layout(idx, E, R, 16, H)
+        recv = ep.dispatch(cast_rows(x), handle)
+    else:
+        recv, _, handle = ep.low_latency_dispatch(x, idx, M, E, R, 1, use_fp8=True,
+                                                  use_ue8m0=bool(flags))
+    start, count = host(handle.layout.offset).numpy(), host(handle.layout.count).numpy()
+    rows_of = {e: np.arange(start[e], start[e] + count[e]) for e in range(E) if count[e]}
+    live = np.concatenate(list(rows_of.values()))
+    y1 = ep.expert_gemm(recv, w1, handle)
+    y2 = ep.expert_gemm(ep.swiglu_fp8(y1, handle, use_ue8m0=bool(flags)), w2, handle)
+
+    d_y2, d_w = ep.combine_grad(d_out, y2, handle, wt)
+    slot = host(handle.layout.slot).numpy().reshape(T, K)
+    do, y64 = (host(t.float()).numpy().astype(np.float64) for t in (d_out, y2))
+    w64 = host(wt).numpy().astype(np.float64)[..., None]
+    got = host(d_y2.float()).numpy().astype(np.float64)[slot]
+    want = w64 * do[:, None]
+    assert np.all(np.abs(got - want) <= (ref.HALF_BF16 + 2 * ref.EPS24) * np.abs(want))
+    prod = do[:, None] * y64[slot]
+    assert np.all(np.abs(host(d_w).numpy() - prod.sum(-1))
+                  <= (H / 256 + 16) * ref.EPS24 * np.abs(prod).sum(-1))
+
+    q2 = cast_rows(d_y2, flags)
+    check_cast(d_y2, q2, live)
+    d_h = ep.expert_gemm(q2, w2t, handle)
+    check_product(q2, w2t, rows_of, d_h)
+    # the same from the weights as they are stored: out = W^T d per expert
+    a = ref.e4m3_values(host(q2[0].view(torch.uint8)).numpy()) * np.repeat(
+        scales64(q2[1]), 128, 1)
+    wq = ref.e4m3_values(host(w2[0].view(torch.uint8)).numpy())
+    full = wq * np.repeat(np.repeat(host(w2[1]).numpy().astype(np.float64), 128, 1), 128, 2)
+    g = host(d_h.float()).numpy().astype(np.float64)
+    for e, r in rows_of.items():
+        b = np.ascontiguousarray(full[e].T)
+        tol = ref.HALF_BF16 * np.abs(a[r] @ full[e]) + ref.product_bound(a[r], b, H // 128)
+        assert np.all(np.abs(g[r] - a[r] @ full[e]) <= tol)
+
+    d_y1 = ep.swiglu_grad(y1, d_h, handle)
+    gg, uu, s, _ = ref.silu_mul(host(y1.float()).numpy()[live])
+    d = g[live]
+    want = np.concatenate([d * uu * s * (1 + gg * (1 - s)), d * gg * s], 1)
+    big = np.concatenate([np.abs(d * uu * s) * (1 + np.abs(gg)), np.abs(d * gg * s)], 1)
+    assert np.all(np.abs(host(d_y1.float()).numpy()[live] - want)
+                  <= ref.HALF_BF16 * np.abs(want) + 16 * ref.EPS24 * big + 1e-40)
+
+    q1 = cast_rows(d_y1, flags)
+    check_cast(d_y1, q1, live)
+    d_recv = ep.expert_gemm(q1, w1t, handle)
+    check_product(q1, w1t, rows_of, d_recv)
+    d_x = ep.dispatch_grad(d_recv, handle)
+    rows64 = host(d_recv.float()).numpy().astype(np.float64)[slot]
+    tot = rows64.sum(1)
+    assert np.all(np.abs(host(d_x.float()).numpy() - tot) <= ref.HALF_BF16 * np.abs(tot)
+                  + K * ref.EPS24 * np.abs(rows64).sum(1))
+    d_logits = host(ep.gate_grad(logits, idx, d_w, renormalize=True)).numpy()
+    xl, ids, dw = host(logits).numpy(), host(idx).numpy(), host(d_w).numpy()
+    want = ref.gate_grad(xl, ids, dw, False, True, 1.0)
+    size = (np.abs(dw) * ref.gate_weights(xl, ids, False, True, 1.0)).sum(1, keepdims=True)
+    assert np.all(np.abs(d_logits - want) <= 200 * ref.EPS24 * (np.abs(want) + size))
+    assert int(handle.layout.status.item()) == 0
+
+
+def test_backward_of_the_experts_in_a_graph(ep):
+    """Forward and the whole backward captured once: every replay on new inputs,
+    with eager runs between, equals the eager run bit for bit."""
+    T, H, E, R, K, I, M = 24, 256, 8, 2, 2, 128, 32
+    rng = np.random.default_rng(43)
+    w1, w2 = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+    w1t, w2t = transposed(w1), transposed(w2)
+    logits = torch.zeros(T, E, device=dev())
+    x, d_out = (torch.zeros(T, H, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+
+    def step():
+        idx, wt = ep.gate(logits, K)
+        recv, _, h = ep.low_latency_dispatch(x, idx, M, E, R, 0, use_fp8=True)
+        y1 = ep.expert_gemm(recv, w1, h)
+        y2 = ep.expert_gemm(ep.swiglu_fp8(y1, h), w2, h)
+        d_y2, d_w = ep.combine_grad(d_out, y2, h, wt)
+        d_h = ep.expert_gemm(cast_rows(d_y2), w2t, h)
+        d_y1 = ep.swiglu_grad(y1, d_h, h)
+        d_recv = ep.expert_gemm(cast_rows(d_y1), w1t, h)
+        return (ep.combine(y2, h, wt), ep.dispatch_grad(d_recv, h), ep.gate_grad(logits, idx, d_w),
+                d_w)
+
+    def fill(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for t in (logits, x, d_out):
+            t.copy_(torch.randn(t.shape, generator=g, device=dev()))
+
+    stream = torch.cuda.Stream()
+    fill(0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        held = step()
+    for seed in (1, 2, 1):
+        fill(seed)
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(held, want)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (seed, i)
+
+
+@pytest.mark.parametrize("T", [5, 70])
+def test_row_gradient_of_a_ragged_product(ep, T):
+    """A product of 200 columns has no transposed form (200 is no whole number of
+    groups); with rows and weights stored 256 wide, zeros behind, it has one."""
+    E, R, K, C, N, P = 4, 2, 2, 256, 200, 256
+    rng = np.random.default_rng(T)
+    w = weights(rng, E, N, C)
+    wide = torch.zeros(E, P, C, dtype=torch.uint8, device=dev())
+    wide[:, :N] = w[0].view(torch.uint8)
+    wt = transposed((wide.view(torch.float8_e4m3fn), w[1]))
+    idx = torch.from_numpy(mi._uniform_subsets(rng, T, E, K)).to(dev())
+    _, _, _, _, h = ep.get_dispatch_layout(idx, E, R, 1)
+    d_out = torch.zeros(h.recv_rows, P, dtype=torch.bfloat16, device=dev())
+    d_out[:, :N] = torch.randn(h.recv_rows, N, device=dev())
+    q = cast_rows(d_out)
+    d_in = ep.expert_gemm(q, wt, h)
+    start, count = host(h.layout.offset).numpy(), host(h.layout.count).numpy()
+    check_product(q, wt, {e: np.arange(start[e], start[e] + count[e]) for e in range(E)
+                          if count[e]}, d_in)
+    a = ref.e4m3_values(host(q[0].view(torch.uint8)).numpy()) * np.repeat(scales64(q[1]), 128, 1)
+    wq = ref.e4m3_values(host(w[0].view(torch.uint8)).numpy())
+    s = np.repeat(np.repeat(host(w[1]).numpy().astype(np.float64), 128, 1)[:, :N], 128, 2)
+    got = host(d_in.float()).numpy().astype(np.float64)
+    for e in range(E):
+        r = slice(start[e], start[e] + count[e])
+        if count[e]:
+            b = np.ascontiguousarray((wq[e] * s[e]).T)
+            want = a[r, :N] @ (wq[e] * s[e])
+            pad = np.pad(b, ((0, 0), (0, P - N)))
+            assert np.all(np.abs(got[r] - want) <= ref.HALF_BF16 * np.abs(want)
+                          + ref.product_bound(a[r], pad, P // 128))
