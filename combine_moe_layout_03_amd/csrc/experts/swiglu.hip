@@ -31,6 +31,14 @@ __device__ __forceinline__ float keep_finite(float h) {
   return __builtin_amdgcn_fmed3f(h, -3.402823466e38f, 3.402823466e38f);
 }
 
+// The bits of the largest |h|, of a NaN if there is one.
+__device__ __forceinline__ uint32_t largest(const float (&h)[8]) {
+  float m = fabsf(h[0]);
+#pragma unroll
+  for (int d = 1; d < 8; ++d) m = __builtin_elementwise_maximum(m, fabsf(h[d]));
+  return __float_as_uint(m) & 0x7fffffffu;
+}
+
 // Whether one of a vector's eight bf16 values is infinite or NaN.
 __device__ __forceinline__ bool any_not_finite(ex_u32x4 v) {
   bool r = false;
@@ -154,25 +162,19 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
       h[2 * d] = 0.25f * a * sigmoid4_of(a) * ex_lo(in.u[d]);
       h[2 * d + 1] = 0.25f * b * sigmoid4_of(b) * ex_hi(in.u[d]);
     }
-    // |h| as bit patterns, whose integer order puts infinities and NaN on top: a
-    // gate or up that is not finite leaves an h that is not
-    uint32_t top = 0;
-#pragma unroll
-    for (int d = 0; d < 8; ++d) top = umax32(top, __float_as_uint(h[d]) & 0x7fffffffu);
-    top = row16_max(top);
+    // The lane's largest |h| (NaN if one is, unlike fmaxf), over the group as bit
+    // patterns, whose integer order puts infinities and NaN on top. A gate or up
+    // that is not finite leaves an h that is not.
+    uint32_t top = row16_max(largest(h));
     bool spoilt = false;
     if (__ballot(top >= kInfBits)) {  // uniform, and rare
       // A product of finite values past the float range is kept at the largest
       // float; a group with an input that is not finite gets the scale NaN and, by
       // the quotients with it, NaN codes.
       const bool mine = any_not_finite(in.g) || any_not_finite(in.u);
-      top = mine ? kInfBits : 0u;
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        h[d] = keep_finite(h[d]);
-        top = umax32(top, __float_as_uint(h[d]) & 0x7fffffffu);
-      }
-      top = row16_max(top);
+      for (int d = 0; d < 8; ++d) h[d] = keep_finite(h[d]);
+      top = row16_max(mine ? kInfBits : largest(h));
       spoilt = top >= kInfBits;
     }
     float am = __uint_as_float(top);
@@ -186,9 +188,11 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
       s = __uint_as_float(b);
     }
     s = spoilt ? __uint_as_float(kNanBits) : s;
-    // codes of the correctly rounded h / s, as the cast of bf16 rows divides (none
-    // passes 448 by more than half a float step, which rounds to 448)
-    const float y = 1.0f / s;
+    // Codes of the correctly rounded h / s, as the cast of bf16 rows divides (none
+    // passes 448 by more than half a float step, which rounds to 448). One
+    // correction makes the reciprocal the correctly rounded one for every float
+    // significand (all 2^23 compared with 1 / s at six exponents).
+    const float r = __builtin_amdgcn_rcpf(s), y = __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
     float d8[8];
 #pragma unroll
     for (int d = 0; d < 8; ++d) d8[d] = div_by_scale(h[d], s, y);
