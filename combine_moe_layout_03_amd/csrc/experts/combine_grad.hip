@@ -9,11 +9,12 @@
 // token's row comes from L2 after the first of them (counted at 8192 x 8 x 7168:
 // 1062 MB read from memory, 1057 MB of y and d_out).
 //
-// Bound by the bytes of y and d_y. 4096 x 6 x 4096: 70 us (428 MB, 6.1 TB/s, a
-// large copy's rate); 8192 x 8 x 7168: 362 us (2.0 GB, 5.5 TB/s: rows of 14 KB
-// in and out at random places; 128 or 512 threads, or the loads of d_out ahead of
-// the slot's check, change it by 1%, loads or stores not marked nontemporal cost
-// 5 to 8%); 128 x 8 x 7168: 8 us, launch and one row's latency.
+// Bound by the bytes of y and d_y, rows at random places both ways. 8192 x 8 x
+// 7168: 362 us (2.0 GB, 5.5 TB/s; a large copy reaches 6.1; 128 or 512 threads, or
+// the loads of d_out ahead of the slot's check, change it by 1%, loads or stores
+// not marked nontemporal cost 5 to 8%); 4096 x 6 x 4096 with a masked rank, whose
+// rows of y are not read: 70 us (378 MB, 5.4 TB/s); 128 x 8 x 7168: 8 us, launch
+// and one row's latency.
 #include "experts.hpp"
 
 namespace moe {

@@ -10,14 +10,14 @@
 // bf16 logits and masks, go by the lowest expert id. Selection thus compares the
 // logits themselves: sigmoid and softmax keep their order, and two logits that
 // a rounded score would merge still rank as they stand. -0 is turned into +0
-// first, so that the two tie. What bounds the kernel is instructions (about 400
-// per token of 256 experts and eight places, one wave instruction in four
-// clocks), not the logits' bytes: 8192 such tokens take 7.7 us, their 9.2 MB
-// 1.5 us at the rate of a large copy; the gradient 7.5 us for 18 MB. Both are
-// near the time of the call itself (launch 1.6 us on the GPU, 6 us on the host).
-// A token per wave, because K rounds over one lane's share of the logits need
-// the maximum of the wave each time: more tokens per wave would split that
-// maximum's six steps over fewer lanes and make the lists longer.
+// first, so that the two tie. What bounds the kernel is instructions (391 per
+// token of 256 experts and eight places, one wave instruction in four clocks),
+// not the logits' bytes: 8192 such tokens take 7.7 us, their 9.2 MB 1.5 us at the
+// rate of a large copy; the gradient 8.0 us (387 instructions) for 18 MB. Both
+// are near the time of the call itself (launch 1.6 us on the GPU, 6 us on the
+// host). A token per wave is the plain form, not a measured optimum: four tokens
+// of a wave in a 16-lane row each would share the maxima, four steps for four
+// tokens, over lists four times as long. That is not built.
 //
 // Lane k then holds the k-th logit, and the weights of a token are computed in
 // its lanes at once. All statistics are float; the renormalised weights come

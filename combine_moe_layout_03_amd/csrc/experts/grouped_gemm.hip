@@ -274,12 +274,12 @@ __global__ __launch_bounds__(kStreamThreads, 2) void grouped_gemm_stream_kernel(
 
 // ---- tiles: segments of many rows -------------------------------------------
 //
-// A tile is 192 weight rows x up to 288 token rows: its float sums (3 x 9 of
-// 16 x 16 per wave) and operands fill 256 registers, its buffers LDS. The larger
-// the tile, the fewer bytes a product copies; 288 rows also take an expert of
-// average size of 8192 tokens x 8 over 256 experts in one piece, so that its
-// weights are read once (counted there, 7168 channels to 4096: 8.6 GB read, 8.0 at
-// least).
+// A tile is 192 weight rows x up to 288 token rows. The larger the tile, the fewer
+// bytes a product copies, and 288 rows are the most that fit: the float sums (3 x 9
+// of 16 x 16 per wave) and operands fill the 256 registers of eight waves, the
+// buffers LDS (four waves of 512 registers are not tried). At 8192 tokens x 8 over
+// 256 experts, 7168 channels to 4096, most experts are one piece: 8.6 GB read, 8.0
+// at least.
 // What bounds it (that product: 2420 us, 1590 TFLOP/s): the copies without the
 // products take 2230 us, the products without the copies 1670, all without memory
 // (rows and weights from L2) 1965. The matrix units are busy 45% of the clocks, at

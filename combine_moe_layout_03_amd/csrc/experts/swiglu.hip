@@ -9,15 +9,16 @@
 // channels of a scale are one 16-lane DPP row, as in the dispatch's cast. h
 // stays in float up to the E4M3 code.
 //
-// Bound by bytes: 65536 rows of 2 x 2048, the cast 675 MB and the gradient 1342 MB,
-// together 381 us (5.3 TB/s; a large copy reaches 6.1). The cast was bound by
-// instructions (268 per unit of 512 channels) until the walk's addresses were
-// left to the scalar unit and the sigmoid and the codes' quotient were cut to what
-// their error allows (162 now). Rows in runs, because a wave then looks a segment
+// Bound by bytes: 65536 rows of 2 x 2048, the cast 675 MB in 132 us and the gradient
+// 1342 MB in 258, the two calls 383 us (5.3 TB/s; a large copy reaches 6.1). The
+// cast was bound by instructions (268 per unit of 512 channels) until the walk's
+// addresses were left to the scalar unit and the sigmoid was cut to what its error
+// allows (181 now; the codes' exact quotients cost 3 us against h times the scale's
+// reciprocal). Rows in runs, because a wave then looks a segment
 // up only when it leaves one: units strided over the whole grid take 394 us;
 // twice the grid, or two units' registers in turn, change nothing, half the grid
 // costs 2%, loads or stores not marked nontemporal 3%. 512 rows in 256 stripes:
-// 4.2 us, most of it the launch and the sum of the counts (8.0 with the run split
+// 4.8 us, most of it the launch and the sum of the counts (8.0 with the run split
 // by 64-bit divisions, which take 2 us of a workgroup's start each).
 #include "segments.hpp"
 

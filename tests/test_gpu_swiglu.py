@@ -428,3 +428,5 @@ def test_rows_that_pass_32_bits_together(capi):
     torch.cuda.synchronize()
     assert int(st.item()) == capi.MOE_STATUS_BAD_SLOT
     assert all(bool((t == 0x1234).all()) for t in ends)
+    del x, dh, ends, t
+    torch.cuda.empty_cache()
