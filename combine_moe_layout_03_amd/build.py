@@ -17,7 +17,8 @@ SOURCES = ["capi.hip", "layout.hip", "fused.hip", "scatter.hip", "fp8.hip", "ran
            "rank_fused.hip", "replica.hip",
            # the operators around the experts (moe_experts.h)
            "experts/experts.hip", "experts/gate.hip", "experts/combine_grad.hip",
-           "experts/swiglu.hip", "experts/grouped_gemm.hip"]
+           "experts/swiglu.hip", "experts/grouped_gemm.hip", "experts/gate_grouped.hip",
+           "experts/norm.hip", "experts/linear.hip", "experts/act_grad.hip"]
 # floor kernels for the benchmark (measurement only; not part of the C ABI)
 FLOOR_LIB = os.path.join(PKG, "libmoe_floors.so")
 FLOOR_SOURCES = ["floors.hip"]

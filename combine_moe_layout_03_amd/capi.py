@@ -33,6 +33,14 @@ MOE_STATUS_BAD_LOGIT = 16
 MOE_GATE_BF16 = 1
 MOE_GATE_SIGMOID = 2
 MOE_GATE_RENORM = 4
+MOE_GATE_GROUP_SUM2 = 8
+
+MOE_LINEAR_SILU = 1
+MOE_LINEAR_GELU = 2
+MOE_LINEAR_SWIGLU = 3
+MOE_LINEAR_F32 = 4
+
+MOE_WORKSPACE_MAX_BYTES = 64 << 20
 
 MOE_FP8_ROUND_SCALE = 1
 MOE_FP8_UE8M0 = 2
@@ -104,6 +112,16 @@ def _load():
                                            P]),
         "moe_swiglu_fp8": (C.c_int, [I32, I32, I64, P, P, P, P, P, I32, P, P]),
         "moe_swiglu_grad": (C.c_int, [I32, I32, I64, P, P, P, P, P, P, P]),
+        "moe_gate_grouped": (C.c_int, [I32, I32, I32, I32, I32, P, P, P, P, I32, C.c_float, P, P]),
+        "moe_rms_norm": (C.c_int, [I32, I32, P, P, P, C.c_float, P, P, P, P, I32, P]),
+        "moe_rms_norm_grad_workspace_bytes": (SZ, [I32, I32]),
+        "moe_rms_norm_grad": (C.c_int, [I32, I32, P, P, C.c_float, P, P, P, P, P, SZ, P]),
+        "moe_linear_workspace_bytes": (SZ, [I32, I32, I32, I32]),
+        "moe_linear": (C.c_int, [I32, I32, I32, P, P, P, P, P, P, I32, P, SZ, P]),
+        "moe_linear_act_grad_workspace_bytes": (SZ, [I32, I32, I32]),
+        "moe_linear_act_grad": (C.c_int, [I32, I32, P, P, P, P, I32, P, SZ, P]),
+        "moe_linear_grad_workspace_bytes": (SZ, [I32, I32, I32]),
+        "moe_linear_grad": (C.c_int, [I32, I32, I32, P, P, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -125,7 +143,11 @@ EXPORTED = ("moe_abi_version", "moe_strerror", "moe_recv_rows_worst", "moe_ll_re
             "moe_replica_weight_sync", "moe_replica_grad_reduce")
 # the entry points of moe_experts.h
 EXPORTED_EXPERTS = ("moe_gate", "moe_gate_grad", "moe_combine_grad", "moe_grouped_gemm_fp8",
-                    "moe_swiglu_fp8", "moe_swiglu_grad")
+                    "moe_swiglu_fp8", "moe_swiglu_grad", "moe_gate_grouped", "moe_rms_norm",
+                    "moe_rms_norm_grad_workspace_bytes", "moe_rms_norm_grad",
+                    "moe_linear_workspace_bytes", "moe_linear",
+                    "moe_linear_act_grad_workspace_bytes", "moe_linear_act_grad",
+                    "moe_linear_grad_workspace_bytes", "moe_linear_grad")
 
 
 def lib():
@@ -720,3 +742,121 @@ def moe_swiglu_grad(E: int, I: int, rows: int, x: torch.Tensor, d_h: torch.Tenso
         _ptr(count, "count", _I32, E, dev),
         _ptr(d_x, "d_x", _BF16_LIKE, rows * 2 * I, dev),
         _ptr(status, "status", _I32, 1, dev, True), _raw_stream(stream, dev)))
+
+
+def moe_gate_grouped(T: int, E: int, K: int, groups: int, topk_groups: int, logits: torch.Tensor,
+                     bias: Optional[torch.Tensor], topk_idx: torch.Tensor,
+                     topk_weights: torch.Tensor, flags: int = 0, scale: float = 1.0,
+                     status: Optional[torch.Tensor] = None, stream=None) -> int:
+    """logits as for moe_gate; bias float32 or None."""
+    dev = _device(logits, "logits")
+    return _check("moe_gate_grouped", _lib.moe_gate_grouped(
+        T, E, K, groups, topk_groups, _ptr(logits, "logits", _F32 + _BF16, T * E, dev),
+        _ptr(bias, "bias", _F32, E, dev, True), _ptr(topk_idx, "topk_idx", _I64, T * K, dev),
+        _ptr(topk_weights, "topk_weights", _F32, T * K, dev), _logits(logits, flags), float(scale),
+        _ptr(status, "status", _I32, 1, dev, True), _raw_stream(stream, dev)))
+
+
+# -- the norm of the residual stream, and the dense product ---------------------
+
+_BYTES = (torch.uint8,)
+
+
+def _workspace(ws: Optional[torch.Tensor], dev: int):
+    """A workspace's address and size (the library knows what the call needs)."""
+    if ws is None:
+        return None, 0
+    return _ptr(ws, "workspace", _BYTES, 0, dev), ws.numel()
+
+
+def moe_rms_norm(T: int, H: int, x: torch.Tensor, residual: Optional[torch.Tensor],
+                 weight: torch.Tensor, eps: float, sum: Optional[torch.Tensor],
+                 y: Optional[torch.Tensor], q: Optional[torch.Tensor] = None,
+                 scale: Optional[torch.Tensor] = None, flags: int = 0, stream=None) -> int:
+    dev = _device(x, "x")
+    n = T * H
+    return _check("moe_rms_norm", _lib.moe_rms_norm(
+        T, H, _ptr(x, "x", _BF16_LIKE, n, dev),
+        _ptr(residual, "residual", _BF16_LIKE, n, dev, True),
+        _ptr(weight, "weight", _BF16_LIKE, H, dev), float(eps),
+        _ptr(sum, "sum", _BF16_LIKE, n, dev, True), _ptr(y, "y", _BF16_LIKE, n, dev, True),
+        _ptr(q, "q", _FP8_CODES, n, dev, True),
+        _ptr(scale, "scale", _fp8_scale_dtypes(flags), T * fp8_scale_cols(H, flags), dev, True),
+        int(flags), _raw_stream(stream, dev)))
+
+
+def moe_rms_norm_grad_workspace_bytes(T: int, H: int) -> int:
+    return int(_lib.moe_rms_norm_grad_workspace_bytes(int(T), int(H)))
+
+
+def moe_rms_norm_grad(T: int, H: int, sum: torch.Tensor, weight: torch.Tensor, eps: float,
+                      d_y: torch.Tensor, d_sum: Optional[torch.Tensor], d_x: torch.Tensor,
+                      d_weight: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None, stream=None) -> int:
+    dev = _device(sum, "sum")
+    n = T * H
+    return _check("moe_rms_norm_grad", _lib.moe_rms_norm_grad(
+        T, H, _ptr(sum, "sum", _BF16_LIKE, n, dev), _ptr(weight, "weight", _BF16_LIKE, H, dev),
+        float(eps), _ptr(d_y, "d_y", _BF16_LIKE, n, dev),
+        _ptr(d_sum, "d_sum", _BF16_LIKE, n, dev, True), _ptr(d_x, "d_x", _BF16_LIKE, n, dev),
+        _ptr(d_weight, "d_weight", _F32, H, dev, True), *_workspace(ws, dev),
+        _raw_stream(stream, dev)))
+
+
+def moe_linear_workspace_bytes(T: int, N: int, C_: int, flags: int = 0) -> int:
+    return int(_lib.moe_linear_workspace_bytes(int(T), int(N), int(C_), int(flags)))
+
+
+def _act_rows(N: int, flags: int) -> int:
+    """Columns of the product in front of the activation."""
+    return 2 * N if flags & 3 == MOE_LINEAR_SWIGLU else N
+
+
+def moe_linear(T: int, N: int, C_: int, x: torch.Tensor, w: torch.Tensor,
+               bias: Optional[torch.Tensor], residual: Optional[torch.Tensor],
+               out: torch.Tensor, pre: Optional[torch.Tensor] = None, flags: int = 0,
+               ws: Optional[torch.Tensor] = None, stream=None) -> int:
+    """out float32 with MOE_LINEAR_F32, else bf16."""
+    dev = _device(x, "x")
+    rows = _act_rows(N, flags)
+    return _check("moe_linear", _lib.moe_linear(
+        T, N, C_, _ptr(x, "x", _BF16_LIKE, T * C_, dev), _ptr(w, "w", _BF16_LIKE, rows * C_, dev),
+        _ptr(bias, "bias", _F32, rows, dev, True),
+        _ptr(residual, "residual", _BF16_LIKE, T * N, dev, True),
+        _ptr(out, "out", _F32 if flags & MOE_LINEAR_F32 else _BF16_LIKE, T * N, dev),
+        _ptr(pre, "pre", _BF16_LIKE, T * rows, dev, True), int(flags), *_workspace(ws, dev),
+        _raw_stream(stream, dev)))
+
+
+def moe_linear_act_grad_workspace_bytes(T: int, N: int, flags: int = 0) -> int:
+    return int(_lib.moe_linear_act_grad_workspace_bytes(int(T), int(N), int(flags)))
+
+
+def moe_linear_act_grad(T: int, N: int, d_out: torch.Tensor, pre: Optional[torch.Tensor],
+                        d_z: Optional[torch.Tensor], d_bias: Optional[torch.Tensor] = None,
+                        flags: int = 0, ws: Optional[torch.Tensor] = None, stream=None) -> int:
+    dev = _device(d_out, "d_out")
+    rows = _act_rows(N, flags)
+    return _check("moe_linear_act_grad", _lib.moe_linear_act_grad(
+        T, N, _ptr(d_out, "d_out", _BF16_LIKE, T * N, dev),
+        _ptr(pre, "pre", _BF16_LIKE, T * rows, dev, True),
+        _ptr(d_z, "d_z", _BF16_LIKE, T * rows, dev, True),
+        _ptr(d_bias, "d_bias", _F32, rows, dev, True), int(flags), *_workspace(ws, dev),
+        _raw_stream(stream, dev)))
+
+
+def moe_linear_grad_workspace_bytes(T: int, N: int, C_: int) -> int:
+    return int(_lib.moe_linear_grad_workspace_bytes(int(T), int(N), int(C_)))
+
+
+def moe_linear_grad(T: int, N: int, C_: int, d_z: torch.Tensor, x: Optional[torch.Tensor],
+                    w: Optional[torch.Tensor], d_x: Optional[torch.Tensor],
+                    d_w: Optional[torch.Tensor], ws: Optional[torch.Tensor] = None,
+                    stream=None) -> int:
+    dev = _device(d_z, "d_z")
+    return _check("moe_linear_grad", _lib.moe_linear_grad(
+        T, N, C_, _ptr(d_z, "d_z", _BF16_LIKE, T * N, dev),
+        _ptr(x, "x", _BF16_LIKE, T * C_, dev, True), _ptr(w, "w", _BF16_LIKE, N * C_, dev, True),
+        _ptr(d_x, "d_x", _BF16_LIKE, T * C_, dev, True),
+        _ptr(d_w, "d_w", _F32, N * C_, dev, True), *_workspace(ws, dev),
+        _raw_stream(stream, dev)))

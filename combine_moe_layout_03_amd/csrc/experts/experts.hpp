@@ -1,6 +1,6 @@
 // Internal launch interface between the C-ABI entry points (experts.hip) and
-// the kernels around the experts (gate.hip, combine_grad.hip, swiglu.hip,
-// grouped_gemm.hip). Not installed.
+// the kernels around the experts (gate.hip, gate_grouped.hip, combine_grad.hip,
+// swiglu.hip, grouped_gemm.hip, norm.hip, linear.hip, act_grad.hip). Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -13,7 +13,9 @@ namespace moe {
 
 constexpr int32_t kStBadLogit = 16;  // MOE_STATUS_BAD_LOGIT
 
-constexpr int kGateBf16 = 1, kGateSigmoid = 2, kGateRenorm = 4;  // MOE_GATE_*
+constexpr int kGateBf16 = 1, kGateSigmoid = 2, kGateRenorm = 4, kGateGroupSum2 = 8;  // MOE_GATE_*
+
+constexpr int64_t kMaxWorkspace = 64 << 20;  // MOE_WORKSPACE_MAX_BYTES
 
 typedef uint32_t ex_u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t ex_u32x2 __attribute__((ext_vector_type(2)));
@@ -94,6 +96,11 @@ hipError_t launch_gate_grad(const void *x, const int64_t *idx, const float *dw, 
                             int32_t E, int32_t K, int32_t flags, float scale, void *dx,
                             int32_t *status, hipStream_t s);
 
+// bias == nullptr: none. G groups, KG of them kept.
+hipError_t launch_gate_grouped(const void *x, const float *bias, int32_t T, int32_t E, int32_t K,
+                               int32_t G, int32_t KG, int32_t flags, float scale, int64_t *idx,
+                               float *w, int32_t *status, hipStream_t s);
+
 // mask.idx == nullptr: no rank mask.
 hipError_t launch_combine_grad(const uint16_t *dout, const uint16_t *y, int64_t rows,
                                const int32_t *slot, const float *w, uint16_t *dy, float *dw,
@@ -119,5 +126,34 @@ struct GemmArgs {
   int32_t *status;
 };
 hipError_t launch_grouped_gemm(const Segments &seg, const GemmArgs &g, hipStream_t s);
+
+// Rows of partial sums (n floats each) added up in an order that depends on P alone.
+hipError_t launch_column_sum(const float *partial, int32_t P, int32_t n, float *out,
+                             hipStream_t s);
+
+hipError_t launch_zeros(float *p, int64_t n, hipStream_t s);
+
+hipError_t launch_rms_norm(int32_t T, int32_t H, const uint16_t *x, const uint16_t *residual,
+                           const uint16_t *weight, float eps, uint16_t *sum, uint16_t *y,
+                           uint8_t *q, void *scale, int32_t flags, hipStream_t s);
+int32_t norm_grad_blocks(int32_t T, int32_t H);  // rows of partial sums in the workspace
+hipError_t launch_rms_norm_grad(int32_t T, int32_t H, const uint16_t *sum, const uint16_t *weight,
+                                float eps, const uint16_t *d_y, const uint16_t *d_sum,
+                                uint16_t *d_x, float *d_weight, float *ws, hipStream_t s);
+
+// The dense product (act: 0 none, 1 SiLU, 2 GELU, 3 SwiGLU) and its gradients;
+// the workspace's bytes of each.
+size_t linear_workspace(int32_t T, int32_t N, int32_t C, int32_t act);
+hipError_t launch_linear(int32_t T, int32_t N, int32_t C, const uint16_t *x, const uint16_t *w,
+                         const float *bias, const uint16_t *residual, void *out, uint16_t *pre,
+                         int32_t act, bool f32, float *ws, hipStream_t s);
+size_t act_grad_workspace(int32_t T, int32_t N, int32_t act);
+hipError_t launch_act_grad(int32_t T, int32_t N, const uint16_t *d_out, const uint16_t *z,
+                           uint16_t *d_z, float *d_bias, int32_t act, float *ws, hipStream_t s);
+size_t linear_grad_workspace(int32_t T, int32_t N, int32_t C);
+hipError_t launch_linear_grad_x(int32_t T, int32_t N, int32_t C, const uint16_t *d_z,
+                                const uint16_t *w, uint16_t *d_x, float *ws, hipStream_t s);
+hipError_t launch_linear_grad_w(int32_t T, int32_t N, int32_t C, const uint16_t *d_z,
+                                const uint16_t *x, float *d_w, float *ws, hipStream_t s);
 
 }  // namespace moe

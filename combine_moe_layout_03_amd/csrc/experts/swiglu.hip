@@ -20,26 +20,13 @@
 // costs 2%, loads or stores not marked nontemporal 3%. 512 rows in 256 stripes:
 // 4.8 us, most of it the launch and the sum of the counts (8.0 with the run split
 // by 64-bit divisions, which take 2 us of a workgroup's start each).
+#include "cast.hpp"
 #include "segments.hpp"
 
 namespace moe {
 namespace {
 
 constexpr int kSwThreads = kPlanThreads;
-constexpr uint32_t kInfBits = 0x7f800000u, kNanBits = 0x7fc00000u;
-
-__device__ __forceinline__ float keep_finite(float h) {
-  return __builtin_amdgcn_fmed3f(h, -3.402823466e38f, 3.402823466e38f);
-}
-
-// The bits of the largest |h|, of a NaN if there is one.
-__device__ __forceinline__ uint32_t largest(const float (&h)[8]) {
-  float m = fabsf(h[0]);
-#pragma unroll
-  for (int d = 1; d < 8; ++d) m = __builtin_elementwise_maximum(m, fabsf(h[d]));
-  return __float_as_uint(m) & 0x7fffffffu;
-}
-
 // Whether one of a vector's eight bf16 values is infinite or NaN.
 __device__ __forceinline__ bool any_not_finite(ex_u32x4 v) {
   bool r = false;
@@ -178,34 +165,15 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_fp8_kernel(
       top = row16_max(mine ? kInfBits : largest(h));
       spoilt = top >= kInfBits;
     }
-    float am = __uint_as_float(top);
-    if (am < 1e-4f) am = 1e-4f;
-    // am / 448, correctly rounded (product, remainder, correction)
-    const float s0 = am * (1.0f / 448.0f);
-    float s = __builtin_fmaf(__builtin_fmaf(-448.0f, s0, am), 1.0f / 448.0f, s0);
-    if (kFlags & kFp8RoundScale) {
-      uint32_t b = __float_as_uint(s);
-      if (b & 0x7fffffu) b = (b & 0xff800000u) + 0x800000u;
-      s = __uint_as_float(b);
-    }
-    s = spoilt ? __uint_as_float(kNanBits) : s;
-    // Codes of the correctly rounded h / s, as the cast of bf16 rows divides (none
-    // passes 448 by more than half a float step, which rounds to 448). One
-    // correction makes the reciprocal the correctly rounded one for every float
-    // significand (all 2^23 compared with 1 / s at six exponents).
-    const float r = __builtin_amdgcn_rcpf(s), y = __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
-    float d8[8];
-#pragma unroll
-    for (int d = 0; d < 8; ++d) d8[d] = div_by_scale(h[d], s, y);
+    const float sc = group_scale<kFlags>(top, spoilt);
+    const ex_u32x2 codes = group_codes(h, sc);
     if (ok)
-      __builtin_nontemporal_store(ex_u32x2{e4m3x4(d8[0], d8[1], d8[2], d8[3]),
-                                           e4m3x4(d8[4], d8[5], d8[6], d8[7])},
-                                  q + row * nv + v);
+      __builtin_nontemporal_store(codes, q + row * nv + v);
     if (kFlags & kFp8Ue8m0) {
-      const uint32_t word = ue8m0_word(s);
+      const uint32_t word = ue8m0_word(sc);
       if (lane == 0) wscale[row * nchunk + c] = word;
     } else if (ok && (lane & 15) == 0) {
-      fscale[row * (I / kFp8Group) + (v >> 4)] = s;
+      fscale[row * (I / kFp8Group) + (v >> 4)] = sc;
     }
   });
 }

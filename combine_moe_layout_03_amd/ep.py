@@ -306,22 +306,43 @@ def _gate_flags(score: str, renormalize: bool) -> int:
 
 
 def gate(logits: torch.Tensor, num_topk: int, score: str = "softmax", renormalize: bool = False,
-         scale: float = 1.0, status: Optional[torch.Tensor] = None):
+         scale: float = 1.0, status: Optional[torch.Tensor] = None,
+         bias: Optional[torch.Tensor] = None, num_groups: int = 1,
+         topk_groups: Optional[int] = None, group_score: str = "max"):
     """Router: (topk_idx [T, K] int64, topk_weights [T, K] float32) of logits
     [T, E] (float32 or bfloat16), ready for the dispatch calls. -inf masks an
-    expert; places no expert is left for get id -1 and weight 0."""
+    expert; places no expert is left for get id -1 and weight 0.
+
+    With bias [E] float32 the experts are chosen by score + bias and weighed by
+    the score; with num_groups > 1 only among the topk_groups groups of E /
+    num_groups neighbours whose best choice (group_score "max"), or whose two best
+    together ("sum2"), are largest."""
     T, E = logits.shape
     idx = torch.empty(T, num_topk, dtype=torch.int64, device=logits.device)
     w = torch.empty(T, num_topk, dtype=torch.float32, device=logits.device)
-    capi.moe_gate(T, E, num_topk, logits.contiguous(), idx, w, _gate_flags(score, renormalize),
-                  scale, status)
+    flags = _gate_flags(score, renormalize)
+    if group_score not in ("max", "sum2"):
+        raise ValueError(f"group_score is {group_score!r}, expected 'max' or 'sum2'")
+    if num_groups != 1 and topk_groups is None:
+        raise ValueError("num_groups needs topk_groups")
+    if bias is None and num_groups == 1 and topk_groups in (None, 1):
+        capi.moe_gate(T, E, num_topk, logits.contiguous(), idx, w, flags, scale, status)
+        return idx, w
+    if bias is not None and bias.shape != (E,):
+        raise ValueError(f"bias {tuple(bias.shape)} for {E} experts")
+    if group_score == "sum2":
+        flags |= capi.MOE_GATE_GROUP_SUM2
+    capi.moe_gate_grouped(T, E, num_topk, num_groups, 1 if topk_groups is None else topk_groups,
+                          logits.contiguous(), bias.contiguous() if bias is not None else None,
+                          idx, w, flags, scale, status)
     return idx, w
 
 
 def gate_grad(logits: torch.Tensor, topk_idx: torch.Tensor, d_weights: torch.Tensor,
               score: str = "softmax", renormalize: bool = False, scale: float = 1.0,
               status: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Gradient of ``gate``'s weights: d_logits [T, E] in the logits' type."""
+    """Gradient of ``gate``'s weights: d_logits [T, E] in the logits' type (with a
+    bias and groups too: none reaches the bias)."""
     T, E = logits.shape
     if topk_idx.shape != d_weights.shape or topk_idx.shape[0] != T:
         raise ValueError(f"topk_idx {tuple(topk_idx.shape)} and d_weights "
@@ -456,3 +477,133 @@ def swiglu_grad(x: torch.Tensor, d_h: torch.Tensor, handle: Handle) -> torch.Ten
     capi.moe_swiglu_grad(handle.shape.E, I, handle.recv_rows, x,
                          d_h.reshape(-1, I).contiguous(), lay.offset, lay.count, d_x, lay.status)
     return d_x
+
+
+# -- before and beside the experts: norm, dense product ------------------------
+
+
+def _bytes(n: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _rows(x: torch.Tensor, name: str) -> torch.Tensor:
+    if x.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected rows")
+    return x.contiguous()
+
+
+def _like(x: Optional[torch.Tensor], shape, name: str) -> Optional[torch.Tensor]:
+    if x is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    return x.contiguous() if x is not None else None
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+             residual: Optional[torch.Tensor] = None, use_fp8: bool = False,
+             round_scale: bool = False, use_ue8m0: bool = False):
+    """Residual addition and root-mean-square norm of rows x [T, H] bf16:
+    (y [T, H] bf16, sum [T, H] bf16, fp8). sum = x + residual, x itself without
+    one; fp8 is the (codes, row-major scales) tuple of y that ``dispatch`` and, with
+    a handle of one expert, ``expert_gemm`` take, None without use_fp8."""
+    x = _rows(x, "x")
+    T, H = x.shape
+    residual = _like(residual, x.shape, "residual")
+    weight = _like(weight, (H,), "weight")
+    y = torch.empty_like(x)
+    total = torch.empty_like(x) if residual is not None else None
+    flags, q, sc = 0, None, None
+    if use_fp8:
+        flags = ((capi.MOE_FP8_ROUND_SCALE if round_scale or use_ue8m0 else 0)
+                 | (capi.MOE_FP8_UE8M0 if use_ue8m0 else 0))
+        q = torch.empty(T, H, dtype=torch.float8_e4m3fn, device=x.device)
+        sc = torch.empty(T, capi.fp8_scale_cols(H, flags),
+                         dtype=torch.int32 if use_ue8m0 else torch.float32, device=x.device)
+    capi.moe_rms_norm(T, H, x, residual, weight, eps, total, y, q, sc, flags)
+    return y, x if total is None else total, (q, sc) if use_fp8 else None
+
+
+def rms_norm_grad(sum: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, eps: float = 1e-6,
+                  d_sum: Optional[torch.Tensor] = None):
+    """Gradient of ``rms_norm`` from its sum: (d_x [T, H] bf16, the gradient of x
+    and of the residual, and d_weight [H] float32). d_sum is what reaches the sum
+    by other ways."""
+    sum = _rows(sum, "sum")
+    T, H = sum.shape
+    d_x = torch.empty_like(sum)
+    d_w = torch.empty(H, dtype=torch.float32, device=sum.device)
+    capi.moe_rms_norm_grad(T, H, sum, _like(weight, (H,), "weight"), eps,
+                           _like(d_y, sum.shape, "d_y"), _like(d_sum, sum.shape, "d_sum"), d_x, d_w,
+                           _bytes(capi.moe_rms_norm_grad_workspace_bytes(T, H), sum.device))
+    return d_x, d_w
+
+
+_ACTIVATIONS = {None: 0, "silu": capi.MOE_LINEAR_SILU, "gelu": capi.MOE_LINEAR_GELU,
+                "swiglu": capi.MOE_LINEAR_SWIGLU}
+
+
+def _activation(name: Optional[str], weight: torch.Tensor):
+    """The library's flags, and the columns of the product's output."""
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation is {name!r}, expected one of {list(_ACTIVATIONS)}")
+    N = weight.shape[0]
+    if name != "swiglu":
+        return _ACTIVATIONS[name], N
+    if N % 2:
+        raise ValueError(f"weights of {N} rows are not gates and ups")
+    return _ACTIVATIONS[name], N // 2
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           activation: Optional[str] = None, residual: Optional[torch.Tensor] = None,
+           out_dtype: torch.dtype = torch.bfloat16, save_pre: bool = False):
+    """activation(x weight^T + bias) + residual of rows x [T, C] and weight [N, C],
+    bf16; bias [N] float32, residual [T, N] bf16. activation None, "silu", "gelu" or
+    "swiglu" (weight and bias hold the gates' rows, then the ups'). Returns out
+    [T, N] in out_dtype (bfloat16 or float32), with save_pre (out, what the
+    activation was applied to, bf16, for ``linear_grad``)."""
+    x, weight = _rows(x, "x"), _rows(weight, "weight")
+    T, Cc = x.shape
+    if weight.shape[1] != Cc:
+        raise ValueError(f"weights {tuple(weight.shape)} for rows of {Cc}")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype is {out_dtype}, expected bfloat16 or float32")
+    flags, N = _activation(activation, weight)
+    if save_pre and not flags:
+        raise ValueError("save_pre without an activation")
+    out = torch.empty(T, N, dtype=out_dtype, device=x.device)
+    pre = torch.empty(T, weight.shape[0], dtype=torch.bfloat16, device=x.device) if save_pre else None
+    if out_dtype == torch.float32:
+        flags |= capi.MOE_LINEAR_F32
+    capi.moe_linear(T, N, Cc, x, weight, _like(bias, (weight.shape[0],), "bias"),
+                    _like(residual, (T, N), "residual"), out, pre, flags,
+                    _bytes(capi.moe_linear_workspace_bytes(T, N, Cc, flags), x.device))
+    return (out, pre) if save_pre else out
+
+
+def linear_grad(d_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                pre: Optional[torch.Tensor] = None, activation: Optional[str] = None,
+                with_bias: bool = False):
+    """Gradients of ``linear``: (d_x [T, C] bf16, d_weight [N, C] float32, d_bias [N]
+    float32 or None); the residual's is d_out. d_out [T, N] bf16; float32, as the
+    router's ``gate_grad`` gives it, is rounded to bf16 first."""
+    x, weight = _rows(x, "x"), _rows(weight, "weight")
+    T, Cc = x.shape
+    flags, N = _activation(activation, weight)
+    rows, dev = weight.shape[0], x.device
+    if weight.shape[1] != Cc:
+        raise ValueError(f"weights {tuple(weight.shape)} for rows of {Cc}")
+    if (pre is not None) != bool(flags):
+        raise ValueError("pre goes with an activation")
+    d_z = _like(d_out, (T, N), "d_out").to(torch.bfloat16)
+    d_bias = torch.empty(rows, dtype=torch.float32, device=dev) if with_bias else None
+    if flags or with_bias:
+        need = capi.moe_linear_act_grad_workspace_bytes(T, N, flags) if with_bias else 0
+        to = torch.empty(T, rows, dtype=torch.bfloat16, device=dev) if flags else None
+        capi.moe_linear_act_grad(T, N, d_z, _like(pre, (T, rows), "pre"), to, d_bias, flags,
+                                 _bytes(need, dev))
+        d_z = to if flags else d_z
+    d_x = torch.empty_like(x)
+    d_w = torch.empty(rows, Cc, dtype=torch.float32, device=dev)
+    capi.moe_linear_grad(T, rows, Cc, d_z, x, weight, d_x, d_w,
+                         _bytes(capi.moe_linear_grad_workspace_bytes(T, rows, Cc), dev))
+    return d_x, d_w, d_bias

@@ -2,20 +2,25 @@
  * moe_experts.h -- C ABI of the operators around the experts, in the same
  * library as moe_ep.h (libmoe_ep.so, one AMD Instinct MI355X, gfx950): the
  * router in front of the layout, the experts' FP8 products and activation
- * between dispatch and combine, and the gradients of router, activation and
- * combine.
+ * between dispatch and combine, the gradients of router, activation and
+ * combine, and what stands before and beside them: the norm of the residual
+ * stream, and a dense product for the router's logits and a shared expert.
  *
  * One layer, forward:
- *   moe_gate -> topk_idx, topk_weights
+ *   moe_rms_norm -> the layer's rows, in bf16 and as FP8 codes
+ *   moe_linear (float logits) -> moe_gate or moe_gate_grouped -> topk_idx, topk_weights
  *   moe_layout_dispatch / moe_ll_layout_dispatch_fp8 / moe_dispatch_fp8 -> FP8 rows
  *   moe_grouped_gemm_fp8 (gate and up columns) -> moe_swiglu_fp8
  *   moe_grouped_gemm_fp8 (down) -> moe_combine
+ *   moe_linear (SwiGLU), moe_linear (down, the combined rows as its residual):
+ *   the shared expert
  * and backward: moe_combine_grad (rows and weights), moe_swiglu_grad,
  * moe_combine with topk_weights = NULL (the gradient of the dispatch is the
- * plain sum of a token's rows), moe_gate_grad. The gradient of a product with
- * respect to its rows is the product of the cast gradient (moe_quantize_fp8) with
- * the transposed weights; the gradient with respect to the weights is not part
- * of this library.
+ * plain sum of a token's rows), moe_gate_grad, moe_linear_act_grad and
+ * moe_linear_grad (rows and weights), moe_rms_norm_grad. The gradient of an
+ * expert's product with respect to its rows is the product of the cast gradient
+ * (moe_quantize_fp8) with the transposed weights; the gradient with respect to the
+ * experts' weights is not part of this library.
  *
  * The conventions of moe_ep.h hold: caller-owned device pointers, nothing
  * allocated, freed or kept between calls, every call enqueues on the caller's
@@ -45,6 +50,16 @@ extern "C" {
 #define MOE_GATE_BF16 1    /* logits (and d_logits) are bf16, else float */
 #define MOE_GATE_SIGMOID 2 /* scores are sigmoid(logit), else softmax over the E experts */
 #define MOE_GATE_RENORM 4  /* the selected scores are divided by their sum */
+
+#define MOE_GATE_GROUP_SUM2 8 /* moe_gate_grouped: a group scores the sum of its best two */
+
+/* moe_linear: the activation (the lowest two bits), and the output's type. */
+#define MOE_LINEAR_SILU 1
+#define MOE_LINEAR_GELU 2
+#define MOE_LINEAR_SWIGLU 3
+#define MOE_LINEAR_F32 4 /* out is float, else bf16 */
+
+#define MOE_WORKSPACE_MAX_BYTES 67108864 /* no workspace of this header is larger */
 
 #define MOE_STATUS_BAD_LOGIT 16 /* a NaN or +infinity among the logits: never selected */
 
@@ -77,6 +92,25 @@ int moe_gate(int32_t T, int32_t E, int32_t K, const void *logits, int64_t *topk_
 int moe_gate_grad(int32_t T, int32_t E, int32_t K, const void *logits, const int64_t *topk_idx,
                   const float *d_weights, void *d_logits, int32_t flags, float scale,
                   int32_t *status, hipStream_t stream);
+
+/* Router with a bias for balance and groups: with s = sigmoid(x) or softmax(x) of
+ * a token's logits, the choices c_e = s_e + bias[e] select and the scores s_e
+ * weigh. The experts are `groups` runs of E / groups neighbours. A group's score
+ * is its largest choice, or with MOE_GATE_GROUP_SUM2 the sum of its two largest
+ * (of the one where it has no other); the topk_groups groups of the largest
+ * scores stay, of equal ones the first. Selected are the K largest choices in
+ * them, larger first, equal ones by lower id; choices and groups' scores are
+ * compared as in 64 bits. bias [E] float, NULL: none; -infinity masks an expert
+ * (its logit still counts in the softmax's sum), NaN and +infinity do too and set
+ * MOE_STATUS_BAD_LOGIT. Logits, places without an expert, topk_weights, scale
+ * and the other flags are moe_gate's, and moe_gate_grad with the same flags
+ * (without MOE_GATE_GROUP_SUM2) is the gradient: none reaches the bias.
+ * E % groups == 0, 1 <= groups <= 64, 1 <= topk_groups <= groups; else as
+ * moe_gate. bias 4-byte aligned. */
+int moe_gate_grouped(int32_t T, int32_t E, int32_t K, int32_t groups, int32_t topk_groups,
+                     const void *logits, const float *bias, int64_t *topk_idx,
+                     float *topk_weights, int32_t flags, float scale, int32_t *status,
+                     hipStream_t stream);
 
 /* Gradient of moe_combine / moe_combine_masked: for every pair (t,k) with a
  * slot,
@@ -153,6 +187,79 @@ int moe_swiglu_fp8(int32_t E, int32_t I, int64_t rows, const uint16_t *x,
 int moe_swiglu_grad(int32_t E, int32_t I, int64_t rows, const uint16_t *x, const uint16_t *d_h,
                     const int32_t *row_start, const int32_t *count, uint16_t *d_x,
                     int32_t *status, hipStream_t stream);
+
+/* Norm of the residual stream: for every row
+ *   sum = bf16_rne( x + residual ),  rstd = 1 / sqrt( mean(sum^2) + eps ),
+ *   y   = sum * rstd * weight,
+ * in float (a row whose sum of squares passes the float range gets rstd 0).
+ *   x, residual [T*H] bf16; residual NULL: sum = x. weight [H] bf16.
+ *   sum [T*H] bf16, may be x or residual; NULL: not written, and NULL without a
+ *   residual (MOE_ERR_NULL).
+ *   y_out [T*H] bf16 = bf16_rne(y), NULL: not written.
+ *   q [T*H] E4M3 codes of y (not of y_out), with scale as moe_quantize_fp8 writes
+ *   it (flags as there); both or neither. A group with a y that is NaN or
+ *   infinite gets the scale NaN (UE8M0: byte 255) and NaN codes.
+ * At least one of y_out and q. H % 8 == 0 (with q 128, with MOE_FP8_UE8M0 512),
+ * 8 <= H <= 65536, T <= 2^24, eps >= 0 and finite. All but scale 16-byte aligned.
+ * Outputs overlap nothing else but as said. */
+int moe_rms_norm(int32_t T, int32_t H, const uint16_t *x, const uint16_t *residual,
+                 const uint16_t *weight, float eps, uint16_t *sum, uint16_t *y_out, uint8_t *q,
+                 void *scale, int32_t flags, hipStream_t stream);
+
+/* Its gradient, from the sum (x without a residual) and d_y [T*H] bf16: with
+ * n = sum * rstd and g = d_y * weight,
+ *   d_x = bf16_rne( d_sum + rstd * ( g - n * mean(g n) ) ),
+ *   d_weight[h] = sum over the rows of d_y n, in float.
+ * d_x is the gradient of x and of the residual alike. d_sum [T*H] bf16: what
+ * reaches the sum by other ways; NULL: nothing. d_x may be d_y or d_sum.
+ * d_weight [H] NULL: not computed (and no workspace is needed); zeros if T = 0.
+ * ws: ws_bytes >= moe_rms_norm_grad_workspace_bytes(T, H), 16-byte aligned;
+ * calls that may run at the same time need one each. */
+size_t moe_rms_norm_grad_workspace_bytes(int32_t T, int32_t H);
+int moe_rms_norm_grad(int32_t T, int32_t H, const uint16_t *sum, const uint16_t *weight,
+                      float eps, const uint16_t *d_y, const uint16_t *d_sum, uint16_t *d_x,
+                      float *d_weight, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Dense product: for 0 <= t < T, 0 <= n < N
+ *   z[t][n] = sum over c of x[t][c] * w[n][c] + bias[n],   out = act(z) + residual
+ * in float, rounded once. x [T*C], w [N*C] bf16; bias float, NULL: none; residual
+ * [T*N] bf16, NULL: none; out [T*N] bf16, or float with MOE_LINEAR_F32; it may be
+ * the residual's buffer if it is bf16. act by flags: none, SiLU z / (1 + exp(-z)),
+ * GELU z Phi(z), or SwiGLU: w [2N*C], bias [2N], the first half gates, the
+ * second ups, act = silu(z[t][n]) * z[t][N + n].
+ * pre [T*N] (SwiGLU [T*2N]) bf16_rne(z), for moe_linear_act_grad; NULL: not
+ * written, and NULL without an activation (MOE_ERR_NULL). out and pre overlap
+ * nothing else.
+ * N % 8 == 0, C % 8 == 0, 8 <= N, C <= 2^20, T <= 2^26 - 64, T*N and N*C at most
+ * 2^36 (a router of another number of experts pads its weights with rows of zeros
+ * and its bias with -infinity, which masks them in moe_gate). All pointers 16-byte aligned.
+ * ws: ws_bytes >= moe_linear_workspace_bytes of the same call (0 for most), 16-byte
+ * aligned; calls that may run at the same time need one each. */
+size_t moe_linear_workspace_bytes(int32_t T, int32_t N, int32_t C, int32_t flags);
+int moe_linear(int32_t T, int32_t N, int32_t C, const uint16_t *x, const uint16_t *w,
+               const float *bias, const uint16_t *residual, void *out, uint16_t *pre,
+               int32_t flags, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradient of its epilogue, from d_out [T*N] and pre bf16 (flags: the activation's):
+ *   d_z = bf16_rne( act'(z) d_out )  [T*N], SwiGLU [T*2N] as pre
+ *   d_bias = sum over the rows of d_z before its rounding, in float; NULL: not computed
+ * (and no workspace is needed), zeros if T = 0. Without an activation pre and d_z are NULL (d_z is
+ * d_out; MOE_ERR_NULL otherwise). The residual's gradient is d_out. d_z may be
+ * pre (SwiGLU too). Sizes, alignment and ws as for moe_linear. */
+size_t moe_linear_act_grad_workspace_bytes(int32_t T, int32_t N, int32_t flags);
+int moe_linear_act_grad(int32_t T, int32_t N, const uint16_t *d_out, const uint16_t *pre,
+                        uint16_t *d_z, float *d_bias, int32_t flags, void *ws, size_t ws_bytes,
+                        hipStream_t stream);
+
+/* Gradients of the product (N: rows of w, twice that of moe_linear for SwiGLU):
+ *   d_x[t][c] = bf16_rne( sum over n of d_z[t][n] * w[n][c] )    [T*C], or NULL
+ *   d_w[n][c] = sum over t of d_z[t][n] * x[t][c], in float      [N*C], or NULL
+ * w may be NULL without d_x, x without d_w. With T = 0 d_w is zeros. Sizes,
+ * alignment and ws as for moe_linear (d_z [T*N], x [T*C], w [N*C] bf16). */
+size_t moe_linear_grad_workspace_bytes(int32_t T, int32_t N, int32_t C);
+int moe_linear_grad(int32_t T, int32_t N, int32_t C, const uint16_t *d_z, const uint16_t *x,
+                    const uint16_t *w, uint16_t *d_x, float *d_w, void *ws, size_t ws_bytes,
+                    hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,193 @@
+"""The norm, the grouped router and the dense product on the CPU: the host checks
+of the library and of the binding refuse bad arguments before a device is touched."""
+import ctypes as C
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from combine_moe_layout_03_amd import capi
+
+    return capi
+
+
+D = C.c_void_p(256)
+HALF = C.c_void_p(258)
+FOUR = C.c_void_p(260)
+EIGHT = C.c_void_p(264)
+NULL, SHAPE, ALIGN, WORKSPACE, FLAGS = -1, -2, -5, -6, -10
+
+
+def test_gate_grouped_checks(lib):
+    raw = lib.lib()
+
+    def call(T=4, E=64, K=4, G=8, KG=2, x=D, b=D, i=D, w=D, flags=0, scale=1.0):
+        return raw.moe_gate_grouped(T, E, K, G, KG, x, b, i, w, flags, scale, None, None)
+
+    for kw in (dict(T=-1), dict(E=0), dict(E=1025), dict(K=0), dict(K=65), dict(K=5, E=4, G=1),
+               dict(T=(1 << 26) - 63), dict(G=0), dict(G=65, E=65), dict(G=7), dict(KG=0),
+               dict(KG=9), dict(scale=float("nan"))):
+        assert call(**kw) == SHAPE, kw
+    for f in (16, -1, 32):
+        assert call(flags=f) == FLAGS
+    for k in "xiw":
+        assert call(**{k: None}) == NULL
+    for kw in (dict(x=HALF), dict(b=HALF), dict(i=FOUR), dict(w=HALF)):
+        assert call(**kw) == ALIGN
+    assert call(T=0, x=None, i=None, w=None) == 0
+    assert raw.moe_gate(4, 64, 4, D, D, D, 8, 1.0, None, None) == FLAGS  # the grouped router's
+
+
+def test_norm_checks(lib):
+    raw = lib.lib()
+
+    def call(T=4, H=512, x=D, r=D, w=D, eps=1e-6, s=D, y=D, q=None, sc=None, flags=0):
+        return raw.moe_rms_norm(T, H, x, r, w, eps, s, y, q, sc, flags, None)
+
+    for kw in (dict(T=-1), dict(T=(1 << 24) + 1), dict(H=0), dict(H=12), dict(H=65544),
+               dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")),
+               dict(q=D, sc=D, H=192), dict(q=D, sc=D, H=640, flags=3)):
+        assert call(**kw) == SHAPE, kw
+    for f in (2, 8, -1):
+        assert call(q=D, sc=D, flags=f) == FLAGS
+    for kw in (dict(x=None), dict(w=None), dict(y=None), dict(q=D), dict(sc=D), dict(r=None)):
+        assert call(**kw) == NULL, kw
+    for kw in (dict(x=EIGHT), dict(r=EIGHT), dict(w=EIGHT), dict(s=EIGHT), dict(y=EIGHT),
+               dict(q=EIGHT, sc=D), dict(q=D, sc=HALF)):
+        assert call(**kw) == ALIGN, kw
+    assert call(T=0, x=None, w=None, y=None) == 0
+
+    def grad(T=4, H=512, s=D, w=D, eps=1e-6, dy=D, ds=D, dx=D, dw=D, ws=D, n=1 << 26):
+        return raw.moe_rms_norm_grad(T, H, s, w, eps, dy, ds, dx, dw, ws, n, None)
+
+    for kw in (dict(T=-1), dict(H=12), dict(eps=-1.0)):
+        assert grad(**kw) == SHAPE
+    for k in ("s", "w", "dy", "dx"):
+        assert grad(**{k: None}) == NULL
+        assert grad(**{k: EIGHT}) == ALIGN
+    assert grad(ds=EIGHT) == ALIGN and grad(dw=HALF) == ALIGN and grad(ws=EIGHT) == ALIGN
+    need = raw.moe_rms_norm_grad_workspace_bytes(4, 512)
+    assert need > 0
+    assert grad(ws=None) == WORKSPACE and grad(n=need - 1) == WORKSPACE
+    assert grad(T=0, s=None, dw=None) == 0
+    assert raw.moe_rms_norm_grad_workspace_bytes(-1, 512) == 0
+
+
+def test_linear_checks(lib):
+    raw = lib.lib()
+
+    def call(T=4, N=64, Cc=128, x=D, w=D, b=D, r=D, o=D, p=None, flags=0, ws=D, n=1 << 26):
+        return raw.moe_linear(T, N, Cc, x, w, b, r, o, p, flags, ws, n, None)
+
+    big = 1 << 20
+    for kw in (dict(T=-1), dict(T=(1 << 26) - 63), dict(N=0), dict(N=12), dict(N=big + 8),
+               dict(Cc=0), dict(Cc=20), dict(Cc=big + 8), dict(T=1 << 17, N=big),
+               dict(T=1 << 17, Cc=big), dict(N=big, Cc=1 << 17)):
+        assert call(**kw) == SHAPE, kw
+    for f in (8, -1, 16):
+        assert call(flags=f) == FLAGS
+    for kw in (dict(x=None), dict(w=None), dict(o=None), dict(p=D), dict(p=D, flags=4)):
+        assert call(**kw) == NULL, kw
+    for k in "xwbro":
+        assert call(**{k: EIGHT}) == ALIGN
+    assert call(p=EIGHT, flags=1) == ALIGN and call(ws=EIGHT) == ALIGN
+    need = raw.moe_linear_workspace_bytes(300, 256, 7168, 0)
+    assert need > 0
+    assert call(T=300, N=256, Cc=7168, n=need - 1) == WORKSPACE
+    assert call(T=300, N=256, Cc=7168, ws=None) == WORKSPACE
+    assert call(T=0, x=None, w=None, o=None, ws=None, n=0) == 0
+
+    def act(T=4, N=64, d=D, p=D, z=D, b=D, flags=1, ws=D, n=1 << 26):
+        return raw.moe_linear_act_grad(T, N, d, p, z, b, flags, ws, n, None)
+
+    for kw in (dict(T=-1), dict(N=12)):
+        assert act(**kw) == SHAPE
+    for f in (4, 5, -1):
+        assert act(flags=f) == FLAGS
+    for kw in (dict(d=None), dict(p=None), dict(z=None), dict(flags=0), dict(flags=0, p=None),
+               dict(flags=0, z=None), dict(flags=0, p=None, z=None, b=None)):
+        assert act(**kw) == NULL, kw
+    for kw in (dict(d=EIGHT), dict(p=EIGHT), dict(z=EIGHT), dict(b=HALF), dict(ws=EIGHT)):
+        assert act(**kw) == ALIGN
+    assert act(ws=None) == WORKSPACE
+    assert act(n=raw.moe_linear_act_grad_workspace_bytes(4, 64, 1) - 1) == WORKSPACE
+    assert act(T=0, d=None, p=None, z=None, b=None) == 0
+
+    def grad(T=300, N=256, Cc=7168, d=D, x=D, w=D, dx=D, dw=D, ws=D, n=1 << 26):
+        return raw.moe_linear_grad(T, N, Cc, d, x, w, dx, dw, ws, n, None)
+
+    for kw in (dict(T=-1), dict(N=12), dict(Cc=12)):
+        assert grad(**kw) == SHAPE
+    for kw in (dict(d=None), dict(dx=None, dw=None), dict(w=None), dict(x=None)):
+        assert grad(**kw) == NULL, kw
+    for k in ("d", "x", "w", "dx", "dw", "ws"):
+        assert grad(**{k: EIGHT}) == ALIGN
+    need = raw.moe_linear_grad_workspace_bytes(300, 256, 7168)
+    if need:
+        assert grad(n=need - 1) == WORKSPACE and grad(ws=None) == WORKSPACE
+    assert grad(T=0, d=None, x=None, w=None, dx=None, dw=None) == 0
+
+
+def test_workspaces_stay_within_the_bound(lib):
+    for T in (1, 3, 16, 100, 1001, 8192, 1 << 20):
+        for N in (8, 256, 2824, 65536):
+            assert lib.moe_rms_norm_grad_workspace_bytes(T, N) <= lib.MOE_WORKSPACE_MAX_BYTES
+            for f in range(4):
+                assert (lib.moe_linear_act_grad_workspace_bytes(T, N, f)
+                        <= lib.MOE_WORKSPACE_MAX_BYTES)
+            for Cc in (8, 256, 7168):
+                assert lib.moe_linear_grad_workspace_bytes(T, N, Cc) <= lib.MOE_WORKSPACE_MAX_BYTES
+                for f in range(4):
+                    assert (lib.moe_linear_workspace_bytes(T, N, Cc, f)
+                            <= lib.MOE_WORKSPACE_MAX_BYTES)
+
+
+def test_binding_refuses_cpu_tensors(lib):
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        lib.moe_rms_norm(4, 128, x, None, x[0], 1e-6, None, x)
+    with pytest.raises(ValueError, match="GPU"):
+        lib.moe_linear(4, 8, 128, x, x, None, None, x)
+    with pytest.raises(ValueError, match="GPU"):
+        lib.moe_gate_grouped(4, 128, 2, 8, 2, x.float(), None, x, x)
+
+
+def test_wrappers_refuse(lib):
+    from combine_moe_layout_03_amd import ep
+
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="activation"):
+        ep.linear(x, w, activation="tanh")
+    with pytest.raises(ValueError, match="weights"):
+        ep.linear(x, w[:, :32])
+    with pytest.raises(ValueError, match="bias"):
+        ep.linear(x, w, bias=torch.zeros(8))
+    with pytest.raises(ValueError, match="residual"):
+        ep.linear(x, w, residual=torch.zeros(4, 8, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="out_dtype"):
+        ep.linear(x, w, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="save_pre"):
+        ep.linear(x, w, save_pre=True)
+    with pytest.raises(ValueError, match="gates and ups"):
+        ep.linear(x, w[:15], activation="swiglu")
+    with pytest.raises(ValueError, match="pre"):
+        ep.linear_grad(torch.zeros(4, 16), x, w, activation="silu")
+    with pytest.raises(ValueError, match="d_out"):
+        ep.linear_grad(torch.zeros(4, 8), x, w)
+    with pytest.raises(ValueError, match="weight"):
+        ep.rms_norm(x, w[0, :32])
+    with pytest.raises(ValueError, match="rows"):
+        ep.rms_norm(x[0], w[0])
+    with pytest.raises(ValueError, match="residual"):
+        ep.rms_norm(x, w[0], residual=x[:2])
+    with pytest.raises(ValueError, match="d_y"):
+        ep.rms_norm_grad(x, w[0], x[:2])
+    lg = torch.zeros(4, 16)
+    with pytest.raises(ValueError, match="bias"):
+        ep.gate(lg, 2, bias=torch.zeros(8))
+    with pytest.raises(ValueError, match="topk_groups"):
+        ep.gate(lg, 2, num_groups=4)
+    with pytest.raises(ValueError, match="group_score"):
+        ep.gate(lg, 2, num_groups=4, topk_groups=2, group_score="mean")

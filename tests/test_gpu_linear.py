@@ -1,0 +1,283 @@
+"""Dense product with its epilogue, and its gradients, on the GPU against 64 bits."""
+import pytest
+import torch
+
+import dense_ref as ref
+from dense_ref import ACTS, EPS24, HALF_BF16, guard_ok, guarded
+from gpu_path import dev
+
+pytestmark = pytest.mark.gpu
+
+F32 = 4
+
+
+@pytest.fixture(scope="module")
+def capi():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from combine_moe_layout_03_amd import capi as c
+
+    return c
+
+
+def rows(g, T, C, sd=1.0):
+    """[T, C] bf16 with NaN behind the last row."""
+    _, v = guarded(T * C, torch.bfloat16, dev())
+    v.copy_((torch.randn(T * C, generator=g, device=dev()) * sd).to(torch.bfloat16))
+    return v.view(T, C)
+
+
+def workspace(n):
+    ws = torch.full((n + 256,), 255, dtype=torch.uint8, device=dev())
+    return ws, (ws[:n] if n else None)
+
+
+SIZES = [(1, 8, 8), (1, 256, 7168), (3, 40, 72), (15, 24, 200), (16, 256, 512), (17, 64, 1000),
+         (32, 264, 2048), (33, 520, 264), (64, 128, 64), (65, 72, 4104), (129, 264, 136),
+         (300, 1416, 520), (513, 264, 2056), (1001, 2824, 328), (2500, 40, 1544)]
+
+
+def check(capi, T, N, C, act, bias, res, f32, pre, seed=0):
+    g = torch.Generator(device=dev()).manual_seed(seed + T * 7 + N * 3 + C)
+    NN = 2 * N if act == "swiglu" else N
+    x, w = rows(g, T, C), rows(g, NN, C, C ** -0.5)
+    b = torch.randn(NN, generator=g, device=dev()) * 0.3 if bias else None
+    r = rows(g, T, N) if res else None
+    ob, out = guarded(T * N, torch.float32 if f32 else torch.bfloat16, dev())
+    pb, p = guarded(T * NN, torch.bfloat16, dev())
+    flags = ACTS.index(act) | (F32 if f32 else 0)
+    need = capi.moe_linear_workspace_bytes(T, N, C, flags)
+    assert need <= capi.MOE_WORKSPACE_MAX_BYTES
+    wb, ws = workspace(need)
+    capi.moe_linear(T, N, C, x, w, b, r, out, p if pre else None, flags, ws)
+    z, err = ref.dot_bound(x, w)
+    if bias:
+        z = z + b.double()
+        err = err + 2 * EPS24 * z.abs()
+    h, s1, s2 = ref.act64(z, act, N)
+    # the slope at the exact z, twice for its change over the error
+    tol = 2 * s1 * (err[:, :N] if act == "swiglu" else err)
+    if s2 is not None:
+        tol = tol + 2 * s2 * err[:, N:]
+    # exp, quotient, erf: 16 half steps of the value (GELU: of z, whose Phi is that exact)
+    tol = tol + 16 * EPS24 * h.abs()
+    if act != "none":
+        tol = tol + err.amax() ** 2
+    if res:
+        h = h + r.double()
+    tol = tol + (EPS24 if f32 else HALF_BF16) * (h.abs() + tol) + 1e-38
+    off = (out.view(T, N).double() - h).abs() / tol
+    assert float(off.max()) <= 1, (float(off.max()), divmod(int(off.argmax()), N))
+    if pre:
+        assert bool(((p.view(T, NN).double() - z).abs() <= HALF_BF16 * (z.abs() + err) + err).all())
+    assert guard_ok(ob, T * N) and guard_ok(pb, T * NN)
+    assert bool((wb[need:] == 255).all())
+    return out
+
+
+@pytest.mark.parametrize("T,N,C", SIZES)
+@pytest.mark.parametrize("act", ACTS)
+def test_sizes(capi, T, N, C, act):
+    check(capi, T, N, C, act, False, False, False, act != "none")
+    check(capi, T, N, C, act, True, True, True, False)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("bias,res,f32", [(True, False, False), (False, True, False),
+                                          (True, True, False), (False, False, True)])
+def test_epilogues(capi, act, bias, res, f32):
+    for T in (7, 200):
+        check(capi, T, 136, 320, act, bias, res, f32, act != "none")
+
+
+@pytest.mark.parametrize("T,N,C,act", [(4100, 3000, 136, "none"), (4100, 3000, 72, "gelu"),
+                                       (4100, 1504, 136, "swiglu"), (8200, 1600, 72, "silu")])
+def test_large(capi, T, N, C, act):
+    check(capi, T, N, C, act, True, True, False, act != "none")
+
+
+def test_in_place_residual(capi):
+    g = torch.Generator(device=dev()).manual_seed(1)
+    for T in (5, 300):
+        x, w, r = rows(g, T, 264), rows(g, 136, 264, 0.1), rows(g, T, 136)
+        _, ws = workspace(capi.moe_linear_workspace_bytes(T, 136, 264, 0))
+        out = torch.empty(T, 136, dtype=torch.bfloat16, device=dev())
+        capi.moe_linear(T, 136, 264, x, w, None, r, out, None, 0, ws)
+        capi.moe_linear(T, 136, 264, x, w, None, r, r, None, 0, ws)
+        assert torch.equal(out, r)
+
+
+@pytest.mark.parametrize("T", [5, 150])
+def test_not_finite_values_stay_in_their_row_and_column(capi, T):
+    g = torch.Generator(device=dev()).manual_seed(2)
+    x, w = rows(g, T, 200), rows(g, 72, 200, 0.1)
+    out, bad = (torch.empty(T, 72, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    _, ws = workspace(capi.moe_linear_workspace_bytes(T, 72, 200, 0))
+    capi.moe_linear(T, 72, 200, x, w, None, None, out, None, 0, ws)
+    x[3, 199] = float("nan")
+    w[70, 0] = float("inf")
+    capi.moe_linear(T, 72, 200, x, w, None, None, bad, None, 0, ws)
+    r = torch.ones(T, dtype=torch.bool, device=dev())
+    r[3] = False
+    c = torch.ones(72, dtype=torch.bool, device=dev())
+    c[70] = False
+    assert torch.equal(bad[r][:, c], out[r][:, c])
+    assert bool(torch.isnan(bad[3]).all()) and not bool(torch.isfinite(bad[:, 70]).any())
+
+
+def test_masked_router_columns(capi):
+    """60 experts: weights padded to 64 rows, the bias -infinity there."""
+    g = torch.Generator(device=dev()).manual_seed(3)
+    T, C = 40, 512
+    x, w = rows(g, T, C), torch.zeros(64, C, dtype=torch.bfloat16, device=dev())
+    w[:60] = rows(g, 60, C, C ** -0.5)
+    b = torch.zeros(64, device=dev())
+    b[60:] = -float("inf")
+    out = torch.empty(T, 64, device=dev())
+    _, ws = workspace(capi.moe_linear_workspace_bytes(T, 64, C, F32))
+    capi.moe_linear(T, 64, C, x, w, b, None, out, None, F32, ws)
+    idx = torch.empty(T, 4, dtype=torch.int64, device=dev())
+    wt = torch.empty(T, 4, device=dev())
+    st = torch.zeros(1, dtype=torch.int32, device=dev())
+    capi.moe_gate(T, 64, 4, out, idx, wt, 0, 1.0, st)
+    assert int(idx.max()) < 60 and int(idx.min()) >= 0 and int(st) == 0
+    z = x.double() @ w.double().t().contiguous()
+    assert bool((torch.sort(z[:, :60], 1, True).indices[:, :4] == idx).all())
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_far_activations(capi, act):
+    """Values of z from the far tails, by the bias; half a bf16 step of a tail's value."""
+    z = torch.tensor([-200.0, -104.0, -90.0, -88.5, -87.4, -60.0, -14.0, -6.0, -1.0, -1e-3, 0.0,
+                      1e-3, 1.0, 6.0, 90.0, 3e4], device=dev())
+    N = 16
+    b = torch.cat([z, torch.full((16,), 1.5, device=dev())]) if act == "swiglu" else z
+    x = torch.zeros(2, 8, dtype=torch.bfloat16, device=dev())
+    w = torch.zeros(b.numel(), 8, dtype=torch.bfloat16, device=dev())
+    out = torch.empty(2, N, device=dev())
+    capi.moe_linear(2, N, 8, x, w, b, None, out, None, ACTS.index(act) | F32)
+    h, _, _ = ref.act64(b.double()[None], act, N)
+    # the exponential's argument is off by half a step of z: |z| half steps of the value;
+    # the complement's of GELU by z^2 of them
+    rel = (16 + 2 * z.double().abs() * (1 + z.double().abs().clamp(max=20))) * EPS24
+    assert bool(((out.double() - h).abs() <= rel * h.abs() + 1e-37).all())
+
+
+@pytest.mark.parametrize("T,N", [(1, 8), (3, 72), (5, 512), (64, 520), (130, 1032), (1001, 2824),
+                                 (2500, 40), (4100, 264)])
+@pytest.mark.parametrize("act", ACTS)
+def test_act_grad(capi, T, N, act):
+    g = torch.Generator(device=dev()).manual_seed(T + N)
+    NN = 2 * N if act == "swiglu" else N
+    d, z = rows(g, T, N, 0.02), rows(g, T, NN, 1.5)
+    zb, dz = guarded(T * NN, torch.bfloat16, dev())
+    bb, db = guarded(NN, torch.float32, dev())
+    k = ACTS.index(act)
+    need = capi.moe_linear_act_grad_workspace_bytes(T, N, k)
+    assert 0 < need <= capi.MOE_WORKSPACE_MAX_BYTES
+    wb, ws = workspace(need)
+    on = act != "none"
+    capi.moe_linear_act_grad(T, N, d, z if on else None, dz if on else None, db, k, ws)
+    want = ref.act_grad64(z.double(), d.double(), act, N)
+    # |z| half steps of the exponential's argument and 24 of the rest, of the terms' size
+    mag = ref.act_grad64(z.double().abs(), d.double().abs(), act, N).abs() + want.abs()
+    one = (24 + 2 * z.double().abs() ** 2) * EPS24 * mag if on else 0 * mag
+    if on:
+        off = (dz.view(T, NN).double() - want).abs()
+        assert bool((off <= HALF_BF16 * want.abs() + one + 1e-38).all())
+    tol = (one + (T / 4 + 64) * EPS24 * want.abs()).sum(0) + 1e-38
+    assert bool(((db.double() - want.sum(0)).abs() <= tol).all())
+    assert guard_ok(zb, T * NN) and guard_ok(bb, NN) and bool((wb[need:] == 255).all())
+    if on:  # in place of pre, without the bias
+        capi.moe_linear_act_grad(T, N, d, z, z, None, k)
+        assert torch.equal(z.view(-1), dz)
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_act_grad_far(capi, act):
+    z = torch.tensor([-3e38, -200.0, -104.0, -90.0, -88.5, -87.5, -60.0, -14.0, -6.0, 0.0, 6.0,
+                      14.0, 60.0, 88.5, 200.0, 3e38], device=dev()).to(torch.bfloat16)
+    N = 16
+    p = torch.cat([z, torch.ones_like(z)]) if act == "swiglu" else z
+    d = torch.ones(1, N, dtype=torch.bfloat16, device=dev())
+    dz = torch.empty(1, p.numel(), dtype=torch.bfloat16, device=dev())
+    capi.moe_linear_act_grad(1, N, d, p[None].contiguous(), dz, None, ACTS.index(act))
+    want = ref.act_grad64(p.double()[None], d.double(), act, N)
+    rel = HALF_BF16 + (24 + 4 * z.double().abs().clamp(max=200) ** 2) * EPS24
+    rel = torch.cat([rel, rel]) if act == "swiglu" else rel
+    assert bool(((dz.double() - want).abs() <= rel * want.abs() + 1e-37).all())
+
+
+@pytest.mark.parametrize("T,N,C", SIZES + [(7, 4096, 264), (4100, 72, 136), (1, 1024, 1032)])
+def test_grad(capi, T, N, C):
+    g = torch.Generator(device=dev()).manual_seed(T + N * 5 + C)
+    d, x, w = rows(g, T, N, 0.02), rows(g, T, C), rows(g, N, C, C ** -0.5)
+    xb, dx = guarded(T * C, torch.bfloat16, dev())
+    wb, dw = guarded(N * C, torch.float32, dev())
+    need = capi.moe_linear_grad_workspace_bytes(T, N, C)
+    assert need <= capi.MOE_WORKSPACE_MAX_BYTES
+    sb, ws = workspace(need)
+    capi.moe_linear_grad(T, N, C, d, x, w, dx, dw, ws)
+    want, err = ref.dot_bound(d, w.t())
+    tol = HALF_BF16 * want.abs() + 1.01 * err + 1e-38
+    off = (dx.view(T, C).double() - want).abs() / tol
+    assert float(off.max()) <= 1, (float(off.max()), divmod(int(off.argmax()), C))
+    want, err = ref.dot_bound(d.t(), x.t())
+    off = (dw.view(N, C).double() - want).abs() / (err + 1e-38)
+    assert float(off.max()) <= 1, (float(off.max()), divmod(int(off.argmax()), C))
+    assert guard_ok(xb, T * C) and guard_ok(wb, N * C) and bool((sb[need:] == 255).all())
+    # each alone, and the same bits again
+    dx2, dw2 = torch.empty_like(dx), torch.empty_like(dw)
+    capi.moe_linear_grad(T, N, C, d, None, w, dx2, None, ws)
+    capi.moe_linear_grad(T, N, C, d, x, None, None, dw2, ws)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("T,N,C", [(4100, 264, 3000), (264, 4100 - 4, 3000)])
+def test_grad_large(capi, T, N, C):
+    test_grad(capi, T, N, C)
+
+
+def test_grad_against_differences(capi):
+    """sum(c * out) of the whole epilogue by central differences of the formula."""
+    g = torch.Generator(device=dev()).manual_seed(9)
+    T, N, C = 5, 24, 40
+    x, w, c = rows(g, T, C), rows(g, 2 * N, C, 0.2), rows(g, T, N)
+    out = torch.empty(T, N, dtype=torch.bfloat16, device=dev())
+    pre, dz = (torch.empty(T, 2 * N, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    db = torch.empty(2 * N, device=dev())
+    capi.moe_linear(T, N, C, x, w, None, None, out, pre, 3)
+    ws = torch.empty(capi.MOE_WORKSPACE_MAX_BYTES, dtype=torch.uint8, device=dev())
+    capi.moe_linear_act_grad(T, N, c, pre, dz, db, 3, ws)
+    dx, dw = torch.empty_like(x), torch.empty(2 * N, C, device=dev())
+    capi.moe_linear_grad(T, 2 * N, C, dz, x, w, dx, dw, ws)
+
+    def f(xx, ww):
+        z = xx @ ww.t().contiguous()
+        return (torch.nn.functional.silu(z[:, :N]) * z[:, N:] * c.double()).sum()
+
+    # z and d_z are rounded to bf16 on the way: each term of a sum by 2^-8 and, through the
+    # slopes (at most 1.1 and its change 0.5 |d|), by as much again
+    h = 1e-5
+    mx = (dz.double().abs() @ w.double().abs()) * 4 * HALF_BF16
+    mw = (dz.double().abs().t().contiguous() @ x.double().abs()) * 4 * HALF_BF16
+    for t, i in ((0, 0), (4, 39), (2, 17)):
+        e = torch.zeros(T, C, dtype=torch.float64, device=dev())
+        e[t, i] = h
+        a = float((f(x.double() + e, w.double()) - f(x.double() - e, w.double())) / (2 * h))
+        assert abs(float(dx[t, i]) - a) <= float(mx[t, i]) + HALF_BF16 * abs(a) + 1e-6
+        e = torch.zeros(2 * N, C, dtype=torch.float64, device=dev())
+        e[t * 9, i] = h
+        a = float((f(x.double(), w.double() + e) - f(x.double(), w.double() - e)) / (2 * h))
+        assert abs(float(dw[t * 9, i]) - a) <= float(mw[t * 9, i]) + 1e-6
+
+
+def test_empty(capi):
+    e = torch.empty(0, 16, dtype=torch.bfloat16, device=dev())
+    w = torch.ones(8, 16, dtype=torch.bfloat16, device=dev())
+    o = torch.empty(0, 8, dtype=torch.bfloat16, device=dev())
+    capi.moe_linear(0, 8, 16, e, w, None, None, o)
+    dw, db = torch.full((8, 16), 3.0, device=dev()), torch.full((8,), 3.0, device=dev())
+    capi.moe_linear_grad(0, 8, 16, o, e, w, e, dw)
+    capi.moe_linear_act_grad(0, 8, o, None, None, db)
+    assert bool((dw == 0).all()) and bool((db == 0).all())
