@@ -37,6 +37,11 @@ struct ProductArgs {
 // 32 lanes of a transposing read touch on all banks.
 __device__ __forceinline__ int spread(int k) { return (k & 3) | ((k >> 1) & 4); }
 
+struct Stage {
+  ex_i32x4 buf;
+  uint32_t mask, to;
+};
+
 // How a wave copies its part of an operand's stages: kN copies a stage.
 template <int kRows, int kWaves, bool kAcross, bool kPairs>
 struct StageCopy {
@@ -84,16 +89,15 @@ struct StageCopy {
     base = scalar_u64((uint64_t)(uintptr_t)p + first);
     left = (int64_t)scalar_u64((uint64_t)(bytes - first));
   }
-  // Copies [from, to) of stage s, whose first k is k0 (of k), into buffer b.
-  template <int kFrom, int kTo>
-  __device__ __forceinline__ void run(int s, int k0, int k, int b, bool on) const {
+  // Stage s, whose first k is k0 (of k); none of it is read if it is off.
+  __device__ __forceinline__ Stage stage(int s, int k0, int k, bool on) const {
     const uint64_t at = (uint64_t)s * step;
-    const ex_i32x4 buf = buffer_at(base + at, on ? left - (int64_t)at : 0);
-    // along k: chunks past the last channel are zeros
-    const uint32_t mask = !kAcross && k0 + lane_k >= k ? kOutside : 0u;
-#pragma unroll
-    for (int i = kFrom; i < kTo; ++i)
-      copy16_bounded(buf, off[i] | mask, lds + b * (kRows * 128) + i * (kWaves * 1024));
+    return {buffer_at(base + at, on ? left - (int64_t)at : 0),
+            // along k: chunks past the last channel are zeros
+            !kAcross && k0 + lane_k >= k ? kOutside : 0u, lds + (s & 1) * (kRows * 128)};
+  }
+  __device__ __forceinline__ void copy(const Stage &g, int i) const {
+    copy16_bounded(g.buf, off[i] | g.mask, g.to + i * (kWaves * 1024));
   }
 };
 
@@ -148,8 +152,8 @@ product_kernel(ProductArgs a) {
   cr.init(a.r, row0, a.rows, a.r_ld, a.k, k0, lds_r, 0);
   cc.init(a.c, col0, kPairs ? 2 * (int64_t)a.e.N : a.cols, a.c_ld, a.k, k0, lds_c, a.e.N);
   constexpr int kRN = decltype(cr)::kN, kCN = decltype(cc)::kN;
-  auto copy_rows = [&](int s) { cr.template run<0, kRN>(s, k0 + s * kStep, a.k, s & 1, s < n); };
-  auto copy_cols = [&](int s) { cc.template run<0, kCN>(s, k0 + s * kStep, a.k, s & 1, s < n); };
+  auto rows_of = [&](int s) { return cr.stage(s, k0 + s * kStep, a.k, s < n); };
+  auto cols_of = [&](int s) { return cc.stage(s, k0 + s * kStep, a.k, s < n); };
 
   f32x4 acc[kRT][kCT];
 #pragma unroll
@@ -157,30 +161,69 @@ product_kernel(ProductArgs a) {
 #pragma unroll
     for (int j = 0; j < kCT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  copy_rows(0);
-  copy_cols(0);
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-  lds_barrier();
-  for (int s = 0; s < n; ++s) {
-    copy_rows(s + 1);
-    copy_cols(s + 1);
+  // Half a stage's fragments are read while the other half's are multiplied:
+  // items 0 ... kCT - 1 are the columns', the rest the rows'.
+  constexpr int kItems = kRT + kCT;
+  bf16x8 fr[2][kRT], fc[2][kCT];
+  auto read = [&](int s, int kk, int from, int to) {
     const uint8_t *sr = lds_r[s & 1], *sc = lds_c[s & 1];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8 fr[kRT], fc[kCT];
-#pragma unroll
-      for (int j = 0; j < kCT; ++j) fc[j] = fragment<kC, kCAcross>(sc, wc * kCT + j, kk);
-#pragma unroll
-      for (int i = 0; i < kRT; ++i) fr[i] = fragment<kR, kRAcross>(sr, wr * kRT + i, kk);
-#pragma unroll
-      for (int i = 0; i < kRT; ++i)
-#pragma unroll
-        for (int j = 0; j < kCT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc[j], fr[i], acc[i][j], 0, 0, 0);
+    for (int m = from; m < to; ++m) {
+      if (m < kCT)
+        fc[kk][m] = fragment<kC, kCAcross>(sc, wc * kCT + m, kk);
+      else if (m < kItems)
+        fr[kk][m - kCT] = fragment<kR, kRAcross>(sr, wr * kRT + m - kCT, kk);
     }
-    __builtin_amdgcn_s_waitcnt(0x0f70);
+  };
+  auto multiply = [&](int i, int kk) {
+#pragma unroll
+    for (int j = 0; j < kCT; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc[kk][j], fr[kk][i], acc[i][j], 0, 0, 0);
+  };
+
+  Stage gr = rows_of(0), gc = cols_of(0);
+#pragma unroll
+  for (int i = 0; i < kRN; ++i) cr.copy(gr, i);
+#pragma unroll
+  for (int i = 0; i < kCN; ++i) cc.copy(gc, i);
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  lds_barrier();
+  gr = rows_of(1);
+#pragma unroll
+  for (int i = 0; i < kRN; ++i) cr.copy(gr, i);
+  read(0, 0, 0, kItems);
+  // A stage has two buffers. Its columns' copies are issued in the first half of the
+  // stage before it, its rows' in the last quarter of the one before that, once
+  // every wave has read what was there.
+  constexpr int kHalf = kRT / 2, kLate = kRT - kHalf;
+  for (int s = 0; s < n; ++s) {
+    gc = cols_of(s + 1);
+#pragma unroll
+    for (int i = 0; i < kRT; ++i) {
+      constexpr int kPer = (kItems + kRT - 1) / kRT, kCopy = (kCN + kRT - 1) / kRT;
+      read(s, 1, i * kPer, (i + 1) * kPer);
+#pragma unroll
+      for (int c = i * kCopy; c < (i + 1) * kCopy && c < kCN; ++c) cc.copy(gc, c);
+      multiply(i, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) multiply(i, 1);
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // the next stage has landed
     lds_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    gr = rows_of(s + 2);
+#pragma unroll
+    for (int i = 0; i < kLate; ++i) {
+      constexpr int kPer = (kItems + kLate - 1) / kLate, kCopy = (kRN + kLate - 1) / kLate;
+      read(s + 1, 0, i * kPer, (i + 1) * kPer);
+#pragma unroll
+      for (int c = i * kCopy; c < (i + 1) * kCopy && c < kRN; ++c) cr.copy(gr, c);
+      multiply(kHalf + i, 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // no copy outlives the workgroup
 
   const int l16 = lane & 15, quad = lane >> 4;
 #pragma unroll
@@ -215,6 +258,7 @@ product_kernel(ProductArgs a) {
         if (c < a.e.N) linear_store<kAct>(a.e, t, c, acc[i][j], acc[i][j]);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
