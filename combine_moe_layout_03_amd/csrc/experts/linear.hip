@@ -16,6 +16,9 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
+// s_waitcnt's operand: at most n vector memory operations still out.
+constexpr int vmcnt(int n) { return 0x0f70 | (n & 15) | (n >> 4) << 14; }
+
 constexpr int kStep = 64;  // k of a stage: 128 bytes of a row
 
 struct ProductArgs {
@@ -161,9 +164,20 @@ product_kernel(ProductArgs a) {
 #pragma unroll
     for (int j = 0; j < kCT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // Half a stage's fragments are read while the other half's are multiplied:
-  // items 0 ... kCT - 1 are the columns', the rest the rows'.
-  constexpr int kItems = kRT + kCT;
+  // A stage passes in 2 kRT slots of kCT products: first those of its channels 0-31,
+  // whose fragments were read during the stage before, then those of 32-63, read
+  // in the slots up to kRead. From slot kFree on, behind a barrier, the stage's LDS
+  // is free, and the copies of the stage after next go there: they have more
+  // than a stage's time to land. From slot kNext on, behind another barrier, the next
+  // stage has landed and its first fragments are read. (Items of a read: the columns'
+  // fragments 0 ... kCT - 1, then the rows'.)
+  constexpr int kItems = kRT + kCT, kCopies = kRN + kCN, kSlots = 2 * kRT;
+  constexpr int kRead = kRT * 5 / 8, kFree = kRT * 6 / 8, kNext = kRT * 3 / 2;
+  constexpr int kReadPer = (kItems + kRead - 1) / kRead;
+  constexpr int kNextPer = (kItems + kSlots - kNext - 1) / (kSlots - kNext);
+  constexpr int kCopyPer = 2;
+  static_assert((kSlots - kFree) * kCopyPer >= kCopies, "a stage's copies fit its slots");
+  constexpr int kAhead = (kNext - kFree) * kCopyPer < kCopies ? (kNext - kFree) * kCopyPer : kCopies;
   bf16x8 fr[2][kRT], fc[2][kCT];
   auto read = [&](int s, int kk, int from, int to) {
     const uint8_t *sr = lds_r[s & 1], *sc = lds_c[s & 1];
@@ -175,55 +189,50 @@ product_kernel(ProductArgs a) {
         fr[kk][m - kCT] = fragment<kR, kRAcross>(sr, wr * kRT + m - kCT, kk);
     }
   };
-  auto multiply = [&](int i, int kk) {
-#pragma unroll
-    for (int j = 0; j < kCT; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc[kk][j], fr[kk][i], acc[i][j], 0, 0, 0);
+  auto copy = [&](const Stage &gr, const Stage &gc, int i) {
+    if (i < kRN)
+      cr.copy(gr, i);
+    else if (i < kCopies)
+      cc.copy(gc, i - kRN);
   };
 
-  Stage gr = rows_of(0), gc = cols_of(0);
 #pragma unroll
-  for (int i = 0; i < kRN; ++i) cr.copy(gr, i);
+  for (int s = 0; s < 2; ++s) {
+    const Stage gr = rows_of(s), gc = cols_of(s);
 #pragma unroll
-  for (int i = 0; i < kCN; ++i) cc.copy(gc, i);
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    for (int i = 0; i < kCopies; ++i) copy(gr, gc, i);
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt(kCopies));
   lds_barrier();
-  gr = rows_of(1);
-#pragma unroll
-  for (int i = 0; i < kRN; ++i) cr.copy(gr, i);
   read(0, 0, 0, kItems);
-  // A stage has two buffers. Its columns' copies are issued in the first half of the
-  // stage before it, its rows' in the last quarter of the one before that, once
-  // every wave has read what was there.
-  constexpr int kHalf = kRT / 2, kLate = kRT - kHalf;
   for (int s = 0; s < n; ++s) {
-    gc = cols_of(s + 1);
+    const Stage gr = rows_of(s + 2), gc = cols_of(s + 2);
 #pragma unroll
-    for (int i = 0; i < kRT; ++i) {
-      constexpr int kPer = (kItems + kRT - 1) / kRT, kCopy = (kCN + kRT - 1) / kRT;
-      read(s, 1, i * kPer, (i + 1) * kPer);
+    for (int q = 0; q < kSlots; ++q) {
+      if (q < kRead) read(s, 1, q * kReadPer, (q + 1) * kReadPer);
+      if (q == kFree) {
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (q == kNext) {
+        __builtin_amdgcn_s_waitcnt(vmcnt(kAhead));
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (q >= kNext) read(s + 1, 0, (q - kNext) * kNextPer, (q - kNext + 1) * kNextPer);
+      if (q >= kFree) {
 #pragma unroll
-      for (int c = i * kCopy; c < (i + 1) * kCopy && c < kCN; ++c) cc.copy(gc, c);
-      multiply(i, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+        for (int c = 0; c < kCopyPer; ++c) copy(gr, gc, (q - kFree) * kCopyPer + c);
+      }
+      const int kk = q / kRT, i = q % kRT;
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i) multiply(i, 1);
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // the next stage has landed
-    lds_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    gr = rows_of(s + 2);
-#pragma unroll
-    for (int i = 0; i < kLate; ++i) {
-      constexpr int kPer = (kItems + kLate - 1) / kLate, kCopy = (kRN + kLate - 1) / kLate;
-      read(s + 1, 0, i * kPer, (i + 1) * kPer);
-#pragma unroll
-      for (int c = i * kCopy; c < (i + 1) * kCopy && c < kRN; ++c) cr.copy(gr, c);
-      multiply(kHalf + i, 1);
+      for (int j = 0; j < kCT; ++j)
+        acc[i][j] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc[kk][j], fr[kk][i], acc[i][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // no copy outlives the workgroup
+  __builtin_amdgcn_s_waitcnt(vmcnt(0));  // no copy outlives the workgroup
 
   const int l16 = lane & 15, quad = lane >> 4;
 #pragma unroll
