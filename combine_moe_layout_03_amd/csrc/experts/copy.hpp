@@ -32,6 +32,12 @@ __device__ __forceinline__ void copy16_bounded(ex_i32x4 buf, uint32_t off, uint3
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(scalar_i((int)to)), "v"(off), "s"(buf) : "memory", "m0");
 }
+// The same to LDS byte `to` + kMore, in one instruction less.
+template <int kMore>
+__device__ __forceinline__ void copy16_bounded(ex_i32x4 buf, uint32_t off, uint32_t to) {
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(scalar_i((int)to)), "v"(off), "s"(buf), "i"(kMore) : "memory", "m0", "scc");
+}
 // The same for bytes that nobody reads again: marked to leave L2 first.
 __device__ __forceinline__ void copy16_bounded_once(ex_i32x4 buf, uint32_t off, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"

@@ -10,6 +10,8 @@
 // row of D. Sums are float.
 #include "linear.hpp"
 
+#include <utility>
+
 namespace moe {
 namespace {
 
@@ -18,6 +20,16 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 // s_waitcnt's operand: at most n vector memory operations still out.
 constexpr int vmcnt(int n) { return 0x0f70 | (n & 15) | (n >> 4) << 14; }
+
+// f(0), f(1), ..., f(kN - 1), each number a type of its own.
+template <class F, int... kI>
+__device__ __forceinline__ void each_of(F &f, std::integer_sequence<int, kI...>) {
+  (f(std::integral_constant<int, kI>{}), ...);
+}
+template <int kN, class F>
+__device__ __forceinline__ void each(F f) {
+  each_of(f, std::make_integer_sequence<int, kN>{});
+}
 
 constexpr int kStep = 64;  // k of a stage: 128 bytes of a row
 
@@ -40,15 +52,20 @@ struct ProductArgs {
 // 32 lanes of a transposing read touch on all banks.
 __device__ __forceinline__ int spread(int k) { return (k & 3) | ((k >> 1) & 4); }
 
+constexpr int stage_rows(int rows, bool across) {
+  return !across ? rows : rows > 128 ? 256 : 128;
+}
+
 struct Stage {
   ex_i32x4 buf;
-  uint32_t mask, to;
+  uint32_t to;
 };
 
 // How a wave copies its part of an operand's stages: kN copies a stage.
 template <int kRows, int kWaves, bool kAcross, bool kPairs>
 struct StageCopy {
-  static constexpr int kN = kRows / 8 / kWaves;
+  // (across k a row of the buffer is a power of two wide; what is over is not used)
+  static constexpr int kWide = stage_rows(kRows, kAcross), kN = kWide / 8 / kWaves;
   uint64_t base;  // the tile's first element at the part's first k
   int64_t left;   // bytes from there to the operand's end
   uint32_t step;  // bytes to the next stage
@@ -65,7 +82,7 @@ struct StageCopy {
     const int64_t bytes = (kAcross ? (int64_t)k : rows) * ld * 2;
     int64_t first;
     if (kAcross) {
-      constexpr int kRowBytes = kRows * 2, kPer = 1024 / kRowBytes;
+      constexpr int kRowBytes = kWide * 2, kPer = 1024 / kRowBytes;
       first = ((int64_t)k0 * ld + row0) * 2;
       step = (uint32_t)ld * 2 * kStep;
       lane_k = 0;
@@ -92,15 +109,21 @@ struct StageCopy {
     base = scalar_u64((uint64_t)(uintptr_t)p + first);
     left = (int64_t)scalar_u64((uint64_t)(bytes - first));
   }
-  // Stage s, whose first k is k0 (of k); none of it is read if it is off.
-  __device__ __forceinline__ Stage stage(int s, int k0, int k, bool on) const {
+  // Stage s; nothing of it is read if it is off.
+  __device__ __forceinline__ Stage stage(int s, bool on) const {
     const uint64_t at = (uint64_t)s * step;
-    return {buffer_at(base + at, on ? left - (int64_t)at : 0),
-            // along k: chunks past the last channel are zeros
-            !kAcross && k0 + lane_k >= k ? kOutside : 0u, lds + (s & 1) * (kRows * 128)};
+    return {buffer_at(base + at, on ? left - (int64_t)at : 0), lds + (s & 1) * (kWide * 128)};
   }
-  __device__ __forceinline__ void copy(const Stage &g, int i) const {
-    copy16_bounded(g.buf, off[i] | g.mask, g.to + i * (kWaves * 1024));
+  // Before the copies of a stage in which only `rest` channels are left, the last:
+  // along k, chunks past them become zeros.
+  __device__ __forceinline__ void cut(int rest) {
+    if (kAcross) return;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) off[i] = lane_k >= rest ? kOutside : off[i];
+  }
+  template <int kI>
+  __device__ __forceinline__ void copy(const Stage &g) const {
+    copy16_bounded<kI * kWaves * 1024>(g.buf, off[kI], g.to);
   }
 };
 
@@ -109,7 +132,7 @@ template <int kRows, bool kAcross>
 __device__ __forceinline__ bf16x8 fragment(const uint8_t *stage, int t, int kk) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, quad = lane >> 4;
   if (kAcross) {
-    constexpr int kRowBytes = kRows * 2;
+    constexpr int kRowBytes = stage_rows(kRows, true) * 2;
     const int kr = kk * 32 + quad * 8 + (l16 >> 2);
     const int at = kr * kRowBytes + ((t ^ spread(kr)) << 5) + (l16 & 3) * 8;
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -123,13 +146,26 @@ __device__ __forceinline__ bf16x8 fragment(const uint8_t *stage, int t, int kk) 
   }
 }
 
-// kRW x kCW waves, each with kRT x kCT fragments of 16.
-template <int kRW, int kCW, int kRT, int kCT, bool kRAcross, bool kCAcross, int kAct>
-__global__ __launch_bounds__(kRW *kCW * 64, kRW *kCW == 4 && kRT * kCT > 32 ? 1 : 2) void
-product_kernel(ProductArgs a) {
+// acc += C R^T of 16 x 16 x 32. In asm, because the compiler, left to place 512
+// registers, moves sums and fragments to and fro between the two files (dw of 8192 x
+// 4096 x 7168: 461 us, with the sums held in the accumulation registers 389). It
+// still waits for the fragments it reads; that the sums are ready, products_done()
+// sees to (a product takes 8 passes of four clocks).
+__device__ __forceinline__ void product(f32x4 &acc, bf16x8 c, bf16x8 r) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(c), "v"(r));
+}
+__device__ __forceinline__ void products_done() {
+  asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+}
+
+// 2 x 2 waves, each with kRT x kCT fragments of 16.
+template <int kRT, int kCT, bool kRAcross, bool kCAcross, int kAct>
+__global__ __launch_bounds__(256, kRT * kCT > 32 ? 1 : 2) void product_kernel(ProductArgs a) {
+  constexpr int kRW = 2, kCW = 2;
   constexpr int kWaves = kRW * kCW, kR = kRW * kRT * 16, kC = kCW * kCT * 16;
   constexpr bool kPairs = kAct == kActSwiglu;
-  __shared__ __align__(1024) uint8_t lds_r[2][kR * 128], lds_c[2][kC * 128];
+  __shared__ __align__(1024) uint8_t lds_r[2][stage_rows(kR, kRAcross) * 128],
+      lds_c[2][stage_rows(kC, kCAcross) * 128];
   // Workgroup b runs on XCD b % 8: every XCD takes a run of neighbouring tiles,
   // four tiles high, which share operands in its L2.
   const int row_units = (a.rows + kR - 1) / kR, tiles = row_units * a.col_units;
@@ -155,84 +191,83 @@ product_kernel(ProductArgs a) {
   cr.init(a.r, row0, a.rows, a.r_ld, a.k, k0, lds_r, 0);
   cc.init(a.c, col0, kPairs ? 2 * (int64_t)a.e.N : a.cols, a.c_ld, a.k, k0, lds_c, a.e.N);
   constexpr int kRN = decltype(cr)::kN, kCN = decltype(cc)::kN;
-  auto rows_of = [&](int s) { return cr.stage(s, k0 + s * kStep, a.k, s < n); };
-  auto cols_of = [&](int s) { return cc.stage(s, k0 + s * kStep, a.k, s < n); };
-
   f32x4 acc[kRT][kCT];
 #pragma unroll
   for (int i = 0; i < kRT; ++i)
 #pragma unroll
     for (int j = 0; j < kCT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // A stage passes in 2 kRT slots of kCT products: first those of its channels 0-31,
-  // whose fragments were read during the stage before, then those of 32-63, read
-  // in the slots up to kRead. From slot kFree on, behind a barrier, the stage's LDS
-  // is free, and the copies of the stage after next go there: they have more
-  // than a stage's time to land. From slot kNext on, behind another barrier, the next
-  // stage has landed and its first fragments are read. (Items of a read: the columns'
-  // fragments 0 ... kCT - 1, then the rows'.)
-  constexpr int kItems = kRT + kCT, kCopies = kRN + kCN, kSlots = 2 * kRT;
-  constexpr int kRead = kRT * 5 / 8, kFree = kRT * 6 / 8, kNext = kRT * 3 / 2;
-  constexpr int kReadPer = (kItems + kRead - 1) / kRead;
-  constexpr int kNextPer = (kItems + kSlots - kNext - 1) / (kSlots - kNext);
-  constexpr int kCopyPer = 2;
-  static_assert((kSlots - kFree) * kCopyPer >= kCopies, "a stage's copies fit its slots");
-  constexpr int kAhead = (kNext - kFree) * kCopyPer < kCopies ? (kNext - kFree) * kCopyPer : kCopies;
+  // A stage is 2 kRT kCT products: first those of its channels 0-31, whose
+  // fragments were read during the stage before, then those of 32-63, read behind
+  // the first products. From product kFree on, behind a barrier, the stage's LDS is
+  // free, and the copies of the stage after next go there: they have more than a
+  // stage's time to land. From kNext on, behind another barrier, the next stage has
+  // landed and its first fragments are read. A wave has its SIMD to itself and
+  // issues about three instructions while a product runs, so reads and copies stand
+  // one by one between the products.
+  constexpr int kItems = kRT + kCT, kCopies = kRN + kCN, kTotal = 2 * kRT * kCT;
+  constexpr int kFree = kTotal * 3 / 8, kNext = kTotal * 3 / 4;
+  constexpr int kReadEvery = kFree * 5 / 6 / kItems, kNextEvery = (kTotal - kNext) / kItems < 2 ? 1 : (kTotal - kNext) * 3 / 4 / kItems;
+  constexpr int kCopyEvery = (kTotal - kFree) / kCopies;
+  static_assert(kReadEvery > 0 && kNextEvery > 0 && kCopyEvery > 0, "a place for each");
+  constexpr int kEarly = (kNext - kFree + kCopyEvery - 1) / kCopyEvery;
+  constexpr int kAhead = kEarly < kCopies ? kEarly : kCopies;
   bf16x8 fr[2][kRT], fc[2][kCT];
-  auto read = [&](int s, int kk, int from, int to) {
-    const uint8_t *sr = lds_r[s & 1], *sc = lds_c[s & 1];
-#pragma unroll
-    for (int m = from; m < to; ++m) {
-      if (m < kCT)
-        fc[kk][m] = fragment<kC, kCAcross>(sc, wc * kCT + m, kk);
-      else if (m < kItems)
-        fr[kk][m - kCT] = fragment<kR, kRAcross>(sr, wr * kRT + m - kCT, kk);
+  // item m: the columns' fragments 0 ... kCT - 1, then the rows'
+  auto read = [&](int s, int kk, int m) {
+    if (m < kCT)
+      fc[kk][m] = fragment<kC, kCAcross>(lds_c[s & 1], wc * kCT + m, kk);
+    else
+      fr[kk][m - kCT] = fragment<kR, kRAcross>(lds_r[s & 1], wr * kRT + m - kCT, kk);
+  };
+  auto copy = [&](const Stage &gr, const Stage &gc, auto i) {
+    if constexpr (i.value < kRN)
+      cr.template copy<i.value>(gr);
+    else
+      cc.template copy<i.value - kRN>(gc);
+  };
+  const int rest = a.k - k0 - (n - 1) * kStep;  // channels of the last stage, or more
+  auto cut_at = [&](int s) {
+    if (s == n - 1 && rest < kStep) {
+      cr.cut(rest);
+      cc.cut(rest);
     }
   };
-  auto copy = [&](const Stage &gr, const Stage &gc, int i) {
-    if (i < kRN)
-      cr.copy(gr, i);
-    else if (i < kCopies)
-      cc.copy(gc, i - kRN);
-  };
 
-#pragma unroll
   for (int s = 0; s < 2; ++s) {
-    const Stage gr = rows_of(s), gc = cols_of(s);
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) copy(gr, gc, i);
+    cut_at(s);
+    const Stage gr = cr.stage(s, s < n), gc = cc.stage(s, s < n);
+    each<kCopies>([&](auto i) { copy(gr, gc, i); });
   }
   __builtin_amdgcn_s_waitcnt(vmcnt(kCopies));
   lds_barrier();
-  read(0, 0, 0, kItems);
-  for (int s = 0; s < n; ++s) {
-    const Stage gr = rows_of(s + 2), gc = cols_of(s + 2);
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) {
-      if (q < kRead) read(s, 1, q * kReadPer, (q + 1) * kReadPer);
-      if (q == kFree) {
+  for (int m = 0; m < kItems; ++m) read(0, 0, m);
+  for (int s = 0; s < n; ++s) {
+    Stage gr, gc;
+    each<kTotal>([&](auto at) {
+      constexpr int p = at.value, kk = p / (kRT * kCT), i = p / kCT % kRT, j = p % kCT;
+      if constexpr (p == kFree) {
         lds_barrier();
-        __builtin_amdgcn_sched_barrier(0);
+        cut_at(s + 2);
       }
-      if (q == kNext) {
+      if constexpr (p == kNext) {
         __builtin_amdgcn_s_waitcnt(vmcnt(kAhead));
         lds_barrier();
-        __builtin_amdgcn_sched_barrier(0);
       }
-      if (q >= kNext) read(s + 1, 0, (q - kNext) * kNextPer, (q - kNext + 1) * kNextPer);
-      if (q >= kFree) {
-#pragma unroll
-        for (int c = 0; c < kCopyPer; ++c) copy(gr, gc, (q - kFree) * kCopyPer + c);
-      }
-      const int kk = q / kRT, i = q % kRT;
-#pragma unroll
-      for (int j = 0; j < kCT; ++j)
-        acc[i][j] =
-            __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc[kk][j], fr[kk][i], acc[i][j], 0, 0, 0);
+      product(acc[i][j], fc[kk][j], fr[kk][i]);
+      if constexpr (p % kReadEvery == 0 && p / kReadEvery < kItems) read(s, 1, p / kReadEvery);
+      if constexpr (p == kFree / 2) gr = cr.stage(s + 2, s + 2 < n);
+      if constexpr (p == kFree * 3 / 4) gc = cc.stage(s + 2, s + 2 < n);
+      if constexpr (p >= kFree && (p - kFree) % kCopyEvery == 0 && (p - kFree) / kCopyEvery < kCopies)
+        copy(gr, gc, std::integral_constant<int, (p - kFree) / kCopyEvery>{});
+      if constexpr (p >= kNext && (p - kNext) % kNextEvery == 0 && (p - kNext) / kNextEvery < kItems)
+        read(s + 1, 0, (p - kNext) / kNextEvery);
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
   }
   __builtin_amdgcn_s_waitcnt(vmcnt(0));  // no copy outlives the workgroup
+  products_done();
 
   const int l16 = lane & 15, quad = lane >> 4;
 #pragma unroll
@@ -292,20 +327,36 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
 }
 
 struct Plan {
-  int tile;         // rows and columns of a tile: 256 or 128
+  int high, wide;     // fragments of 16 a wave has: tiles of 32 high x 32 wide
   int splits, steps;  // parts of k and their stages
 };
 
-// Tiles of 256 x 256 where they fill the chip, else of 128 x 128; too few of
-// those to fill it, k is split as far as that leaves a part eight stages.
-Plan plan(int64_t rows, int64_t cols, int64_t k) {
-  auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((cols + t - 1) / t); };
+// The tile whose rounds over the 256 CUs take the least, in units of 22 ns, what a
+// wave takes for a fragment's products of a stage: starting and storing a tile takes
+// 11 us, eight stages of a large one.
+Plan plan(int64_t rows, int64_t cols, int64_t k, bool pairs) {
   const int64_t steps = (k + kStep - 1) / kStep;
-  Plan p{256, 1, (int)steps};
-  if (tiles(256) >= 192) return p;
-  p.tile = 128;
-  const int64_t n = tiles(128);
-  int64_t s = 512 / n;
+  auto tiles = [&](int64_t h, int64_t w) {
+    return ((rows + 32 * h - 1) / (32 * h)) * ((cols + 32 * w - 1) / (32 * w));
+  };
+  Plan p{8, 8, 1, (int)steps};
+  double best = 0;
+  for (int w = 8; w >= 6; w -= pairs ? 2 : 1) {  // (a wave has both halves of its pairs)
+    const double t = (double)((tiles(8, w) + 255) / 256) * (8 * w * steps + 520);
+    if (w == 8 || t < best) {
+      best = t;
+      p.wide = w;
+    }
+  }
+  // Small tiles, two to a CU: half a microsecond a stage alone, 0.8 beside another;
+  // a large one's stage takes 1.4. Parts of k, written and read again, only
+  // where there are tiles for at most half the CUs.
+  const int64_t n = tiles(4, 4), last = n % 512;
+  const double small = (double)(n / 512) * (36 * steps + 128) +
+                       (last == 0 ? 0.0 : last <= 256 ? 23 * steps + 128 : 36 * steps + 128);
+  if (best <= small) return p;
+  p.high = p.wide = 4;
+  int64_t s = 256 / n;
   if (s > steps / 8) s = steps / 8;
   const int64_t fit = kMaxWorkspace / 4 / (rows * cols);
   if (s > fit) s = fit;
@@ -320,18 +371,21 @@ template <bool kRAcross, bool kCAcross, int kAct>
 hipError_t launch_product(ProductArgs a, hipStream_t s) {
   const int64_t cols = kAct == kActSwiglu ? 2 * (int64_t)a.e.N : a.e.N;
   a.cols = (int32_t)cols;
-  const Plan p = plan(a.rows, cols, a.k);
-  a.col_units = (int32_t)((cols + p.tile - 1) / p.tile);
+  const Plan p = plan(a.rows, cols, a.k, kAct == kActSwiglu);
+  a.col_units = (int32_t)((cols + 32 * p.wide - 1) / (32 * p.wide));
   a.splits = p.splits;
   a.split_steps = p.steps;
-  const int64_t units = (int64_t)a.col_units * ((a.rows + p.tile - 1) / p.tile) * p.splits;
-  const dim3 grid((unsigned)((units + 7) / 8 * 8));
-  if (p.tile == 256)
-    hipLaunchKernelGGL((product_kernel<2, 2, 8, 8, kRAcross, kCAcross, kAct>), grid, dim3(256), 0,
-                       s, a);
-  else
-    hipLaunchKernelGGL((product_kernel<2, 2, 4, 4, kRAcross, kCAcross, kAct>), grid, dim3(256), 0,
-                       s, a);
+  const int64_t units = (int64_t)a.col_units * ((a.rows + 32 * p.high - 1) / (32 * p.high)) * p.splits;
+  const dim3 grid((unsigned)((units + 7) / 8 * 8)), block(256);
+  if (p.high == 4)
+    hipLaunchKernelGGL((product_kernel<4, 4, kRAcross, kCAcross, kAct>), grid, block, 0, s, a);
+  else if (p.wide == 8)
+    hipLaunchKernelGGL((product_kernel<8, 8, kRAcross, kCAcross, kAct>), grid, block, 0, s, a);
+  else if (p.wide == 7) {
+    if constexpr (kAct != kActSwiglu)
+      hipLaunchKernelGGL((product_kernel<8, 7, kRAcross, kCAcross, kAct>), grid, block, 0, s, a);
+  } else
+    hipLaunchKernelGGL((product_kernel<8, 6, kRAcross, kCAcross, kAct>), grid, block, 0, s, a);
   if (p.splits > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -342,16 +396,17 @@ hipError_t launch_product(ProductArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
-size_t plan_bytes(int64_t rows, int64_t cols, int64_t k) {
+size_t plan_bytes(int64_t rows, int64_t cols, int64_t k, bool pairs = false) {
   if (rows == 0) return 0;
-  const Plan p = plan(rows, cols, k);
+  const Plan p = plan(rows, cols, k, pairs);
   return p.splits > 1 ? (size_t)(p.splits * rows * cols * 4) : 0;
 }
 
 }  // namespace
 
 size_t linear_workspace(int32_t T, int32_t N, int32_t C, int32_t act) {
-  return plan_bytes(T, act == kActSwiglu ? 2 * (int64_t)N : N, C);
+  const bool pairs = act == kActSwiglu;
+  return plan_bytes(T, pairs ? 2 * (int64_t)N : N, C, pairs);
 }
 size_t linear_grad_workspace(int32_t T, int32_t N, int32_t C) {
   const size_t x = plan_bytes(T, C, N), w = plan_bytes(N, C, T);
