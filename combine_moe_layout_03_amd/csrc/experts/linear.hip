@@ -326,6 +326,88 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
   linear_store<kAct>(a.e, t, n, z, up);
 }
 
+// ---- stream: few rows -----------------------------------------------------------
+//
+// Few rows make this a read of the weights. A workgroup takes kW rows of them (SwiGLU:
+// half of them gates) and 16 tokens; its waves share the channels out in groups of
+// 64, each through a ring of groups in its own part of LDS, without a barrier, and
+// join their sums at the end.
+
+constexpr int kStreamWaves = 4, kStreamRing = 4;
+
+template <int kW, int kAct>
+__global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(ProductArgs a) {
+  constexpr bool kPairs = kAct == kActSwiglu;
+  constexpr int kOut = kPairs ? kW / 2 : kW, kCopies = 2 + kW / 8, kRows = 16 + kW;
+  constexpr int kPitch = 20;  // floats of a token's sums
+  // (with kW = 8 the instruction's other weight rows are what stands behind the group)
+  __shared__ __align__(1024) uint8_t ring[kStreamWaves * kStreamRing * kRows * 128 + 1024];
+  static_assert(16 * kPitch * 4 <= kStreamRing * kRows * 128, "sums replace a wave's ring");
+  const int lane = threadIdx.x & 63, wave = scalar_i(threadIdx.x >> 6);
+  const int l16 = lane & 15, quad = lane >> 4;
+  const int tb = scalar_i((uint32_t)blockIdx.x / (uint32_t)a.col_units);
+  const int n0 = ((int)blockIdx.x - tb * a.col_units) * kOut, t0 = tb * 16;
+  const int64_t ld = (int64_t)a.c_ld * 2;  // bytes of a row, of both operands
+  const ex_i32x4 wbuf = buffer_at(scalar_u64((uint64_t)(uintptr_t)a.c + n0 * ld),
+                                  (int64_t)scalar_u64((uint64_t)((a.cols - n0) * ld)));
+  const ex_i32x4 tbuf = buffer_at(scalar_u64((uint64_t)(uintptr_t)a.r + t0 * ld),
+                                  (int64_t)scalar_u64((uint64_t)((a.rows - t0) * ld)));
+  const int chunk = (lane & 7) ^ (lane >> 3), row = lane >> 3;
+  uint32_t w_off[kW / 8], t_off[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = i * 8 + row;
+    t_off[i] = (uint32_t)r * (uint32_t)ld + chunk * 16;
+    if (i < kW / 8)
+      w_off[i] = (uint32_t)(kPairs && r >= kOut ? a.e.N + r - kOut : r) * (uint32_t)ld + chunk * 16;
+  }
+  const int groups = (a.k + kStep - 1) / kStep;
+  uint8_t *const mine = ring + wave * (kStreamRing * kRows * 128);
+  const uint32_t lds = lds_offset(mine);
+  auto issue = [&](int g, int slot) {  // groups past the last, and chunks, arrive as zeros
+    const uint32_t more = (uint32_t)g * 128, mask = g * kStep + chunk * 8 < a.k ? 0u : kOutside;
+    const uint32_t to = lds + slot * (kRows * 128);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) copy16_bounded(tbuf, (t_off[i] + more) | mask, to + i * 1024);
+#pragma unroll
+    for (int i = 0; i < kW / 8; ++i)
+      copy16_bounded_once(wbuf, (w_off[i] + more) | mask, to + 2048 + i * 1024);
+  };
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kStreamRing - 1; ++i) issue(wave + i * kStreamWaves, i);
+  int slot = 0;
+  for (int g = wave; g < groups; g += kStreamWaves) {
+    issue(g + (kStreamRing - 1) * kStreamWaves, (slot + kStreamRing - 1) % kStreamRing);
+    __builtin_amdgcn_s_waitcnt(vmcnt((kStreamRing - 1) * kCopies));
+    asm volatile("" ::: "memory");
+    const uint8_t *st = mine + slot * (kRows * 128);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fragment<16, false>(st, 1, kk),
+                                                    fragment<16, false>(st, 0, kk), acc, 0, 0, 0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the slot is read, and free
+    asm volatile("" ::: "memory");
+    slot = (slot + 1) % kStreamRing;
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt(0));  // also the zeros have landed
+  lds_barrier();                         // and with kW = 8 a ring is read up into the next
+  *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(mine) + l16 * kPitch + quad * 4) = acc;
+  lds_barrier();
+  constexpr int kQuads = kOut / 4;
+  if (threadIdx.x >= 16 * kQuads) return;
+  const int t = threadIdx.x / kQuads, n = threadIdx.x % kQuads * 4;
+  f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f}, up = z;
+#pragma unroll
+  for (int w = 0; w < kStreamWaves; ++w) {
+    const float *p =
+        reinterpret_cast<const float *>(ring + w * (kStreamRing * kRows * 128)) + t * kPitch + n;
+    z += *reinterpret_cast<const f32x4 *>(p);
+    if (kPairs) up += *reinterpret_cast<const f32x4 *>(p + kOut);
+  }
+  if (t0 + t < a.rows && n0 + n < a.e.N) linear_store<kAct>(a.e, t0 + t, n0 + n, z, up);
+}
+
 struct Plan {
   int high, wide;     // fragments of 16 a wave has: tiles of 32 high x 32 wide
   int splits, steps;  // parts of k and their stages
@@ -367,6 +449,37 @@ Plan plan(int64_t rows, int64_t cols, int64_t k, bool pairs) {
   return p;
 }
 
+// Whether a product is streamed, its rows in blocks of 16 that each read the weights
+// again: with one block always; with more while all that is read is less than 2.75
+// million channels of 32 rows. (At 7168 channels, streamed against tiles: 256 units of
+// 16 x 16 8.4 against 13.6 us, 512 units 17.3 against 14 to 16; at 1024 channels 512
+// units 4.1 against 9.9.) The second half of a SwiGLU's weights has to be within
+// reach of a 32-bit offset.
+bool streamed(int64_t rows, int64_t N, int64_t k, bool pairs) {
+  if (pairs && (N + 16) * k * 2 >= 0xffffffe0ll) return false;
+  const int64_t units = (rows + 15) / 16 * ((N * (pairs ? 2 : 1) + 15) / 16);
+  return rows <= 16 || units * k <= 2750000;
+}
+
+template <int kW, int kAct>
+hipError_t launch_stream(ProductArgs a, hipStream_t s) {
+  constexpr int kOut = kAct == kActSwiglu ? kW / 2 : kW;
+  a.cols = kAct == kActSwiglu ? 2 * a.e.N : a.e.N;
+  a.col_units = (a.e.N + kOut - 1) / kOut;
+  hipLaunchKernelGGL((stream_kernel<kW, kAct>),
+                     dim3((unsigned)(a.col_units * ((a.rows + 15) / 16))),
+                     dim3(kStreamWaves * 64), 0, s, a);
+  return hipGetLastError();
+}
+
+// Eight weight rows a workgroup where sixteen leave CUs without one.
+template <int kAct>
+hipError_t launch_streamed(const ProductArgs &a, hipStream_t s) {
+  const int64_t rows = (a.rows + 15) / 16, w = kAct == kActSwiglu ? 2 * (int64_t)a.e.N : a.e.N;
+  return rows * ((w + 15) / 16) < 256 ? launch_stream<8, kAct>(a, s)
+                                      : launch_stream<16, kAct>(a, s);
+}
+
 template <bool kRAcross, bool kCAcross, int kAct>
 hipError_t launch_product(ProductArgs a, hipStream_t s) {
   const int64_t cols = kAct == kActSwiglu ? 2 * (int64_t)a.e.N : a.e.N;
@@ -406,6 +519,7 @@ size_t plan_bytes(int64_t rows, int64_t cols, int64_t k, bool pairs = false) {
 
 size_t linear_workspace(int32_t T, int32_t N, int32_t C, int32_t act) {
   const bool pairs = act == kActSwiglu;
+  if (streamed(T, N, C, pairs)) return 0;
   return plan_bytes(T, pairs ? 2 * (int64_t)N : N, C, pairs);
 }
 size_t linear_grad_workspace(int32_t T, int32_t N, int32_t C) {
@@ -417,6 +531,14 @@ hipError_t launch_linear(int32_t T, int32_t N, int32_t C, const uint16_t *x, con
                          const float *bias, const uint16_t *residual, void *out, uint16_t *pre,
                          int32_t act, bool f32, float *ws, hipStream_t s) {
   ProductArgs a{x, w, T, 0, C, C, C, 0, 1, 0, ws, {bias, residual, out, pre, N, f32}};
+  if (streamed(T, N, C, act == kActSwiglu)) {
+    switch (act) {
+      case kActNone: return launch_streamed<kActNone>(a, s);
+      case kActSilu: return launch_streamed<kActSilu>(a, s);
+      case kActGelu: return launch_streamed<kActGelu>(a, s);
+      default: return launch_streamed<kActSwiglu>(a, s);
+    }
+  }
   switch (act) {
     case kActNone: return launch_product<false, false, kActNone>(a, s);
     case kActSilu: return launch_product<false, false, kActSilu>(a, s);
