@@ -7,6 +7,8 @@
 // order wrongly by its rounding, still rank as they stand.
 #include "gate.hpp"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -21,16 +23,35 @@ __device__ __forceinline__ double key_choice(uint64_t k) {
   return __longlong_as_double(u ^ (int64_t)((uint64_t)~(u >> 63) | 0x8000000000000000ull));
 }
 
+// The high words' maximum, then the low ones' among those that have it.
 __device__ __forceinline__ uint64_t wave_max_u64(uint64_t m) {
-  for (int d = 32; d; d >>= 1) {
-    const uint64_t o = (uint64_t)__shfl_xor((unsigned long long)m, d);
-    m = o > m ? o : m;
-  }
-  return m;
+  const uint32_t hi = wave_max_u((uint32_t)(m >> 32));
+  const uint32_t lo = wave_max_u((uint32_t)(m >> 32) == hi ? (uint32_t)m : 0u);
+  return (uint64_t)hi << 32 | lo;
+}
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kCtrl, 0xf, 0xf, false);
+}
+template <int kCtrl>
+__device__ __forceinline__ double dpp_d(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x);
+  return __longlong_as_double((int64_t)((uint64_t)dpp_u<kCtrl>((uint32_t)u) |
+                                        (uint64_t)dpp_u<kCtrl>((uint32_t)(u >> 32)) << 32));
+}
+__device__ __forceinline__ double lane_d(double x, int lane) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x);
+  return __longlong_as_double(
+      (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane) |
+                (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane)
+                    << 32));
 }
 __device__ __forceinline__ double wave_sum_d(double x) {
-  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
-  return x;
+  x += dpp_d<0x128>(x);
+  x += dpp_d<0x124>(x);
+  x += dpp_d<0x122>(x);
+  x += dpp_d<0x121>(x);
+  return (lane_d(x, 0) + lane_d(x, 16)) + (lane_d(x, 32) + lane_d(x, 48));
 }
 
 struct GroupArgs {
@@ -44,68 +65,72 @@ struct GroupArgs {
   int32_t *status;
 };
 
+// What a choice is compared by: the logit itself without a bias (as moe_gate
+// compares), else score + bias as a double.
+//
+// One token, in one wave: expert e = lane + 64 * j in register j, choices as doubles.
+// `choices` is LDS of 64 V keys of the wave's own.
 template <int V, int kMode>
-__global__ __launch_bounds__(256) void gate_grouped_kernel(GroupArgs a) {
+__device__ void exact_token(const GroupArgs &a, int t, uint64_t *choices, bool *bad) {
   constexpr bool kSig = kMode & kGateSigmoid;
-  __shared__ uint64_t choices[4][V * 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + wave));
-  if (t >= a.T) return;
+  const int lane = threadIdx.x & 63;
   const int E = a.E;
-  bool bad = false;
   float x[V];
   gate_row<V>(a.x, (int64_t)t * E, E, a.bf16, x);
   uint64_t key[V];
   uint32_t top_key = 0;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const uint32_t k = gate_key(x[j], &bad);
+    const uint32_t k = gate_key(x[j], bad);
     x[j] = lane + 64 * j < E && k ? key_logit(k) : -INFINITY;
     top_key = umax32(top_key, lane + 64 * j < E ? k : 0u);
   }
   top_key = wave_max_u(top_key);
   const float top = top_key ? key_logit(top_key) : 0.0f;
+  const bool scores = a.bias || (a.sum2 && a.G > 1) || !(kMode & (kGateSigmoid | kGateRenorm));
   double sum = 1.0;
   double p[V];
+  if (scores) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) p[j] = exp(kSig ? -(double)x[j] : (double)x[j] - (double)top);
-  if (kSig) {
+    for (int j = 0; j < V; ++j) p[j] = exp(kSig ? -(double)x[j] : (double)x[j] - (double)top);
+    if (kSig) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) p[j] = 1.0 / (1.0 + p[j]);
-  } else {
-    double s = 0.0;
+      for (int j = 0; j < V; ++j) p[j] = 1.0 / (1.0 + p[j]);
+    } else {
+      double s = 0.0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) s += p[j];
-    sum = wave_sum_d(s);
+      for (int j = 0; j < V; ++j) s += p[j];
+      sum = wave_sum_d(s);
 #pragma unroll
-    for (int j = 0; j < V; ++j) p[j] /= sum;
+      for (int j = 0; j < V; ++j) p[j] /= sum;
+    }
   }
-  bool bad_bias = false;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     bool ok = x[j] != -INFINITY;
-    double c = p[j];
+    double c = x[j];
     if (a.bias) {
       const float b = a.bias[min(lane + 64 * j, E - 1)];
-      bool bb = false;
-      if (gate_key(b, &bb) == 0) ok = false;
-      bad_bias = bad_bias || bb;
-      c += (double)b;
+      if (gate_key(b, bad) == 0) ok = false;
+      c = p[j] + (double)b;
     }
     key[j] = ok ? choice_key(c) : kNone;
   }
   if (a.G > 1) {
     const int n = E / a.G;
+    const bool by_score = a.sum2 && !a.bias;  // the groups' keys differ from the choices'
 #pragma unroll
-    for (int j = 0; j < V; ++j) choices[wave][lane + 64 * j] = key[j];
+    for (int j = 0; j < V; ++j)
+      choices[lane + 64 * j] = by_score && key[j] != kNone ? choice_key(p[j]) : key[j];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
     // lane g: group g
     uint64_t group = kNone;
     if (lane < a.G) {
       uint64_t k1 = kNone, k2 = kNone;
+#pragma unroll 8
       for (int i = 0; i < n; ++i) {
-        const uint64_t k = choices[wave][lane * n + i];
+        const uint64_t k = choices[lane * n + i];
         const uint64_t lo = k < k1 ? k : k1;
         k1 = k > k1 ? k : k1;
         k2 = lo > k2 ? lo : k2;
@@ -113,6 +138,7 @@ __global__ __launch_bounds__(256) void gate_grouped_kernel(GroupArgs a) {
       group = k1;
       if (a.sum2 && k2 != kNone) group = choice_key(key_choice(k1) + key_choice(k2));
     }
+    __builtin_amdgcn_wave_barrier();
     uint64_t kept = 0;
     for (int k = 0; k < a.KG; ++k) {
       const uint64_t m = wave_max_u64(group);
@@ -167,7 +193,300 @@ __global__ __launch_bounds__(256) void gate_grouped_kernel(GroupArgs a) {
     a.idx[o] = my_id;
     a.w[o] = my_id < 0 ? 0.0f : s * a.scale;
   }
-  if (a.status && __ballot(bad || bad_bias) && lane == 0) atomicOr(a.status, kStBadLogit);
+}
+
+template <int V, int kMode>
+__global__ __launch_bounds__(256) void gate_grouped_kernel(GroupArgs a) {
+  __shared__ uint64_t choices[4][V * 64];
+  const int wave = threadIdx.x >> 6;
+  const int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + wave));
+  if (t >= a.T) return;
+  bool bad = false;
+  exact_token<V, kMode>(a, t, choices[wave], &bad);
+  if (a.status && __ballot(bad) && (threadIdx.x & 63) == 0) atomicOr(a.status, kStBadLogit);
+}
+
+// ---- four tokens a wave -----------------------------------------------------------
+//
+// A token has the 16 lanes of a DPP row, lane c the experts c V ... c V + V - 1, so that
+// maxima over a token's lanes are four steps for four tokens, and a group is a run of
+// L lanes. Choices are floats here, and their keys give up their lowest bits to the
+// expert's place in its lane. That orders all but neighbours closer than `near`: the
+// exact order of those is settled among the token's 16 best candidates, one a
+// lane, by their doubles; and where that does not reach (groups too close, more
+// candidates within reach, a softmax's bias) the token is done again by exact_token.
+
+__device__ __forceinline__ float row_sum16(float x) {
+  x += dpp_f<0x128>(x);
+  x += dpp_f<0x124>(x);
+  x += dpp_f<0x122>(x);
+  return x + dpp_f<0x121>(x);
+}
+__device__ __forceinline__ float row_max16(float x) {
+  x = fmaxf(x, dpp_f<0x128>(x));
+  x = fmaxf(x, dpp_f<0x124>(x));
+  x = fmaxf(x, dpp_f<0x122>(x));
+  return fmaxf(x, dpp_f<0x121>(x));
+}
+
+// How close two choices, rounded and without the places in their keys, may be to
+// be told apart: 2^-21 for a score (its exponential's argument and result, the sum
+// and the quotient, at slopes of at most 1/4; a softmax's sum of 256 terms is common
+// to both), 2^-24 of the sum with the bias, 2^-19 for the place, twice each and
+// twice that. Logits are as they stand: equal but for the places.
+__device__ __forceinline__ float near(float c, bool exact, float largest_score) {
+  return exact ? 0.0f : 0x1p-18f * largest_score + 0x1p-17f * fabsf(c);
+}
+
+// The best two of the L lanes of a group, in all of them.
+template <int kCtrl>
+__device__ __forceinline__ void best_two(float &m1, float &m2) {
+  const float o1 = dpp_f<kCtrl>(m1), o2 = dpp_f<kCtrl>(m2);
+  m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+  m1 = fmaxf(m1, o1);
+}
+
+// How many groups of the row score more than the lane's by more than tol, and by
+// more than -tol; of equal ones the first scores more.
+template <int L, int kStart = L>
+__device__ __forceinline__ void better_groups(float s, float tol, int &sure, int &maybe) {
+  if constexpr (kStart < 16) {
+    const float o = dpp_f<0x120 + kStart>(s);  // of lane c - kStart, around the row
+    const bool first = (int)(threadIdx.x & 15) >= kStart;
+    sure += (o > s + tol) | (first & (o == s + tol));
+    maybe += (o > s - tol) | (first & (o == s - tol));
+    better_groups<L, kStart + L>(s, tol, sure, maybe);
+  }
+}
+
+__device__ __forceinline__ uint32_t float_key(float x) {
+  const int32_t u = (int32_t)__float_as_uint(x);
+  return (uint32_t)(u ^ ((u >> 31) | (int32_t)0x80000000));
+}
+
+// Larger keys first (Batcher's odd-even merges).
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j <= V - 1 - q; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t lo = k[i + j] < k[i + j + q] ? k[i + j] : k[i + j + q];
+            k[i + j] = umax32(k[i + j], k[i + j + q]);
+            k[i + j + q] = lo;
+          }
+}
+
+template <int kStart = 1>
+__device__ __forceinline__ int better_candidates(double c, uint32_t id) {
+  if constexpr (kStart >= 16) {
+    return 0;
+  } else {
+    const double o = dpp_d<0x120 + kStart>(c);
+    const uint32_t oid = dpp_u<0x120 + kStart>(id);
+    return (o > c || (o == c && oid < id)) + better_candidates<kStart + 1>(c, id);
+  }
+}
+
+// NaN or +infinity
+__device__ __forceinline__ bool wrong(float x) {
+  return __builtin_amdgcn_classf(x, 0x001 | 0x002 | 0x200);
+}
+
+template <int V, int kMode>
+__global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) {
+  constexpr bool kSig = kMode & kGateSigmoid, kRenorm = kMode & kGateRenorm;
+  constexpr int kExact = (V * 16 + 63) / 64;  // registers of a token in a whole wave
+  constexpr uint32_t kPlace = V > 8 ? 15 : V > 4 ? 7 : 3;
+  __shared__ uint64_t choices[4][kExact * 64];
+  __shared__ ex_u32x2 taken[4][64];  // a lane's key and the lane, in order
+  const int lane = threadIdx.x & 63, c = lane & 15, wave = threadIdx.x >> 6;
+  const int t0 = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + wave)) * 4;
+  if (t0 >= a.T) return;
+  const int t = t0 + (lane >> 4), tt = min(t, a.T - 1);
+  const int E = a.E, K = a.K;
+  const int64_t row = (int64_t)tt * E;
+  bool bad = false;
+  float x[V], v[V];
+  if (a.bf16) {
+    uint32_t w[V / 2];
+    __builtin_memcpy(w, static_cast<const uint16_t *>(a.x) + row + c * V, V * 2);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      x[2 * j] = ex_lo(w[j]);
+      x[2 * j + 1] = ex_hi(w[j]);
+    }
+  } else {
+    __builtin_memcpy(x, static_cast<const float *>(a.x) + row + c * V, V * 4);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    bad |= wrong(x[j]);
+    x[j] = __builtin_isfinite(x[j]) ? x[j] + 0.0f : -INFINITY;
+    v[j] = x[j];
+  }
+  const bool sums = a.sum2 && a.G > 1, exact = !a.bias;
+  float top = 0.0f, sum = 1.0f;
+  if (!kSig && (!kRenorm || a.bias || sums)) {
+    float m = x[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) m = fmaxf(m, x[j]);
+    m = row_max16(m);
+    top = m == -INFINITY ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) s += exp_below(x[j] - top);
+    sum = row_sum16(s);
+  }
+  const float largest = kSig ? 1.0f : 1.0f / sum;  // no score is larger
+  float g1 = -INFINITY, g2 = -INFINITY;  // the lane's best two choices, for its group
+  if (a.bias || sums) {
+    float b[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = 0.0f;
+    if (a.bias) __builtin_memcpy(b, a.bias + c * V, V * 4);
+    const float r = kSig ? 1.0f : __builtin_amdgcn_rcpf(sum);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float s = kSig ? __builtin_amdgcn_rcpf(
+                                 1.0f + __builtin_amdgcn_exp2f(x[j] * -1.44269504f))
+                           : exp_below(x[j] - top) * r;
+      bad |= wrong(b[j]);
+      // (one masked by its logit or bias)
+      const float choice = __builtin_isfinite(x[j] + b[j] * 0.0f) ? s + b[j] : -INFINITY;
+      g2 = __builtin_amdgcn_fmed3f(g1, g2, choice);
+      g1 = fmaxf(g1, choice);
+      v[j] = a.bias ? choice : x[j];
+    }
+  } else if (a.G > 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) g1 = fmaxf(g1, x[j]);
+  }
+  bool unsure = false;
+  bool kept = true;
+  if (a.G > 1) {
+    if (lanes > 1) best_two<0xB1>(g1, g2);
+    if (lanes > 2) best_two<0x4E>(g1, g2);
+    if (lanes > 4) best_two<0x141>(g1, g2);
+    if (lanes > 8) best_two<0x140>(g1, g2);
+    const float s = sums && g2 != -INFINITY ? g1 + g2 : g1;
+    // (a sum of two scores with their biases is off by twice what a choice is, without
+    // places: 2^-20 + 2^-23 of it)
+    const float tol = !(a.bias || sums) || s == -INFINITY ? 0.0f : 0x1p-19f * largest + 0x1p-21f * fabsf(s);
+    int sure = 0, maybe = 0;
+    switch (lanes) {
+      case 1: better_groups<1>(s, tol, sure, maybe); break;
+      case 2: better_groups<2>(s, tol, sure, maybe); break;
+      case 4: better_groups<4>(s, tol, sure, maybe); break;
+      case 8: better_groups<8>(s, tol, sure, maybe); break;
+      default: break;
+    }
+    kept = sure < a.KG;
+    unsure = kept && maybe >= a.KG;
+  }
+  // A masked expert's key is that of -infinity, an exhausted list's or dropped
+  // group's head 0.
+  uint32_t key[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) key[j] = (float_key(v[j]) & ~kPlace) | (kPlace - j);
+  sort_keys<V>(key);
+  key[0] = kept ? key[0] : 0u;
+  constexpr int kShort = V < 9 ? V : 9;  // of a list, for up to eight places
+  auto take = [&](int k, auto depth) {   // the k-th candidate
+    const uint32_t m = row16_max(key[0]);
+    // of equal choices the first lane's, so the lower id
+    const uint64_t same = __ballot((key[0] ^ m) <= kPlace);
+    const int first = __ffs((int)((uint32_t)(same >> (lane & 48)) & 0xffffu)) - 1;
+    if (c == first && m) {
+      taken[wave][lane & 48 | k] = ex_u32x2{key[0], (uint32_t)lane};
+#pragma unroll
+      for (int j = 0; j + 1 < depth.value; ++j) key[j] = key[j + 1];
+      key[depth.value - 1] = 0u;
+    }
+  };
+  taken[wave][lane] = ex_u32x2{0u, 0u};
+  if (K <= 8) {
+    for (int k = 0; k <= K; ++k) take(k, std::integral_constant<int, kShort>{});
+  } else {
+    for (int k = 0; k <= K; ++k) take(k, std::integral_constant<int, V>{});
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  uint32_t my_key = taken[wave][lane].x;
+  int my_lane = (int)taken[wave][lane].y & 15;
+  my_key = my_key > kKeyNegInf ? my_key : 0u;
+  auto value = [&](uint32_t k) {  // of a key without its place
+    const int32_t u = (int32_t)(k & ~kPlace);
+    return __uint_as_float((uint32_t)(u ^ (~(u >> 31) | (int32_t)0x80000000)));
+  };
+  int place = c;  // where the lane's candidate stands
+  const uint32_t before = dpp_u<0x111>(my_key);
+  const float f = value(my_key);
+  // (equal bf16 logits are in order; others with equal keys may differ in the places)
+  const bool tie = c >= 1 && c <= K && my_key && value(before) - f <= near(f, exact, largest) &&
+                   !(exact && a.bf16);
+  if (__ballot(tie)) {  // uniform
+    const uint64_t rows = __ballot(tie);
+    const bool here = (uint32_t)(rows >> (lane & 48)) & 0xffffu;
+    for (int k = K + 1; k < 16; ++k) take(k, std::integral_constant<int, V>{});
+    // a short list that ended may have had more
+    if (K <= 8 && V > kShort && here && kept && key[0] == 0u) unsure = true;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    my_key = taken[wave][lane].x;
+    my_lane = (int)taken[wave][lane].y & 15;
+    my_key = my_key > kKeyNegInf ? my_key : 0u;
+    const int id = my_key ? my_lane * V + (int)(kPlace - (my_key & kPlace)) : E + c;
+    const float xc = gate_load(a.x, row + min(id, E - 1), a.bf16);
+    double d = xc;
+    if (a.bias) {
+      d = 1.0 / (1.0 + exp(-(double)xc)) + (double)a.bias[min(id, E - 1)];
+      if (!kSig) unsure = unsure || here;
+    }
+    if (!my_key) d = -INFINITY;
+    const int rank = better_candidates(d, (uint32_t)id);
+    if (here) {
+      place = rank;
+      // the last candidate bounds those that are none
+      const uint32_t last = (uint32_t)__shfl((int)my_key, (lane & 48) + 15);
+      if (rank == K - 1 && my_key && last && value(my_key) - value(last) <= near(value(last), exact, largest))
+        unsure = true;
+    }
+  }
+  const uint64_t again = __ballot(unsure);
+  const bool on = place < K, found = on && my_key;
+  const int id = found ? my_lane * V + (int)(kPlace - (my_key & kPlace)) : -1;
+  float xs = -INFINITY;
+  if (found) xs = gate_load(a.x, row + id, a.bf16);
+  float p;
+  if (kRenorm) {
+    const float z = kSig ? log_sigmoid(xs) : xs;
+    const float m = row_max16(found ? z : -INFINITY);
+    const float ez = found ? expf(z - m) : 0.0f;
+    const float all = row_sum16(ez);
+    p = found ? ez / all : 0.0f;
+  } else if (kSig) {
+    p = found ? sigmoid(xs) : 0.0f;
+  } else {
+    p = found ? expf(xs - top) / sum : 0.0f;
+  }
+  if (on && t < a.T && !((uint32_t)(again >> (lane & 48)) & 0xffffu)) {
+    const int64_t o = (int64_t)t * K + place;
+    a.idx[o] = id;
+    a.w[o] = found ? p * a.scale : 0.0f;
+  }
+  if (again) {  // uniform
+#pragma unroll 1
+    for (int r = 0; r < 4; ++r)
+      if ((again >> (16 * r) & 0xffff) && t0 + r < a.T)
+        exact_token<kExact, kMode>(a, t0 + r, choices[wave], &bad);
+  }
+  if (a.status && __ballot(bad) && lane == 0) atomicOr(a.status, kStBadLogit);
 }
 
 template <int V, int kMode>
@@ -176,8 +495,34 @@ hipError_t gate_grouped_vm(const GroupArgs &a, hipStream_t s) {
                      s, a);
   return hipGetLastError();
 }
+template <int V, int kMode>
+hipError_t gate_rows_vm(const GroupArgs &a, int lanes, hipStream_t s) {
+  hipLaunchKernelGGL((gate_rows_kernel<V, kMode>), dim3((unsigned)((a.T + 15) / 16)), dim3(256), 0,
+                     s, a, lanes);
+  return hipGetLastError();
+}
+
+// Lanes of a group where a token fits a row of 16: 4, 8, 10 or 16 experts a lane,
+// K + 1 candidates, groups of whole lanes whose number is a power of two, rows on
+// whole words. 0: a wave a token.
+int row_lanes(const GroupArgs &a) {
+  const int v = a.E / 16, n = a.E / a.G;
+  if (a.E % 16 || (v != 4 && v != 8 && v != 10 && v != 16) || a.K > 15 || n % v) return 0;
+  if (reinterpret_cast<uintptr_t>(a.x) & 3u) return 0;
+  const int lanes = n / v;
+  return lanes & (lanes - 1) ? 0 : lanes;
+}
+
 template <int kMode>
 hipError_t gate_grouped_m(const GroupArgs &a, hipStream_t s) {
+  if (const int lanes = row_lanes(a)) {
+    switch (a.E / 16) {
+      case 4: return gate_rows_vm<4, kMode>(a, lanes, s);
+      case 8: return gate_rows_vm<8, kMode>(a, lanes, s);
+      case 10: return gate_rows_vm<10, kMode>(a, lanes, s);
+      default: return gate_rows_vm<16, kMode>(a, lanes, s);
+    }
+  }
   if (a.E <= 64) return gate_grouped_vm<1, kMode>(a, s);
   if (a.E <= 128) return gate_grouped_vm<2, kMode>(a, s);
   if (a.E <= 256) return gate_grouped_vm<4, kMode>(a, s);

@@ -100,7 +100,8 @@ int moe_gate_grad(int32_t T, int32_t E, int32_t K, const void *logits, const int
  * (of the one where it has no other); the topk_groups groups of the largest
  * scores stay, of equal ones the first. Selected are the K largest choices in
  * them, larger first, equal ones by lower id; choices and groups' scores are
- * compared as in 64 bits. bias [E] float, NULL: none; -infinity masks an expert
+ * compared as in 64 bits (without a bias the choices by the logits, whose order
+ * scores that saturate no longer show). bias [E] float, NULL: none; -infinity masks an expert
  * (its logit still counts in the softmax's sum), NaN and +infinity do too and set
  * MOE_STATUS_BAD_LOGIT. Logits, places without an expert, topk_weights, scale
  * and the other flags are moe_gate's, and moe_gate_grad with the same flags
