@@ -20,8 +20,10 @@ struct ActGradArgs {
 
 template <int kAct>
 __device__ __forceinline__ float slope(float z) {
-  if (kAct == kActGelu)
-    return __builtin_fmaf(z * 0.39894228f, expf(-0.5f * z * z), 0.5f * erfcf(z * -0.70710678f));
+  if (kAct == kActGelu) {
+    const Normal n = normal(z);
+    return __builtin_fmaf(z, n.density, n.below);
+  }
   const Sigmoids g = sigmoids(z);
   return g.s * __builtin_fmaf(z, g.rest, 1.0f);
 }

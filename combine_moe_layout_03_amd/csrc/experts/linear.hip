@@ -164,8 +164,9 @@ __global__ __launch_bounds__(256, kRT * kCT > 32 ? 1 : 2) void product_kernel(Pr
   constexpr int kRW = 2, kCW = 2;
   constexpr int kWaves = kRW * kCW, kR = kRW * kRT * 16, kC = kCW * kCT * 16;
   constexpr bool kPairs = kAct == kActSwiglu;
-  __shared__ __align__(1024) uint8_t lds_r[2][stage_rows(kR, kRAcross) * 128],
-      lds_c[2][stage_rows(kC, kCAcross) * 128];
+  constexpr int kRBytes = stage_rows(kR, kRAcross) * 128, kCBytes = stage_rows(kC, kCAcross) * 128;
+  __shared__ __align__(1024) uint8_t lds[2 * (kRBytes + kCBytes)];
+  uint8_t *const lds_r = lds, *const lds_c = lds + 2 * kRBytes;
   // Workgroup b runs on XCD b % 8: every XCD takes a run of neighbouring tiles,
   // four tiles high, which share operands in its L2.
   const int row_units = (a.rows + kR - 1) / kR, tiles = row_units * a.col_units;
@@ -216,9 +217,9 @@ __global__ __launch_bounds__(256, kRT * kCT > 32 ? 1 : 2) void product_kernel(Pr
   // item m: the columns' fragments 0 ... kCT - 1, then the rows'
   auto read = [&](int s, int kk, int m) {
     if (m < kCT)
-      fc[kk][m] = fragment<kC, kCAcross>(lds_c[s & 1], wc * kCT + m, kk);
+      fc[kk][m] = fragment<kC, kCAcross>(lds_c + (s & 1) * kCBytes, wc * kCT + m, kk);
     else
-      fr[kk][m - kCT] = fragment<kR, kRAcross>(lds_r[s & 1], wr * kRT + m - kCT, kk);
+      fr[kk][m - kCT] = fragment<kR, kRAcross>(lds_r + (s & 1) * kRBytes, wr * kRT + m - kCT, kk);
   };
   auto copy = [&](const Stage &gr, const Stage &gc, auto i) {
     if constexpr (i.value < kRN)
@@ -269,61 +270,83 @@ __global__ __launch_bounds__(256, kRT * kCT > 32 ? 1 : 2) void product_kernel(Pr
   __builtin_amdgcn_s_waitcnt(vmcnt(0));  // no copy outlives the workgroup
   products_done();
 
+  // The sums go through LDS, 32 rows of a wave at a time, so that a lane finishes eight
+  // neighbouring columns: whole lines of the output and the residual.
+  lds_barrier();  // no wave reads its stages any more
   const int l16 = lane & 15, quad = lane >> 4;
+  constexpr int kPitch = kCT * 64 + 16;                   // bytes of a row: all banks in turn
+  constexpr int kPer = kCT * 2 / (kPairs ? 2 : 1);        // lanes of a row
+  constexpr int kPasses = kPer / 2;
+  static_assert(4 * 32 * kPitch <= sizeof(lds), "the rows fit");
+  uint8_t *const mine = lds + wave * (32 * kPitch);
+  const int n0 = (col0 + wc * kCT * 16) / (kPairs ? 2 : 1);
+  each<kRT / 2>([&](auto pair) {
+    constexpr int i = 2 * pair.value;
+    const int64_t t0 = row0 + (wr * kRT + i) * 16;
+    auto row = [&](int p) { return (p * 64 + lane) / kPer; };
+    auto col = [&](int p) { return (p * 64 + lane) % kPer * 8; };  // of the wave's
+    ex_u32x4 res[kPasses];
+    if (a.splits == 1) {
 #pragma unroll
-  for (int i = 0; i < kRT; ++i) {
-    const int64_t t = row0 + (wr * kRT + i) * 16 + l16;
-    if (t >= a.rows) continue;
-    if (a.splits > 1) {  // as they are; a pair's halves in their own columns
+      for (int p = 0; p < kPasses; ++p)
+        res[p] = linear_residual(a.e, min(t0 + row(p), (int64_t)a.rows - 1),
+                                 min(n0 + col(p), a.e.N - 8));
+    }
 #pragma unroll
-      for (int j = 0; j < kCT; ++j) {
-        int c = col0 + (wc * kCT + j) * 16 + quad * 4;
-        int at = c;
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < kCT; ++j)
+        *reinterpret_cast<f32x4 *>(mine + (h * 16 + l16) * kPitch + j * 64 + quad * 16) =
+            acc[i + h][j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      // a pair's blocks of 16 stand next to each other
+      const int c = kPairs ? (col(p) & ~15) * 2 + (col(p) & 15) : col(p);
+      const float *from = reinterpret_cast<const float *>(mine + row(p) * kPitch) + c;
+      const f32x8 z = two_of(from), up = kPairs ? two_of(from + 16) : z;
+      const int64_t t = t0 + row(p);
+      const int n = n0 + col(p);
+      if (t >= a.rows || n >= a.e.N) continue;
+      if (a.splits > 1) {  // as they are
+        const int64_t NN = kPairs ? 2 * (int64_t)a.e.N : a.e.N;
+        float *o = a.ws + ((int64_t)part * a.rows + t) * NN + n;
+        *reinterpret_cast<f32x4 *>(o) = f32x4{z[0], z[1], z[2], z[3]};
+        *reinterpret_cast<f32x4 *>(o + 4) = f32x4{z[4], z[5], z[6], z[7]};
         if (kPairs) {
-          const int b = c >> 4;
-          c = (b >> 1) * 16 + (c & 15);
-          at = c + (b & 1) * a.e.N;
+          *reinterpret_cast<f32x4 *>(o + a.e.N) = f32x4{up[0], up[1], up[2], up[3]};
+          *reinterpret_cast<f32x4 *>(o + a.e.N + 4) = f32x4{up[4], up[5], up[6], up[7]};
         }
-        if (c < a.e.N)
-          *reinterpret_cast<f32x4 *>(a.ws + ((int64_t)part * a.rows + t) *
-                                                (kPairs ? 2 * (int64_t)a.e.N : a.e.N) + at) =
-              acc[i][j];
-      }
-    } else if (kPairs) {
-#pragma unroll
-      for (int j = 0; j < kCT; j += 2) {
-        const int c = (col0 + (wc * kCT + j) * 16) / 2 + quad * 4;
-        if (c < a.e.N) linear_store<kAct>(a.e, t, c, acc[i][j], acc[i][j + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kCT; ++j) {
-        const int c = col0 + (wc * kCT + j) * 16 + quad * 4;
-        if (c < a.e.N) linear_store<kAct>(a.e, t, c, acc[i][j], acc[i][j]);
+      } else {
+        linear_store<kAct>(a.e, t, n, z, up, res[p]);
       }
     }
+    __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_sched_barrier(0);
-  }
+  });
 }
 
 // Adds the parts of a split product up, in order, and finishes them.
 template <int kAct>
 __global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
-  const int NN = kAct == kActSwiglu ? 2 * a.e.N : a.e.N, quads = a.e.N / 4;
+  constexpr bool kPairs = kAct == kActSwiglu;
+  const int NN = kPairs ? 2 * a.e.N : a.e.N, per = a.e.N / 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)a.rows * quads) return;
-  const int64_t t = i / quads;
-  const int n = (int)(i - t * quads) * 4;
+  if (i >= (int64_t)a.rows * per) return;
+  const int64_t t = i / per;
+  const int n = (int)(i - t * per) * 8;
   const float *p = a.ws + t * NN + n;
   const int64_t part = (int64_t)a.rows * NN;
-  f32x4 z = *reinterpret_cast<const f32x4 *>(p), up = z;
-  if (kAct == kActSwiglu) up = *reinterpret_cast<const f32x4 *>(p + a.e.N);
+  const ex_u32x4 res = linear_residual(a.e, t, n);
+  f32x8 z = two_of(p), up = z;
+  if (kPairs) up = two_of(p + a.e.N);
   for (int s = 1; s < a.splits; ++s) {
     p += part;
-    z += *reinterpret_cast<const f32x4 *>(p);
-    if (kAct == kActSwiglu) up += *reinterpret_cast<const f32x4 *>(p + a.e.N);
+    z += two_of(p);
+    if (kPairs) up += two_of(p + a.e.N);
   }
-  linear_store<kAct>(a.e, t, n, z, up);
+  linear_store<kAct>(a.e, t, n, z, up, res);
 }
 
 // ---- stream: few rows -----------------------------------------------------------
@@ -394,9 +417,9 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(ProductArgs a
   lds_barrier();                         // and with kW = 8 a ring is read up into the next
   *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(mine) + l16 * kPitch + quad * 4) = acc;
   lds_barrier();
-  constexpr int kQuads = kOut / 4;
-  if (threadIdx.x >= 16 * kQuads) return;
-  const int t = threadIdx.x / kQuads, n = threadIdx.x % kQuads * 4;
+  constexpr int kPer = kOut / 4;  // threads of a token, four columns each
+  if (threadIdx.x >= 16 * kPer) return;
+  const int t = threadIdx.x / kPer, n = threadIdx.x % kPer * 4;
   f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f}, up = z;
 #pragma unroll
   for (int w = 0; w < kStreamWaves; ++w) {
@@ -405,7 +428,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(ProductArgs a
     z += *reinterpret_cast<const f32x4 *>(p);
     if (kPairs) up += *reinterpret_cast<const f32x4 *>(p + kOut);
   }
-  if (t0 + t < a.rows && n0 + n < a.e.N) linear_store<kAct>(a.e, t0 + t, n0 + n, z, up);
+  if (t0 + t < a.rows && n0 + n < a.e.N) linear_store4<kAct>(a.e, t0 + t, n0 + n, z, up);
 }
 
 struct Plan {
@@ -434,8 +457,8 @@ Plan plan(int64_t rows, int64_t cols, int64_t k, bool pairs) {
   // a large one's stage takes 1.4. Parts of k, written and read again, only
   // where there are tiles for at most half the CUs.
   const int64_t n = tiles(4, 4), last = n % 512;
-  const double small = (double)(n / 512) * (36 * steps + 128) +
-                       (last == 0 ? 0.0 : last <= 256 ? 23 * steps + 128 : 36 * steps + 128);
+  const double small = (double)(n / 512) * (38 * steps + 364) +
+                       (last == 0 ? 0.0 : last <= 256 ? 23 * steps + 180 : 38 * steps + 364);
   if (best <= small) return p;
   p.high = p.wide = 4;
   int64_t s = 256 / n;
@@ -503,7 +526,7 @@ hipError_t launch_product(ProductArgs a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(join_kernel<kAct>,
-                       dim3((unsigned)(((int64_t)a.rows * (a.e.N / 4) + 255) / 256)), dim3(256), 0,
+                       dim3((unsigned)(((int64_t)a.rows * (a.e.N / 8) + 255) / 256)), dim3(256), 0,
                        s, a);
   }
   return hipGetLastError();
