@@ -42,12 +42,24 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
 #pragma unroll
     for (int d = 0; d < 8; ++d) sum[h][d] = 0.0f;
   const int end = min(a.T, ((int)blockIdx.y + 1) * a.run);
-  for (int t = blockIdx.y * a.run + wave; t < end; t += 4) {
-    const ex_u32x4 e = __builtin_nontemporal_load(a.d_out + (int64_t)t * a.nv + at);
-    ex_u32x4 z = e, u = e, dz, du;
+  struct Row {
+    ex_u32x4 e, z, u;
+  };
+  auto load = [&](int t) {
+    Row r;
     const int64_t row = (int64_t)t * a.nv * kHalves + at;
-    if (kAct != kActNone) z = __builtin_nontemporal_load(a.z + row);
-    if (kPairs) u = __builtin_nontemporal_load(a.z + row + a.nv);
+    r.e = __builtin_nontemporal_load(a.d_out + (int64_t)t * a.nv + at);
+    r.z = kAct != kActNone ? __builtin_nontemporal_load(a.z + row) : r.e;
+    r.u = kPairs ? __builtin_nontemporal_load(a.z + row + a.nv) : r.e;
+    return r;
+  };
+  int t = blockIdx.y * a.run + wave;
+  Row next = load(min(t, end - 1));
+  for (; t < end; t += 4) {
+    const ex_u32x4 e = next.e, z = next.z, u = next.u;
+    ex_u32x4 dz, du;
+    next = load(min(t + 4, end - 1));
+    const int64_t row = (int64_t)t * a.nv * kHalves + at;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float g[2], k[2];
@@ -66,8 +78,8 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
         }
         sum[0][2 * j + b] += g[b];
       }
-      dz[j] = ex_bf16x2(g[0], g[1]);
-      du[j] = ex_bf16x2(k[0], k[1]);
+      dz[j] = ex_round2(g[0], g[1]);
+      du[j] = ex_round2(k[0], k[1]);
     }
     if (kAct != kActNone && ok) {
       __builtin_nontemporal_store(dz, a.d_z + row);
@@ -97,7 +109,7 @@ int32_t run_rows(int32_t T, int32_t nv, int32_t halves) {
   if (runs > fit) runs = fit;
   if (runs < 1) runs = 1;
   int64_t rows = (T + runs - 1) / runs;
-  return (int32_t)(rows < 4 ? 4 : (rows + 3) / 4 * 4);
+  return (int32_t)(rows < 8 ? 8 : (rows + 3) / 4 * 4);
 }
 
 }  // namespace

@@ -33,6 +33,13 @@ __device__ __forceinline__ uint32_t ex_bf16x2(float a, float b) {
   return ex_bf16(a) | (ex_bf16(b) << 16);
 }
 
+// The same by the conversion instruction (one for both; a NaN stays a NaN).
+typedef float ex_f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 ex_bf16p __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t ex_round2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(ex_f32x2{a, b}, ex_bf16p));
+}
+
 template <int kCtrl>
 __device__ __forceinline__ float dpp_f(float x) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(

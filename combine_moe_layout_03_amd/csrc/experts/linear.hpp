@@ -69,8 +69,8 @@ __device__ __forceinline__ f32x8 two_of(const float *p) {  // 16-byte aligned
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 __device__ __forceinline__ ex_u32x4 bf16_of(f32x8 v) {
-  return ex_u32x4{ex_bf16x2(v[0], v[1]), ex_bf16x2(v[2], v[3]), ex_bf16x2(v[4], v[5]),
-                  ex_bf16x2(v[6], v[7])};
+  return ex_u32x4{ex_round2(v[0], v[1]), ex_round2(v[2], v[3]), ex_round2(v[4], v[5]),
+                  ex_round2(v[6], v[7])};
 }
 
 // The residual of eight columns n ... n + 7 of row t, to be loaded ahead.
@@ -126,10 +126,10 @@ __device__ __forceinline__ void linear_store4(const LinearEpilogue &e, int64_t t
   }
   if (kAct != kActNone && e.pre) {
     uint16_t *p = e.pre + t * NN + n;
-    *reinterpret_cast<ex_u32x2 *>(p) = ex_u32x2{ex_bf16x2(z[0], z[1]), ex_bf16x2(z[2], z[3])};
+    *reinterpret_cast<ex_u32x2 *>(p) = ex_u32x2{ex_round2(z[0], z[1]), ex_round2(z[2], z[3])};
     if (kAct == kActSwiglu)
       *reinterpret_cast<ex_u32x2 *>(p + e.N) =
-          ex_u32x2{ex_bf16x2(up[0], up[1]), ex_bf16x2(up[2], up[3])};
+          ex_u32x2{ex_round2(up[0], up[1]), ex_round2(up[2], up[3])};
   }
   f32x4 h;
 #pragma unroll
@@ -145,7 +145,7 @@ __device__ __forceinline__ void linear_store4(const LinearEpilogue &e, int64_t t
     *reinterpret_cast<f32x4 *>(static_cast<float *>(e.out) + t * e.N + n) = h;
   else
     *reinterpret_cast<ex_u32x2 *>(static_cast<uint16_t *>(e.out) + t * e.N + n) =
-        ex_u32x2{ex_bf16x2(h[0], h[1]), ex_bf16x2(h[2], h[3])};
+        ex_u32x2{ex_round2(h[0], h[1]), ex_round2(h[2], h[3])};
 }
 
 }  // namespace moe

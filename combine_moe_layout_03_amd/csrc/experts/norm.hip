@@ -23,8 +23,8 @@ __device__ __forceinline__ void unpack(ex_u32x4 v, float (&f)[8]) {
   }
 }
 __device__ __forceinline__ ex_u32x4 pack(const float (&f)[8]) {
-  return ex_u32x4{ex_bf16x2(f[0], f[1]), ex_bf16x2(f[2], f[3]), ex_bf16x2(f[4], f[5]),
-                  ex_bf16x2(f[6], f[7])};
+  return ex_u32x4{ex_round2(f[0], f[1]), ex_round2(f[2], f[3]), ex_round2(f[4], f[5]),
+                  ex_round2(f[6], f[7])};
 }
 
 // Sum over the kWaves waves that share a row (one: over the wave). `part` is
@@ -148,24 +148,40 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void norm_grad_ker
 #pragma unroll
     for (int d = 0; d < 8; ++d) dw[j][d] = 0.0f;
   int turn = 0;
-  for (int row = (int)blockIdx.x * kRows + (kWaves == 1 ? wave : 0); row < a.T;
-       row += (int)gridDim.x * kRows, turn ^= 1) {
-    const int64_t at = (int64_t)row * a.nv;
+  struct Row {
     ex_u32x4 v[V], e[V], ds[V];
+  };
+  auto load = [&](int row) {
+    Row r;
+    const int64_t at = (int64_t)row * a.nv;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int i = min(tid + j * kStride, a.nv - 1);
-      v[j] = __builtin_nontemporal_load(a.sum + at + i);
-      e[j] = __builtin_nontemporal_load(a.dy + at + i);
-      ds[j] = a.dsum ? __builtin_nontemporal_load(a.dsum + at + i) : ex_u32x4{0, 0, 0, 0};
+      r.v[j] = __builtin_nontemporal_load(a.sum + at + i);
+      r.e[j] = __builtin_nontemporal_load(a.dy + at + i);
+      r.ds[j] = a.dsum ? __builtin_nontemporal_load(a.dsum + at + i) : ex_u32x4{0, 0, 0, 0};
     }
+    return r;
+  };
+  ex_u32x4 weight[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) weight[j] = a.weight[min(tid + j * kStride, a.nv - 1)];
+  const int step = (int)gridDim.x * kRows;
+  int row = (int)blockIdx.x * kRows + (kWaves == 1 ? wave : 0);
+  if (row >= a.T && kWaves > 1) return;  // (no workgroup is without a row)
+  Row next = load(min(row, a.T - 1));
+  for (; row < a.T; row += step, turn ^= 1) {
+    const Row now = next;
+    next = load(min(row + step, a.T - 1));  // the last one's again behind the end
+    const int64_t at = (int64_t)row * a.nv;
+    const ex_u32x4 *v = now.v, *e = now.e, *ds = now.ds;
     float ss = 0.0f, gs = 0.0f;  // of squares, and of sum * g (rstd follows)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       float f[8], g[8], w[8];
       unpack(v[j], f);
       unpack(e[j], g);
-      unpack(a.weight[min(tid + j * kStride, a.nv - 1)], w);
+      unpack(weight[j], w);
       float s = 0.0f, t = 0.0f;
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
@@ -201,7 +217,7 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void norm_grad_ker
       float f[8], g[8], w[8], o[8];
       unpack(v[j], f);
       unpack(e[j], g);
-      unpack(a.weight[min(i, a.nv - 1)], w);
+      unpack(weight[j], w);
       unpack(ds[j], o);
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
@@ -239,27 +255,31 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void norm_grad_ker
 }
 
 // out[i] = sum over the P rows of partial[p][i], in an order that depends on P
-// alone. 64 columns a workgroup of 16 waves, each a sixteenth of the rows.
+// alone. A workgroup takes 32 columns, a line of every row; its 32 half waves
+// share the rows out, eight loads of each in flight.
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restrict__ partial,
                                                           int32_t P, int32_t n,
                                                           float *__restrict__ out) {
-  __shared__ float part[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i = min((int)blockIdx.x * 64 + lane, n - 1);
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const float *p = partial + i;
-  int r = wave;
-  for (; r + 48 < P; r += 64)
+  __shared__ float part[32][33];
+  const int col = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const float *p = partial + min((int)blockIdx.x * 32 + col, n - 1);
+  float s[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s[k] += p[(int64_t)(r + 16 * k) * n];
-  for (; r < P; r += 16) s[0] += p[(int64_t)r * n];
-  part[wave][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+  for (int k = 0; k < 8; ++k) s[k] = 0.0f;
+  for (int r = group; r < P; r += 256) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = p[(int64_t)min(r + 32 * k, P - 1) * n];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k] += r + 32 * k < P ? v[k] : 0.0f;
+  }
+  part[group][col] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   lds_barrier();
-  if (wave) return;
+  if (threadIdx.x >= 32) return;
   float t = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 16; ++w) t += part[w][lane];
-  if ((int)blockIdx.x * 64 + lane < n) out[i] = t;
+  for (int g = 0; g < 32; ++g) t += part[g][col];
+  if ((int)blockIdx.x * 32 + col < n) out[blockIdx.x * 32 + col] = t;
 }
 
 __global__ __launch_bounds__(256) void zeros_kernel(float *p, int64_t n) {
@@ -277,6 +297,7 @@ Spread spread(int32_t T, int32_t nv) {
   if (nv <= 128 && T >= 512) return {1, 2};
   if (nv <= 256 && T >= 512) return {1, 4};
   if (nv <= 256) return {4, 1};
+  if (nv <= 1024 && T <= 256) return {16, 1};
   if (nv <= 512) return {4, 2};
   if (nv <= 1024) return {4, 4};
   if (nv <= 2048) return {4, 8};
@@ -309,6 +330,7 @@ hipError_t norm_grad_wv(const NormGradArgs &a, int32_t blocks, hipStream_t s) {
     if (SP.waves == 1 && SP.v == 1) return FN<1, 1>(__VA_ARGS__);    \
     if (SP.waves == 1 && SP.v == 2) return FN<1, 2>(__VA_ARGS__);    \
     if (SP.waves == 1) return FN<1, 4>(__VA_ARGS__);                 \
+    if (SP.waves == 16 && SP.v == 1) return FN<16, 1>(__VA_ARGS__);  \
     if (SP.waves == 16) return FN<16, 8>(__VA_ARGS__);               \
     if (SP.v == 1) return FN<4, 1>(__VA_ARGS__);                     \
     if (SP.v == 2) return FN<4, 2>(__VA_ARGS__);                     \
@@ -325,7 +347,7 @@ hipError_t norm_grad_launch(const NormGradArgs &a, const Spread &sp, int32_t blo
 
 hipError_t launch_column_sum(const float *partial, int32_t P, int32_t n, float *out,
                              hipStream_t s) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((n + 63) / 64), dim3(1024), 0, s, partial, P, n, out);
+  hipLaunchKernelGGL(column_sum_kernel, dim3((n + 31) / 32), dim3(1024), 0, s, partial, P, n, out);
   return hipGetLastError();
 }
 
@@ -360,7 +382,7 @@ hipError_t launch_rms_norm(int32_t T, int32_t H, const uint16_t *x, const uint16
 int32_t norm_grad_blocks(int32_t T, int32_t H) {
   const Spread sp = spread(T, H / 8);
   const int64_t rows = sp.waves == 1 ? ((int64_t)T + 3) / 4 : T;
-  int64_t n = sp.waves == 16 ? 256 : 512;
+  int64_t n = sp.waves == 16 && sp.v > 1 ? 256 : 512;
   if (n > rows) n = rows;
   if (n > kMaxWorkspace / 4 / H) n = kMaxWorkspace / 4 / H;
   return (int32_t)n;
