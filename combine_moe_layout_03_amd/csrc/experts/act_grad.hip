@@ -101,10 +101,10 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
             (join[0][h][i] + join[1][h][i]) + (join[2][h][i] + join[3][h][i]);
 }
 
-// Runs of rows: about eight workgroups a CU, and partial sums within kMaxWorkspace.
+// Runs of rows: about four workgroups a CU, and partial sums within kMaxWorkspace.
 int32_t run_rows(int32_t T, int32_t nv, int32_t halves) {
   const int64_t blocks = (nv + 63) / 64;
-  int64_t runs = 2048 / blocks;
+  int64_t runs = 1024 / blocks;
   const int64_t fit = kMaxWorkspace / 4 / ((int64_t)nv * 8 * halves);
   if (runs > fit) runs = fit;
   if (runs < 1) runs = 1;

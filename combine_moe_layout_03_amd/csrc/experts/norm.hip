@@ -169,10 +169,12 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void norm_grad_ker
   const int step = (int)gridDim.x * kRows;
   int row = (int)blockIdx.x * kRows + (kWaves == 1 ? wave : 0);
   if (row >= a.T && kWaves > 1) return;  // (no workgroup is without a row)
-  Row next = load(min(row, a.T - 1));
+  constexpr bool kAhead = kWaves * V <= 64;  // (the widest rows fill the registers alone)
+  Row next;
+  if (kAhead) next = load(min(row, a.T - 1));
   for (; row < a.T; row += step, turn ^= 1) {
-    const Row now = next;
-    next = load(min(row + step, a.T - 1));  // the last one's again behind the end
+    const Row now = kAhead ? next : load(row);
+    if (kAhead) next = load(min(row + step, a.T - 1));  // the last one's again behind the end
     const int64_t at = (int64_t)row * a.nv;
     const ex_u32x4 *v = now.v, *e = now.e, *ds = now.ds;
     float ss = 0.0f, gs = 0.0f;  // of squares, and of sum * g (rstd follows)
