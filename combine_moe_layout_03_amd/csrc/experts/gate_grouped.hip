@@ -2,9 +2,15 @@
 // the K largest choices c = score + bias of each token, and their weights, from
 // the scores alone.
 //
-// One wave holds one token, expert e = lane + 64 * j in register j. A choice is
-// compared as a double: scores of different logits that a float would merge, or
-// order wrongly by its rounding, still rank as they stand.
+// Choices are compared as doubles: scores of different logits that a float would
+// merge, or order wrongly by its rounding, still rank as they stand. Two kernels
+// do that. One takes a token a wave and computes every choice in 64 bits; the
+// other, for the usual shapes, takes four tokens a wave, orders floats and goes back
+// to 64 bits only where two are too near to be told apart. 8192 tokens x 256 experts,
+// 8 groups, top 8: 25 us by the first, 8.3 by the second, of which a launch is 1.6;
+// bound by instructions (about 1000 for four tokens, at two waves a SIMD) and their
+// latencies. Where a batch holds a token that has to be done again (about one in 8000:
+// two groups' sums within 3e-6), the call ends about 4 us later. 16 tokens: 5 us.
 #include "gate.hpp"
 
 #include <type_traits>

@@ -7,7 +7,8 @@
 // along k ([r][k]) or across it ([k][r]); only the copies to LDS and the reads of
 // the fragments differ. The columns' operand comes first in the matrix
 // instruction (16 x 16 x 32), so that a lane's four results are neighbours in a
-// row of D. Sums are float.
+// row of D. Sums are float: those of 7168 products are off by 5e-7 of the result's norm
+// (a chain of fused multiply-adds by 9e-7).
 #include "linear.hpp"
 
 #include <utility>
@@ -45,6 +46,23 @@ struct ProductArgs {
 };
 
 // ---- tiles --------------------------------------------------------------------
+//
+// Four waves share a tile of up to 256 x 256, one wave a SIMD: each has 128 x 128 sums
+// in its 256 accumulation registers and a whole stage's fragments, in two halves, in
+// the others. So a stage's 64 KB are read from LDS once per two waves (1024 of the 2048
+// clocks that its products take; with eight waves of 128 x 64 it would be 1536), and
+// LDS is free for the stage after next as soon as the second half is in registers.
+//
+// What bounds it: 8192 x 4096 x 7168 take 330 us (1450 TFLOP/s; a library product of
+// this size 300 to 310), the gradients 368 and 364 (370 to 390, 490 to 500): the matrix
+// units are busy 60% of the clocks at 1.9 GHz, where the GPU's power holds them. About
+// 9 us go around every tile: its start, and its sums on their way out. 8192 x 7168 x
+// 2048 198 us, with bias and residual 226 (176 to 181).
+// Measured and not kept (us, beside the kernel of that time): copies issued in one
+// half of a stage for the next one 364 against 346; reads and copies in clumps before
+// every eight products 351 against 338; tiles taken in turn by resident workgroups that
+// start the next one's copies before they store 203 against 198; panels of 2, 6 or 8
+// tiles, other places for the two barriers: within 2%.
 //
 // An operand stage in LDS. Along k: rows of 128 bytes, the 16-byte chunk c of
 // row r at chunk c ^ (r & 7). Across k: 64 rows (k) of the tile's width, the
@@ -208,7 +226,9 @@ __global__ __launch_bounds__(256, kRT * kCT > 32 ? 1 : 2) void product_kernel(Pr
   // one by one between the products.
   constexpr int kItems = kRT + kCT, kCopies = kRN + kCN, kTotal = 2 * kRT * kCT;
   constexpr int kFree = kTotal * 3 / 8, kNext = kTotal * 3 / 4;
-  constexpr int kReadEvery = kFree * 5 / 6 / kItems, kNextEvery = (kTotal - kNext) / kItems < 2 ? 1 : (kTotal - kNext) * 3 / 4 / kItems;
+  constexpr int kReadEvery = kFree * 5 / 6 / kItems;
+  constexpr int kNextEvery =
+      (kTotal - kNext) / kItems < 2 ? 1 : (kTotal - kNext) * 3 / 4 / kItems;
   constexpr int kCopyEvery = (kTotal - kFree) / kCopies;
   static_assert(kReadEvery > 0 && kNextEvery > 0 && kCopyEvery > 0, "a place for each");
   constexpr int kEarly = (kNext - kFree + kCopyEvery - 1) / kCopyEvery;
@@ -355,6 +375,11 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
 // half of them gates) and 16 tokens; its waves share the channels out in groups of
 // 64, each through a ring of groups in its own part of LDS, without a barrier, and
 // join their sums at the end.
+//
+// 16 tokens, 7168 to 4096 channels: 11.3 us, 5.2 TB/s of weights (they come through L2
+// beside as many bytes of tokens); 128 tokens, 7168 to 256: 7.4 us (13.4 as split tiles),
+// 33 bytes a clock into a CU. Rings of 2, 3, 4 or 8 groups and 4, 8 or 16 waves: within
+// 5%, but for those that leave a CU one workgroup, slower where there are more.
 
 constexpr int kStreamWaves = 4, kStreamRing = 4;
 
@@ -437,8 +462,10 @@ struct Plan {
 };
 
 // The tile whose rounds over the 256 CUs take the least, in units of 22 ns, what a
-// wave takes for a fragment's products of a stage: starting and storing a tile takes
-// 11 us, eight stages of a large one.
+// wave takes for a fragment's products of a stage; starting and storing a tile takes
+// about 11 us, eight stages of a large one. (8192 x 7168 columns in rounds of 3.5
+// tiles of 256: 229 us, of 4 tiles of 224 wide: 207; 8192 x 2048 the other way round,
+// 180 against 279.)
 Plan plan(int64_t rows, int64_t cols, int64_t k, bool pairs) {
   const int64_t steps = (k + kStep - 1) / kStep;
   auto tiles = [&](int64_t h, int64_t w) {
@@ -495,7 +522,9 @@ hipError_t launch_stream(ProductArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Eight weight rows a workgroup where sixteen leave CUs without one.
+// Eight weight rows a workgroup where sixteen leave CUs without one (7168 channels, 16
+// rows x 256: 7.5 against 9.5 us, 128 x 256: 7.4 against 8.8, 16 x 2048: 8.7 against 10.2;
+// 16 x 4096, where they do not, 15.1 against 11.3).
 template <int kAct>
 hipError_t launch_streamed(const ProductArgs &a, hipStream_t s) {
   const int64_t rows = (a.rows + 15) / 16, w = kAct == kActSwiglu ? 2 * (int64_t)a.e.N : a.e.N;

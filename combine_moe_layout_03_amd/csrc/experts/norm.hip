@@ -7,9 +7,20 @@
 //
 // A row stays in the registers of the threads that read it (8 channels a
 // thread and vector), so every tensor passes once. The mean is float: 8 squares
-// a lane and vector in order, then the lanes, then the waves, always alike.
+// a lane and vector in order, then the lanes, then the waves, always alike. y is
+// rounded once, from the sum as it is stored, so that the gradient, which has only
+// that, sees the same n. The codes are those of the float y.
 // d_weight: a workgroup adds its rows up in registers and writes one row of
 // partial sums; a second kernel adds those in order.
+//
+// Bound by bytes. 8192 rows of 7168: 470 MB in 71 us (6.6 TB/s; a large copy reaches
+// 6.1), the gradient as many and 15 MB of partial sums in 81 us (5.8), their sum 4 us;
+// 4096 rows of 4096 with codes: 152 MB in 26 us, the gradient 25.7. The gradient was
+// bound by instructions (97 us) while it rounded in integer arithmetic, the conversion
+// instruction does two values at once, and unpacked the weight from memory for every
+// row. A row is loaded while the one before it is computed: two workgroups of a CU
+// then keep 96 KB in flight. 16 rows of 7168 with codes: 3.9 us, most of it the launch
+// and two trips to memory; a row over 16 waves instead of 4 took 1.1 us off.
 #include "cast.hpp"
 
 namespace moe {
