@@ -216,7 +216,9 @@ MOE_API int moe_gate_grouped(int32_t T, int32_t E, int32_t K, int32_t groups, in
 namespace {
 
 int norm_ok(int32_t T, int32_t H, float eps) {
-  if (T < 0 || T > (1 << 24) || H < 8 || H > (1 << 16) || H % 8 != 0) return MOE_ERR_SHAPE;
+  if (T < 0 || T > (1 << 24) - 64 || H < 8 || H > (1 << 16) || H % 8 != 0) return MOE_ERR_SHAPE;
+  // a launch holds fewer than 2^32 threads: 256 a row, above 16384 channels 1024
+  if ((int64_t)T * H > (int64_t)1 << 36) return MOE_ERR_SHAPE;
   if (!std::isfinite(eps) || eps < 0.0f) return MOE_ERR_SHAPE;
   return MOE_OK;
 }

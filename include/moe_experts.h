@@ -201,7 +201,7 @@ int moe_swiglu_grad(int32_t E, int32_t I, int64_t rows, const uint16_t *x, const
  *   it (flags as there); both or neither. A group with a y that is NaN or
  *   infinite gets the scale NaN (UE8M0: byte 255) and NaN codes.
  * At least one of y_out and q. H % 8 == 0 (with q 128, with MOE_FP8_UE8M0 512),
- * 8 <= H <= 65536, T <= 2^24, eps >= 0 and finite. All but scale 16-byte aligned.
+ * 8 <= H <= 65536, T <= 2^24 - 64, T*H <= 2^36, eps >= 0 and finite. All but scale 16-byte aligned.
  * Outputs overlap nothing else but as said. */
 int moe_rms_norm(int32_t T, int32_t H, const uint16_t *x, const uint16_t *residual,
                  const uint16_t *weight, float eps, uint16_t *sum, uint16_t *y_out, uint8_t *q,

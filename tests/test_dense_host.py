@@ -93,10 +93,10 @@ def test_linear_checks(lib):
     for k in "xwbro":
         assert call(**{k: EIGHT}) == ALIGN
     assert call(p=EIGHT, flags=1) == ALIGN and call(ws=EIGHT) == ALIGN
-    need = raw.moe_linear_workspace_bytes(300, 256, 7168, 0)
+    need = raw.moe_linear_workspace_bytes(1000, 256, 7168, 0)  # parts of a sum to join
     assert need > 0
-    assert call(T=300, N=256, Cc=7168, n=need - 1) == WORKSPACE
-    assert call(T=300, N=256, Cc=7168, ws=None) == WORKSPACE
+    assert call(T=1000, N=256, Cc=7168, n=need - 1) == WORKSPACE
+    assert call(T=1000, N=256, Cc=7168, ws=None) == WORKSPACE
     assert call(T=0, x=None, w=None, o=None, ws=None, n=0) == 0
 
     def act(T=4, N=64, d=D, p=D, z=D, b=D, flags=1, ws=D, n=1 << 26):
@@ -191,3 +191,13 @@ def test_wrappers_refuse(lib):
         ep.gate(lg, 2, num_groups=4)
     with pytest.raises(ValueError, match="group_score"):
         ep.gate(lg, 2, num_groups=4, topk_groups=2, group_score="mean")
+
+
+def test_norm_launch_limits(lib):
+    """A row is up to 1024 threads, a launch fewer than 2^32."""
+    raw = lib.lib()
+    for T, H, code in (((1 << 24) - 63, 8, SHAPE), (1 << 22, 16392, SHAPE), (1 << 21, 65536, SHAPE),
+                       (1 << 20, 65536, WORKSPACE)):
+        assert raw.moe_rms_norm_grad(T, H, D, D, 1e-6, D, None, D, D, None, 0, None) == code
+        if code == SHAPE:
+            assert raw.moe_rms_norm(T, H, D, None, D, 1e-6, None, D, None, None, 0, None) == code

@@ -172,3 +172,60 @@ def test_empty(capi):
     e = torch.empty(0, 64, device=dev())
     i, w = torch.empty(0, 4, dtype=torch.int64, device=dev()), torch.empty(0, 4, device=dev())
     capi.moe_gate_grouped(0, 64, 4, 8, 2, e, None, i, w)
+
+
+@pytest.mark.parametrize("E,G,KG", [(256, 8, 4), (160, 8, 3), (64, 8, 4)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_rows_that_start_anywhere(capi, E, G, KG, bf16):
+    """Logits and bias aligned to their own type only: the same ids and weights."""
+    T, K = 21, 6
+    x = logits(T, E, 61, bf16).to(dev())
+    b = torch.from_numpy(biases(E, 62)).to(dev())
+    want = None
+    for off in (0, 1, 2, 3, 5):
+        xs = torch.zeros(T * E + 8, dtype=x.dtype, device=dev())[off:off + T * E].view(T, E)
+        bs = torch.zeros(E + 8, device=dev())[off:off + E]
+        xs.copy_(x)
+        bs.copy_(b)
+        idx = torch.empty(T, K, dtype=torch.int64, device=dev())
+        w = torch.empty(T, K, device=dev())
+        capi.moe_gate_grouped(T, E, K, G, KG, xs, bs, idx, w, SIG | SUM2, 1.0)
+        if want is None:
+            want = idx.clone(), w.clone()
+            assert np.array_equal(idx.cpu().numpy(), ref.grouped_select(
+                x.float().cpu().numpy().astype(np.float64), b.cpu().numpy(), K, G, KG, True, True)[0])
+        assert torch.equal(idx, want[0]) and bool(((w - want[1]).abs() <= 8 * ref.EPS24 * w).all())
+
+
+@pytest.mark.parametrize("K", [8, 9, 15, 16])
+def test_many_places_in_one_lane(capi, K):
+    """The best experts all neighbours, so that one lane's list runs out; and near ties
+    among them."""
+    T, E = 8, 256
+    x = logits(T, E, 71) * 0.1
+    for t in range(T):
+        s = 16 * (t % 15)
+        x[t, s:s + 16] += 3.0
+        if t % 2:
+            x[t, s:s + 16] = 3.0 + torch.arange(16).flip(0) * 2.0 ** -22
+        if t % 3 == 2:
+            x[t, s + 16:s + 20] = x[t, s + 9]
+    for flags in (SIG, SIG | REN | SUM2, 0):
+        check(capi, x, np.full(256, 0.25, np.float32), K, 8, 3, flags)
+        check(capi, x, None, K, 8, 3, flags)
+        check(capi, x.to(torch.bfloat16), None, K, 1, 1, flags)
+
+
+@pytest.mark.parametrize("flags", [SIG | SUM2, SUM2, SIG])
+def test_groups_too_near_to_tell(capi, flags):
+    """Groups whose sums differ by less than their floats' errors, or not at all."""
+    rng = np.random.default_rng(81)
+    T, E = 32, 256
+    x = (rng.standard_normal((T, E)) * 0.5 - 3).astype(np.float32)
+    for t in range(T):
+        for g in range(8):
+            x[t, g * 32 + 5] = np.float32(1.0) + np.float32(rng.integers(0, 3)) * 2.0 ** -23
+            x[t, g * 32 + 9 + g] = np.float32(0.5) + np.float32(rng.integers(0, 3)) * 2.0 ** -24
+    check(capi, torch.from_numpy(x), None, 6, 8, 4, flags)
+    check(capi, torch.from_numpy(x), np.full(256, 0.125, np.float32), 6, 8, 4, flags)
+    check(capi, torch.from_numpy(x).to(torch.bfloat16), None, 6, 8, 4, flags)

@@ -281,3 +281,12 @@ def test_empty(capi):
     capi.moe_linear_grad(0, 8, 16, o, e, w, e, dw)
     capi.moe_linear_act_grad(0, 8, o, None, None, db)
     assert bool((dw == 0).all()) and bool((db == 0).all())
+
+
+@pytest.mark.parametrize("T,N,C", [(16, 4096, 7168), (128, 256, 7168), (129, 1024, 1032),
+                                   (640, 64, 4104), (48, 520, 40), (17, 8, 16392), (20, 8, 8)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_streams_and_splits(capi, T, N, C, act):
+    """Few rows, and parts of long sums joined: the same bits every time."""
+    a = check(capi, T, N, C, act, True, True, False, False)
+    assert torch.equal(a, check(capi, T, N, C, act, True, True, False, False))
