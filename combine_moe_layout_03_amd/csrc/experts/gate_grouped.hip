@@ -265,6 +265,29 @@ __device__ __forceinline__ void better_groups(float s, float tol, int &sure, int
   }
 }
 
+template <int kCtrl>
+__device__ __forceinline__ void best_two_d(double &m1, double &m2) {
+  const double o1 = dpp_d<kCtrl>(m1), o2 = dpp_d<kCtrl>(m2);
+  m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+  m1 = fmax(m1, o1);
+}
+
+// How many groups score more than the lane's, those within tol of it by their doubles.
+template <int L, int kStart = L>
+__device__ __forceinline__ void settle_groups(float s, float tol, double sd, bool unsure,
+                                              int &better, bool &open) {
+  if constexpr (kStart < 16) {
+    const float o = dpp_f<0x120 + kStart>(s);
+    const double od = dpp_d<0x120 + kStart>(sd);
+    const bool known = dpp_u<0x120 + kStart>(unsure) != 0u;
+    const bool first = (int)(threadIdx.x & 15) >= kStart;
+    const bool near = !(o > s + tol) && !(o < s - tol);
+    open |= near & !known;
+    better += near ? (od > sd) | (first & (od == sd)) : o > s + tol;
+    settle_groups<L, kStart + L>(s, tol, sd, unsure, better, open);
+  }
+}
+
 __device__ __forceinline__ uint32_t float_key(float x) {
   const int32_t u = (int32_t)__float_as_uint(x);
   return (uint32_t)(u ^ ((u >> 31) | (int32_t)0x80000000));
@@ -351,6 +374,9 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) 
   }
   const float largest = kSig ? 1.0f : 1.0f / sum;  // no score is larger
   float g1 = -INFINITY, g2 = -INFINITY;  // the lane's best two choices, for its group
+  float by[V];                           // what its group is scored by
+#pragma unroll
+  for (int j = 0; j < V; ++j) by[j] = x[j];
   if (a.bias || sums) {
     float b[V];
 #pragma unroll
@@ -367,6 +393,7 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) 
       const float choice = __builtin_isfinite(x[j] + b[j] * 0.0f) ? s + b[j] : -INFINITY;
       g2 = __builtin_amdgcn_fmed3f(g1, g2, choice);
       g1 = fmaxf(g1, choice);
+      by[j] = choice;
       v[j] = a.bias ? choice : x[j];
     }
   } else if (a.G > 1) {
@@ -394,6 +421,37 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) 
     }
     kept = sure < a.KG;
     unsure = kept && maybe >= a.KG;
+    if (kSig && __ballot(unsure)) {  // uniform, and rare: the groups on the border in 64 bits
+      // Of a group that is unsure, the choices that may be its best two.
+      const float least = (sums ? g2 : g1) - (0x1p-18f + 0x1p-20f * fabsf(g1));
+      double d1 = -INFINITY, d2 = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool in = unsure && by[j] != -INFINITY && !(by[j] < least);
+        if (!__ballot(in)) continue;
+        double d = 1.0 / (1.0 + exp(-(double)x[j]));
+        if (a.bias) d += (double)a.bias[c * V + j];
+        if (!in) d = -INFINITY;
+        d2 = fmax(d2, fmin(d1, d));
+        d1 = fmax(d1, d);
+      }
+      if (lanes > 1) best_two_d<0xB1>(d1, d2);
+      if (lanes > 2) best_two_d<0x4E>(d1, d2);
+      if (lanes > 4) best_two_d<0x141>(d1, d2);
+      const double sd = sums && d2 != -INFINITY ? d1 + d2 : d1;
+      int better = 0;
+      bool open = false;  // one as near that has no such value
+      switch (lanes) {
+        case 1: settle_groups<1>(s, tol, sd, unsure, better, open); break;
+        case 2: settle_groups<2>(s, tol, sd, unsure, better, open); break;
+        case 4: settle_groups<4>(s, tol, sd, unsure, better, open); break;
+        default: settle_groups<8>(s, tol, sd, unsure, better, open);
+      }
+      if (unsure) {
+        kept = better < a.KG;
+        unsure = open;
+      }
+    }
   }
   // A masked expert's key is that of -infinity, an exhausted list's or dropped
   // group's head 0.

@@ -393,8 +393,13 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(ProductArgs a
   static_assert(16 * kPitch * 4 <= kStreamRing * kRows * 128, "sums replace a wave's ring");
   const int lane = threadIdx.x & 63, wave = scalar_i(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
-  const int tb = scalar_i((uint32_t)blockIdx.x / (uint32_t)a.col_units);
-  const int n0 = ((int)blockIdx.x - tb * a.col_units) * kOut, t0 = tb * 16;
+  // Workgroup b runs on XCD b % 8: an XCD takes neighbouring weight rows for all tokens,
+  // so that its L2 holds an eighth of the weights.
+  const int blocks = (a.rows + 15) / 16, units = a.col_units * blocks, per = (units + 7) / 8;
+  const int u = scalar_i((int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3));
+  if ((int)(blockIdx.x >> 3) >= per || u >= units) return;
+  const int nb = scalar_i((uint32_t)u / (uint32_t)blocks);
+  const int n0 = nb * kOut, t0 = (u - nb * blocks) * 16;
   const int64_t ld = (int64_t)a.c_ld * 2;  // bytes of a row, of both operands
   const ex_i32x4 wbuf = buffer_at(scalar_u64((uint64_t)(uintptr_t)a.c + n0 * ld),
                                   (int64_t)scalar_u64((uint64_t)((a.cols - n0) * ld)));
@@ -517,7 +522,7 @@ hipError_t launch_stream(ProductArgs a, hipStream_t s) {
   a.cols = kAct == kActSwiglu ? 2 * a.e.N : a.e.N;
   a.col_units = (a.e.N + kOut - 1) / kOut;
   hipLaunchKernelGGL((stream_kernel<kW, kAct>),
-                     dim3((unsigned)(a.col_units * ((a.rows + 15) / 16))),
+                     dim3((unsigned)((a.col_units * ((a.rows + 15) / 16) + 7) / 8 * 8)),
                      dim3(kStreamWaves * 64), 0, s, a);
   return hipGetLastError();
 }
