@@ -311,14 +311,25 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
           }
 }
 
-template <int kStart = 1>
-__device__ __forceinline__ int better_candidates(double c, uint32_t id) {
+// How many of the row's 16 candidates come before the lane's. A softmax's choices
+// rest on a float sum, off by 2^-19 of it at most (16 + 4 additions and the terms'
+// own errors), which moves two choices apart by as much of the scores' difference:
+// doubt, where that decides. (Equal logits have equal scores whatever the sum.)
+template <bool kDoubt, int kStart = 1>
+__device__ __forceinline__ int better_candidates(double c, float p, float x, uint32_t id,
+                                                 bool &doubt) {
   if constexpr (kStart >= 16) {
     return 0;
   } else {
     const double o = dpp_d<0x120 + kStart>(c);
     const uint32_t oid = dpp_u<0x120 + kStart>(id);
-    return (o > c || (o == c && oid < id)) + better_candidates<kStart + 1>(c, id);
+    if (kDoubt) {
+      const float op = dpp_f<0x120 + kStart>(p);
+      const bool same = dpp_f<0x120 + kStart>(x) == x;
+      doubt |= !same & (fabs(o - c) <= (double)(0x1p-18f * (fabsf(op - p) + 0x1p-22f * p)));
+    }
+    return (o > c || (o == c && oid < id)) +
+           better_candidates<kDoubt, kStart + 1>(c, p, x, id, doubt);
   }
 }
 
@@ -508,12 +519,17 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) 
     const int id = my_key ? my_lane * V + (int)(kPlace - (my_key & kPlace)) : E + c;
     const float xc = gate_load(a.x, row + min(id, E - 1), a.bf16);
     double d = xc;
+    float score = 0.0f;
     if (a.bias) {
-      d = 1.0 / (1.0 + exp(-(double)xc)) + (double)a.bias[min(id, E - 1)];
-      if (!kSig) unsure = unsure || here;
+      const double e = exp(kSig ? -(double)xc : (double)xc - (double)top);
+      d = kSig ? 1.0 / (1.0 + e) : e / (double)sum;
+      score = (float)d;
+      d += (double)a.bias[min(id, E - 1)];
     }
     if (!my_key) d = -INFINITY;
-    const int rank = better_candidates(d, (uint32_t)id);
+    bool doubt = false;
+    const int rank = better_candidates<!kSig>(d, score, xc, (uint32_t)id, doubt);
+    unsure |= here && doubt && !exact;
     if (here) {
       place = rank;
       // the last candidate bounds those that are none
