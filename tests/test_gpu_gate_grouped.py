@@ -229,3 +229,16 @@ def test_groups_too_near_to_tell(capi, flags):
     check(capi, torch.from_numpy(x), None, 6, 8, 4, flags)
     check(capi, torch.from_numpy(x), np.full(256, 0.125, np.float32), 6, 8, 4, flags)
     check(capi, torch.from_numpy(x).to(torch.bfloat16), None, 6, 8, 4, flags)
+
+
+@pytest.mark.parametrize("flags", [0, SUM2, REN])
+@pytest.mark.parametrize("E,G,KG", [(256, 8, 4), (64, 1, 1), (96, 3, 2)])
+def test_softmax_choices_a_float_merges(capi, flags, E, G, KG):
+    """Biases that make up for all but the last bits of a softmax."""
+    rng = np.random.default_rng(91)
+    y = (rng.standard_normal((16, E)) * 1.5).astype(np.float32)
+    y[1:8] = y[0]
+    e = np.exp(y[0].astype(np.float64) - y[0].max())
+    bias = (0.5 - e / e.sum()).astype(np.float32)
+    check(capi, torch.from_numpy(y), bias, 6, G, KG, flags)
+    check(capi, torch.from_numpy(y).to(torch.bfloat16), bias, 6, G, KG, flags)
