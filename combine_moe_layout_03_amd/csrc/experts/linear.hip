@@ -300,18 +300,21 @@ __global__ __launch_bounds__(256, kRT * kCT > 32 ? 1 : 2) void product_kernel(Pr
   static_assert(4 * 32 * kPitch <= sizeof(lds), "the rows fit");
   uint8_t *const mine = lds + wave * (32 * kPitch);
   const int n0 = (col0 + wc * kCT * 16) / (kPairs ? 2 : 1);
+  auto row = [&](int p) { return (p * 64 + lane) / kPer; };
+  auto col = [&](int p) { return (p * 64 + lane) % kPer * 8; };  // of the wave's
+  ex_u32x4 res[kRT / 2][kPasses];  // all of the residual at once: one wait for memory
+  if (a.splits == 1 && a.e.residual) {
+#pragma unroll
+    for (int i = 0; i < kRT / 2; ++i)
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p)
+        res[i][p] = linear_residual(
+            a.e, min(row0 + (wr * kRT + 2 * i) * 16 + (int64_t)row(p), (int64_t)a.rows - 1),
+            min(n0 + col(p), a.e.N - 8));
+  }
   each<kRT / 2>([&](auto pair) {
     constexpr int i = 2 * pair.value;
     const int64_t t0 = row0 + (wr * kRT + i) * 16;
-    auto row = [&](int p) { return (p * 64 + lane) / kPer; };
-    auto col = [&](int p) { return (p * 64 + lane) % kPer * 8; };  // of the wave's
-    ex_u32x4 res[kPasses];
-    if (a.splits == 1) {
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p)
-        res[p] = linear_residual(a.e, min(t0 + row(p), (int64_t)a.rows - 1),
-                                 min(n0 + col(p), a.e.N - 8));
-    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -320,12 +323,18 @@ __global__ __launch_bounds__(256, kRT * kCT > 32 ? 1 : 2) void product_kernel(Pr
             acc[i + h][j];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
+    f32x8 zs[kPasses], ups[kPairs ? kPasses : 1];
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
       // a pair's blocks of 16 stand next to each other
       const int c = kPairs ? (col(p) & ~15) * 2 + (col(p) & 15) : col(p);
       const float *from = reinterpret_cast<const float *>(mine + row(p) * kPitch) + c;
-      const f32x8 z = two_of(from), up = kPairs ? two_of(from + 16) : z;
+      zs[p] = two_of(from);
+      if (kPairs) ups[p] = two_of(from + 16);
+    }
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const f32x8 z = zs[p], up = kPairs ? ups[p] : z;
       const int64_t t = t0 + row(p);
       const int n = n0 + col(p);
       if (t >= a.rows || n >= a.e.N) continue;
@@ -339,7 +348,7 @@ __global__ __launch_bounds__(256, kRT * kCT > 32 ? 1 : 2) void product_kernel(Pr
           *reinterpret_cast<f32x4 *>(o + a.e.N + 4) = f32x4{up[4], up[5], up[6], up[7]};
         }
       } else {
-        linear_store<kAct>(a.e, t, n, z, up, res[p]);
+        linear_store<kAct>(a.e, t, n, z, up, res[pair.value][p]);
       }
     }
     __builtin_amdgcn_wave_barrier();
