@@ -133,7 +133,7 @@ hipError_t launch_act_grad(int32_t T, int32_t N, const uint16_t *d_out, const ui
   const ActGradArgs a{reinterpret_cast<const ex_u32x4 *>(d_out),
                       reinterpret_cast<const ex_u32x4 *>(z),
                       reinterpret_cast<ex_u32x4 *>(d_z),
-                      d_bias ? ws : nullptr,
+                      !d_bias ? nullptr : runs == 1 ? d_bias : ws,
                       T,
                       nv,
                       run};
@@ -145,7 +145,7 @@ hipError_t launch_act_grad(int32_t T, int32_t N, const uint16_t *d_out, const ui
     default: hipLaunchKernelGGL(act_grad_kernel<kActSwiglu>, grid, block, 0, s, a);
   }
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !d_bias) return e;
+  if (e != hipSuccess || !d_bias || runs == 1) return e;  // one run's sums are the result
   return launch_column_sum(ws, runs, N * halves, d_bias, s);
 }
 

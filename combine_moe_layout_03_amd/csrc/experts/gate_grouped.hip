@@ -8,9 +8,10 @@
 // other, for the usual shapes, takes four tokens a wave, orders floats and goes back
 // to 64 bits only where two are too near to be told apart. 8192 tokens x 256 experts,
 // 8 groups, top 8: 25 us by the first, 8.3 by the second, of which a launch is 1.6;
-// bound by instructions (about 1000 for four tokens, at two waves a SIMD) and their
-// latencies. Where a batch holds a token that has to be done again (about one in 8000:
-// two groups' sums within 3e-6), the call ends about 4 us later. 16 tokens: 5 us.
+// bound by instructions (1100 for four tokens, at two waves a SIMD) and their
+// latencies. Near choices cost little (one token in 100 has some among its best, one
+// in 8000 two groups on the border), a token that is done again 4 us at the call's
+// end. 16 tokens: 5 us.
 #include "gate.hpp"
 
 #include <type_traits>
@@ -219,8 +220,9 @@ __global__ __launch_bounds__(256) void gate_grouped_kernel(GroupArgs a) {
 // L lanes. Choices are floats here, and their keys give up their lowest bits to the
 // expert's place in its lane. That orders all but neighbours closer than `near`: the
 // exact order of those is settled among the token's 16 best candidates, one a
-// lane, by their doubles; and where that does not reach (groups too close, more
-// candidates within reach, a softmax's bias) the token is done again by exact_token.
+// lane, by their doubles, and of groups by their best two's; where that does not reach
+// (more candidates or groups within reach, a softmax's sum in doubt) the token is done
+// again by exact_token.
 
 __device__ __forceinline__ float row_sum16(float x) {
   x += dpp_f<0x128>(x);

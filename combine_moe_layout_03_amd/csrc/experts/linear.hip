@@ -53,16 +53,18 @@ struct ProductArgs {
 // clocks that its products take; with eight waves of 128 x 64 it would be 1536), and
 // LDS is free for the stage after next as soon as the second half is in registers.
 //
-// What bounds it: 8192 x 4096 x 7168 take 330 us (1450 TFLOP/s; a library product of
-// this size 300 to 310), the gradients 368 and 364 (370 to 390, 490 to 500): the matrix
-// units are busy 60% of the clocks at 1.9 GHz, where the GPU's power holds them. About
-// 9 us go around every tile: its start, and its sums on their way out. 8192 x 7168 x
-// 2048 198 us, with bias and residual 226 (176 to 181).
+// What bounds it: 8192 x 4096 x 7168 take 314 to 330 us on different GPUs of this kind
+// (1450 to 1530 TFLOP/s; a library product of this size 294 to 308), the gradients 347
+// to 365 both (362 to 385, 488): the matrix units are busy 60% of the clocks at 1.9 GHz,
+// where the GPU's power holds them. About 9 us go around every tile: its start, and its
+// sums on their way out. 8192 x 7168 x 2048 186 to 193 us, with bias and residual 214 to
+// 220 (171 to 180 without).
 // Measured and not kept (us, beside the kernel of that time): copies issued in one
 // half of a stage for the next one 364 against 346; reads and copies in clumps before
 // every eight products 351 against 338; tiles taken in turn by resident workgroups that
 // start the next one's copies before they store 203 against 198; panels of 2, 6 or 8
-// tiles, other places for the two barriers: within 2%.
+// tiles, other places for the two barriers: within 2%; products of 32 x 32 x 16 360
+// against 337; sums stored past L2 1% less for bf16 and 2 to 10% more for float.
 //
 // An operand stage in LDS. Along k: rows of 128 bytes, the 16-byte chunk c of
 // row r at chunk c ^ (r & 7). Across k: 64 rows (k) of the tile's width, the

@@ -391,12 +391,15 @@ hipError_t launch_rms_norm(int32_t T, int32_t H, const uint16_t *x, const uint16
 }
 
 // Workgroups of the gradient, and so rows of partial sums: two for every CU, as
-// far as there are rows and the partial sums stay within kMaxWorkspace.
+// far as there are rows and the partial sums stay within kMaxWorkspace. Up to four
+// rows (of workgroups) are one workgroup's, whose sums are the weight's gradient
+// itself: 2 us more for it, a second launch less.
 int32_t norm_grad_blocks(int32_t T, int32_t H) {
   const Spread sp = spread(T, H / 8);
   const int64_t rows = sp.waves == 1 ? ((int64_t)T + 3) / 4 : T;
   int64_t n = sp.waves == 16 && sp.v > 1 ? 256 : 512;
   if (n > rows) n = rows;
+  if (rows <= 4) n = 1;
   if (n > kMaxWorkspace / 4 / H) n = kMaxWorkspace / 4 / H;
   return (int32_t)n;
 }
@@ -404,19 +407,21 @@ int32_t norm_grad_blocks(int32_t T, int32_t H) {
 hipError_t launch_rms_norm_grad(int32_t T, int32_t H, const uint16_t *sum, const uint16_t *weight,
                                 float eps, const uint16_t *d_y, const uint16_t *d_sum,
                                 uint16_t *d_x, float *d_weight, float *ws, hipStream_t s) {
+  const int32_t blocks = norm_grad_blocks(T, H);
+  // (the kernel stores its sums in vectors)
+  const bool direct = blocks == 1 && (reinterpret_cast<uintptr_t>(d_weight) & 15u) == 0;
   const NormGradArgs a{reinterpret_cast<const ex_u32x4 *>(sum),
                        reinterpret_cast<const ex_u32x4 *>(weight),
                        reinterpret_cast<const ex_u32x4 *>(d_y),
                        reinterpret_cast<const ex_u32x4 *>(d_sum),
                        reinterpret_cast<ex_u32x4 *>(d_x),
-                       d_weight ? ws : nullptr,
+                       !d_weight ? nullptr : direct ? d_weight : ws,
                        T,
                        H / 8,
                        (float)H,
                        eps};
-  const int32_t blocks = norm_grad_blocks(T, H);
   const hipError_t e = norm_grad_launch(a, spread(T, a.nv), blocks, s);
-  if (e != hipSuccess || !d_weight) return e;
+  if (e != hipSuccess || !d_weight || direct) return e;
   return launch_column_sum(ws, blocks, H, d_weight, s);
 }
 #undef MOE_BY_SPREAD

@@ -290,3 +290,23 @@ def test_streams_and_splits(capi, T, N, C, act):
     """Few rows, and parts of long sums joined: the same bits every time."""
     a = check(capi, T, N, C, act, True, True, False, False)
     assert torch.equal(a, check(capi, T, N, C, act, True, True, False, False))
+
+
+@pytest.mark.parametrize("T", [1, 8, 9])
+@pytest.mark.parametrize("act", ["silu", "swiglu"])
+def test_bias_gradient_of_few_rows(capi, T, act):
+    """One run's sums are the result; it starts at any float."""
+    N = 520
+    NN = 2 * N if act == "swiglu" else N
+    g = torch.Generator(device=dev()).manual_seed(T)
+    d, z = rows(g, T, N, 0.02), rows(g, T, NN, 1.5)
+    b = torch.full((NN + 8,), float("nan"), device=dev())
+    dz = torch.empty(T, NN, dtype=torch.bfloat16, device=dev())
+    k = ACTS.index(act)
+    _, ws = workspace(capi.moe_linear_act_grad_workspace_bytes(T, N, k))
+    capi.moe_linear_act_grad(T, N, d, z, dz, b[1:1 + NN], k, ws)
+    want = ref.act_grad64(z.double(), d.double(), act, N)
+    mag = ref.act_grad64(z.double().abs(), d.double().abs(), act, N).abs() + want.abs()
+    tol = ((24 + 2 * z.double().abs() ** 2) * EPS24 * mag + 80 * EPS24 * want.abs()).sum(0) + 1e-38
+    assert bool(((b[1:1 + NN].double() - want.sum(0)).abs() <= tol).all())
+    assert bool(torch.isnan(b[:1]).all()) and bool(torch.isnan(b[1 + NN:]).all())

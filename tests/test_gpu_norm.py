@@ -225,3 +225,20 @@ def test_empty(capi):
     dw = torch.full((256,), 3.0, device=dev())
     capi.moe_rms_norm_grad(0, 256, e, w, EPS, e, None, e, dw)
     assert bool((dw == 0).all())
+
+
+@pytest.mark.parametrize("T,H", [(1, 4096), (3, 4096), (4, 7168), (5, 7168), (9, 512), (17, 512),
+                                 (2, 20480)])
+@pytest.mark.parametrize("off", [0, 1])
+def test_grad_of_few_rows(capi, T, H, off):
+    """One workgroup's sums are the result; also where the result starts at any float."""
+    x, _, w = inputs(T, H, T)
+    g = torch.Generator(device=dev()).manual_seed(8)
+    dy = (torch.randn(T, H, generator=g, device=dev()) * 0.02).to(torch.bfloat16)
+    b = torch.full((H + 8,), float("nan"), device=dev())
+    dw, dx = b[off:off + H], torch.empty_like(x)
+    ws = torch.empty(capi.moe_rms_norm_grad_workspace_bytes(T, H), dtype=torch.uint8, device=dev())
+    capi.moe_rms_norm_grad(T, H, x, w, EPS, dy, None, dx, dw, ws)
+    _, _, want, total = grads64(x, w, dy, None)
+    assert bool(((dw.double() - want).abs() <= (T + 64) * EPS24 * total + DEPTH * total).all())
+    assert bool(torch.isnan(b[off + H:]).all()) and bool(torch.isnan(b[:off]).all())
