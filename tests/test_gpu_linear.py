@@ -310,3 +310,56 @@ def test_bias_gradient_of_few_rows(capi, T, act):
     tol = ((24 + 2 * z.double().abs() ** 2) * EPS24 * mag + 80 * EPS24 * want.abs()).sum(0) + 1e-38
     assert bool(((b[1:1 + NN].double() - want.sum(0)).abs() <= tol).all())
     assert bool(torch.isnan(b[:1]).all()) and bool(torch.isnan(b[1 + NN:]).all())
+
+
+def test_past_32_bits(capi):
+    """Rows, results and sums of more than 4 GiB."""
+    T, N, C = 540001, 8, 4104
+    g = torch.Generator(device=dev()).manual_seed(4)
+    x = torch.empty(T, C, dtype=torch.bfloat16, device=dev())
+    for at in torch.arange(T, device=dev()).split(65536):
+        x[at] = torch.randn(len(at), C, generator=g, device=dev()).to(torch.bfloat16)
+    w, d = rows(g, N, C, C ** -0.5), rows(g, T, N, 0.02)
+    _, ws = workspace(capi.MOE_WORKSPACE_MAX_BYTES)
+    out = torch.full((T, N), float("nan"), device=dev())
+    capi.moe_linear(T, N, C, x, w, None, None, out, None, F32, ws)
+    dx = torch.full((T, C), float("nan"), dtype=torch.bfloat16, device=dev())
+    dw = torch.empty(N, C, device=dev())
+    capi.moe_linear_grad(T, N, C, d, x, w, dx, dw, ws)
+    want = torch.zeros(N, C, dtype=torch.float64, device=dev())
+    mag = torch.zeros_like(want)
+    for at in torch.arange(T, device=dev()).split(65536):
+        z, err = ref.dot_bound(x[at], w)
+        assert bool(((out[at].double() - z).abs() <= err).all())
+        z, err = ref.dot_bound(d[at], w.t())
+        assert bool(((dx[at].double() - z).abs() <= HALF_BF16 * z.abs() + 1.01 * err + 1e-38).all())
+        p, q = d[at].double().t().contiguous(), x[at].double()
+        want += p @ q
+        mag += p.abs() @ q.abs()
+    assert bool(((dw.double() - want).abs() <= (T / 8 + 80) * 2 * EPS24 * mag).all())
+    # the sums' errors are random: within a thousandth of that bound in the mean
+    assert float((dw.double() - want).norm() / want.norm()) < 1e-4
+
+
+def test_act_grad_past_32_bits(capi):
+    T, N = 262145, 4104
+    g = torch.Generator(device=dev()).manual_seed(5)
+    z, d = (torch.empty(T, 2 * N, dtype=torch.bfloat16, device=dev()),
+            torch.empty(T, N, dtype=torch.bfloat16, device=dev()))
+    for at in torch.arange(T, device=dev()).split(32768):
+        z[at] = torch.randn(len(at), 2 * N, generator=g, device=dev()).to(torch.bfloat16)
+        d[at] = torch.randn(len(at), N, generator=g, device=dev()).to(torch.bfloat16)
+    dz = torch.full_like(z, float("nan"))
+    db = torch.empty(2 * N, device=dev())
+    _, ws = workspace(capi.moe_linear_act_grad_workspace_bytes(T, N, 3))
+    capi.moe_linear_act_grad(T, N, d, z, dz, db, 3, ws)
+    total, mags = 0, 0
+    for at in torch.arange(T, device=dev()).split(16384):
+        v = z[at].double()
+        want = ref.act_grad64(v, d[at].double(), "swiglu", N)
+        mag = ref.act_grad64(v.abs(), d[at].double().abs(), "swiglu", N).abs() + want.abs()
+        one = (24 + 2 * v.abs() ** 2) * EPS24 * mag
+        assert bool(((dz[at].double() - want).abs() <= HALF_BF16 * want.abs() + one + 1e-38).all())
+        total = total + want.sum(0)
+        mags = mags + (one + (T / 4 + 64) * EPS24 * want.abs()).sum(0)
+    assert bool(((db.double() - total).abs() <= mags).all())

@@ -242,3 +242,31 @@ def test_grad_of_few_rows(capi, T, H, off):
     _, _, want, total = grads64(x, w, dy, None)
     assert bool(((dw.double() - want).abs() <= (T + 64) * EPS24 * total + DEPTH * total).all())
     assert bool(torch.isnan(b[off + H:]).all()) and bool(torch.isnan(b[:off]).all())
+
+
+def test_past_32_bits(capi):
+    """Rows of more than 4 GiB, with codes and their gradient."""
+    T, H = 300001, 8192
+    g = torch.Generator(device=dev()).manual_seed(3)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=dev())
+    for at in torch.arange(T, device=dev()).split(32768):
+        x[at] = torch.randn(len(at), H, generator=g, device=dev()).to(torch.bfloat16)
+    w = (1 + 0.3 * torch.randn(H, generator=g, device=dev())).to(torch.bfloat16)
+    y = torch.full_like(x, float("nan"))
+    q = torch.zeros(T, H, dtype=torch.float8_e4m3fn, device=dev())
+    s = torch.empty(T, H // 128, device=dev())
+    capi.moe_rms_norm(T, H, x, None, w, EPS, None, y, q, s)
+    dx, dw = torch.empty_like(x), torch.empty(H, device=dev())
+    ws = torch.empty(capi.moe_rms_norm_grad_workspace_bytes(T, H), dtype=torch.uint8, device=dev())
+    capi.moe_rms_norm_grad(T, H, x, w, EPS, y, None, dx, dw, ws)
+    want, total = 0, 0
+    for at in torch.arange(T, device=dev()).split(16384):
+        _, v, _ = y64(x[at], w)
+        assert bool(((y[at].double() - v).abs() <= (HALF_BF16 + DEPTH) * v.abs()).all())
+        t = v.view(len(at), -1, 128) / s[at].double()[..., None]
+        off = (q[at].float().double().view_as(t) - t).abs()
+        assert bool((off <= 2.0 ** -4 * t.abs().clamp_min(2.0 ** -6) + 4 * DEPTH * t.abs()).all())
+        d, mag, a, b = grads64(x[at], w, y[at], None)
+        assert bool(((dx[at].double() - d).abs() <= HALF_BF16 * d.abs() + 4 * DEPTH * mag).all())
+        want, total = want + a, total + b
+    assert bool(((dw.double() - want).abs() <= (600 + 64) * EPS24 * total + DEPTH * total).all())
