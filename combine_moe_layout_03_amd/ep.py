@@ -503,8 +503,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
              round_scale: bool = False, use_ue8m0: bool = False):
     """Residual addition and root-mean-square norm of rows x [T, H] bf16:
     (y [T, H] bf16, sum [T, H] bf16, fp8). sum = x + residual, x itself without
-    one; fp8 is the (codes, row-major scales) tuple of y that ``dispatch`` and, with
-    a handle of one expert, ``expert_gemm`` take, None without use_fp8."""
+    one; fp8 is the (codes, row-major scales) tuple of y that ``dispatch`` (with
+    float scales) and, with a handle of one expert, ``expert_gemm`` take, None
+    without use_fp8."""
     x = _rows(x, "x")
     T, H = x.shape
     residual = _like(residual, x.shape, "residual")
