@@ -434,8 +434,12 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(ProductArgs a
 #pragma unroll
     for (int i = 0; i < 2; ++i) copy16_bounded(tbuf, (t_off[i] + more) | mask, to + i * 1024);
 #pragma unroll
-    for (int i = 0; i < kW / 8; ++i)
-      copy16_bounded_once(wbuf, (w_off[i] + more) | mask, to + 2048 + i * 1024);
+    for (int i = 0; i < kW / 8; ++i) {
+      if (blocks == 1)  // uniform
+        copy16_bounded_once(wbuf, (w_off[i] + more) | mask, to + 2048 + i * 1024);
+      else  // the next tokens' workgroups read them again
+        copy16_bounded(wbuf, (w_off[i] + more) | mask, to + 2048 + i * 1024);
+    }
   };
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
