@@ -388,8 +388,8 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
 // join their sums at the end.
 //
 // 16 tokens, 7168 to 4096 channels: 11.3 us, 5.2 TB/s of weights (they come through L2
-// beside as many bytes of tokens); 128 tokens, 7168 to 256: 7.4 us (13.4 as split tiles),
-// 33 bytes a clock into a CU. Rings of 2, 3, 4 or 8 groups and 4, 8 or 16 waves: within
+// beside as many bytes of tokens); 128 tokens, 7168 to 256: 7.0 us (13.4 as split tiles),
+// about 35 bytes a clock into a CU. Rings of 2, 3, 4 or 8 groups and 4, 8 or 16 waves: within
 // 5%, but for those that leave a CU one workgroup, slower where there are more.
 
 constexpr int kStreamWaves = 4, kStreamRing = 4;
@@ -435,9 +435,9 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(ProductArgs a
     for (int i = 0; i < 2; ++i) copy16_bounded(tbuf, (t_off[i] + more) | mask, to + i * 1024);
 #pragma unroll
     for (int i = 0; i < kW / 8; ++i) {
-      if (blocks == 1)  // uniform
+      if (blocks == 1)  // 16 x 4096 of 7168 channels 12.6 us, unmarked 13.6
         copy16_bounded_once(wbuf, (w_off[i] + more) | mask, to + 2048 + i * 1024);
-      else  // the next tokens' workgroups read them again
+      else  // the other tokens' workgroups read them too (128 x 256: 7.05 us, marked 8.0)
         copy16_bounded(wbuf, (w_off[i] + more) | mask, to + 2048 + i * 1024);
     }
   };
@@ -520,15 +520,18 @@ Plan plan(int64_t rows, int64_t cols, int64_t k, bool pairs) {
 }
 
 // Whether a product is streamed, its rows in blocks of 16 that each read the weights
-// again: with one block always; with more while all that is read is less than 2.75
-// million channels of 32 rows. (At 7168 channels, streamed against tiles: 256 units of
-// 16 x 16 8.4 against 13.6 us, 512 units 17.3 against 14 to 16; at 1024 channels 512
-// units 4.1 against 9.9.) The second half of a SwiGLU's weights has to be within
+// again: with one block of 1024 channels or more always; else where its units of 16 x 16
+// are at most 1024 (two rounds of two to a CU) and what they read is at most 3.7 million
+// channels of 32 rows. Streamed against tiles, us: 1024 units of 256 channels 5.2 and 6.4,
+// 2048 of them 8.9 and 6.6; 1024 units of 512 or 2048 channels 5.9 and 8.2, 10.4 and 12.6;
+// 768 of 4096 14.9 and 16.4, 1024 of them 18.6 to 21 and 17.4; 512 of 7168 16 to 20 and 18
+// to 20, 640 of them 23 and 20; 16 rows x 65536 of 256 or 512 channels 20 and 11, 24 and 18,
+// 16 x 32768 of 2048: 27 and 36. The second half of a SwiGLU's weights has to be within
 // reach of a 32-bit offset.
 bool streamed(int64_t rows, int64_t N, int64_t k, bool pairs) {
   if (pairs && (N + 16) * k * 2 >= 0xffffffe0ll) return false;
   const int64_t units = (rows + 15) / 16 * ((N * (pairs ? 2 : 1) + 15) / 16);
-  return rows <= 16 || units * k <= 2750000;
+  return (rows <= 16 && k >= 1024) || (units <= 1024 && units * k <= 3700000);
 }
 
 template <int kW, int kAct>
@@ -542,14 +545,14 @@ hipError_t launch_stream(ProductArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Eight weight rows a workgroup where sixteen leave CUs without one (7168 channels, 16
-// rows x 256: 7.5 against 9.5 us, 128 x 256: 7.4 against 8.8, 16 x 2048: 8.7 against 10.2;
-// 16 x 4096, where they do not, 15.1 against 11.3).
+// Eight weight rows a workgroup where that is one for every CU at most (7168 channels, 16
+// rows x 256: 7.8 against 10.1 us, 128 x 256: 7.0 against 8.1, 16 x 2048: 9.5 against 11.1;
+// 16 x 2304, 128 x 288, where it is not, 14.9 against 11.3 and 9.9 against 8.0).
 template <int kAct>
 hipError_t launch_streamed(const ProductArgs &a, hipStream_t s) {
   const int64_t rows = (a.rows + 15) / 16, w = kAct == kActSwiglu ? 2 * (int64_t)a.e.N : a.e.N;
-  return rows * ((w + 15) / 16) < 256 ? launch_stream<8, kAct>(a, s)
-                                      : launch_stream<16, kAct>(a, s);
+  return rows * ((w + 7) / 8) <= 256 ? launch_stream<8, kAct>(a, s)
+                                     : launch_stream<16, kAct>(a, s);
 }
 
 template <bool kRAcross, bool kCAcross, int kAct>

@@ -292,6 +292,16 @@ def test_streams_and_splits(capi, T, N, C, act):
     assert torch.equal(a, check(capi, T, N, C, act, True, True, False, False))
 
 
+@pytest.mark.parametrize("T,N,C", [(16, 16384, 264), (16, 16392, 264), (5, 16400, 1016),
+                                   (5, 16400, 1024), (512, 512, 256), (500, 528, 256),
+                                   (128, 1024, 7168), (125, 1032, 7168), (1024, 256, 3616),
+                                   (16, 2048, 1032), (9, 2056, 1032), (33, 680, 264), (40, 688, 264)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_border_of_streams_and_tiles(capi, T, N, C, act):
+    """The last sizes that are streamed and the first that are not."""
+    check(capi, T, N, C, act, True, True, False, act != "none")
+
+
 @pytest.mark.parametrize("T", [1, 8, 9])
 @pytest.mark.parametrize("act", ["silu", "swiglu"])
 def test_bias_gradient_of_few_rows(capi, T, act):
