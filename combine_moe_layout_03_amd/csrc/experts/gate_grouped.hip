@@ -420,10 +420,14 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) 
     if (lanes > 2) best_two<0x4E>(g1, g2);
     if (lanes > 4) best_two<0x141>(g1, g2);
     if (lanes > 8) best_two<0x140>(g1, g2);
-    const float s = sums && g2 != -INFINITY ? g1 + g2 : g1;
+    // Choices are compared as quarters, so that neither the sum of two nor a tolerance
+    // beside it passes the float range; logits as they stand.
+    const bool chosen = a.bias || sums;
+    float s = g1;
+    if (chosen) s = 0.25f * g1 + (sums && g2 != -INFINITY ? 0.25f * g2 : 0.0f);
     // (a sum of two scores with their biases is off by twice what a choice is, without
     // places: 2^-20 + 2^-23 of it)
-    const float tol = !(a.bias || sums) || s == -INFINITY ? 0.0f : 0x1p-19f * largest + 0x1p-21f * fabsf(s);
+    const float tol = !chosen || s == -INFINITY ? 0.0f : 0x1p-21f * largest + 0x1p-21f * fabsf(s);
     int sure = 0, maybe = 0;
     switch (lanes) {
       case 1: better_groups<1>(s, tol, sure, maybe); break;
