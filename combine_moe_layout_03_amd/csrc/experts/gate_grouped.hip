@@ -254,15 +254,17 @@ __device__ __forceinline__ void best_two(float &m1, float &m2) {
   m1 = fmaxf(m1, o1);
 }
 
-// How many groups of the row score more than the lane's by more than tol, and by
-// more than -tol; of equal ones the first scores more.
+// How many groups of the row score more than the lane's by more than the scores may be
+// off (tol, each group's own), and by more than less that; of equal ones the first
+// scores more.
 template <int L, int kStart = L>
 __device__ __forceinline__ void better_groups(float s, float tol, int &sure, int &maybe) {
   if constexpr (kStart < 16) {
     const float o = dpp_f<0x120 + kStart>(s);  // of lane c - kStart, around the row
+    const float both = tol + dpp_f<0x120 + kStart>(tol);
     const bool first = (int)(threadIdx.x & 15) >= kStart;
-    sure += (o > s + tol) | (first & (o == s + tol));
-    maybe += (o > s - tol) | (first & (o == s - tol));
+    sure += (o > s + both) | (first & (o == s + both));
+    maybe += (o > s - both) | (first & (o == s - both));
     better_groups<L, kStart + L>(s, tol, sure, maybe);
   }
 }
@@ -274,18 +276,19 @@ __device__ __forceinline__ void best_two_d(double &m1, double &m2) {
   m1 = fmax(m1, o1);
 }
 
-// How many groups score more than the lane's, those within tol of it by their doubles.
+// How many groups score more than the lane's, those too near by their doubles.
 template <int L, int kStart = L>
 __device__ __forceinline__ void settle_groups(float s, float tol, double sd, bool unsure,
                                               int &better, bool &open) {
   if constexpr (kStart < 16) {
     const float o = dpp_f<0x120 + kStart>(s);
+    const float both = tol + dpp_f<0x120 + kStart>(tol);
     const double od = dpp_d<0x120 + kStart>(sd);
     const bool known = dpp_u<0x120 + kStart>(unsure) != 0u;
     const bool first = (int)(threadIdx.x & 15) >= kStart;
-    const bool near = !(o > s + tol) && !(o < s - tol);
+    const bool near = !(o > s + both) && !(o < s - both);
     open |= near & !known;
-    better += near ? (od > sd) | (first & (od == sd)) : o > s + tol;
+    better += near ? (od > sd) | (first & (od == sd)) : o > s + both;
     settle_groups<L, kStart + L>(s, tol, sd, unsure, better, open);
   }
 }
@@ -425,9 +428,15 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) 
     const bool chosen = a.bias || sums;
     float s = g1;
     if (chosen) s = 0.25f * g1 + (sums && g2 != -INFINITY ? 0.25f * g2 : 0.0f);
-    // (a sum of two scores with their biases is off by twice what a choice is, without
-    // places: 2^-20 + 2^-23 of it)
-    const float tol = !chosen || s == -INFINITY ? 0.0f : 0x1p-21f * largest + 0x1p-21f * fabsf(s);
+    // How far a group's score may be off: each of its two scores by 2^-21; by 2^-24 of
+    // each choice, which may cancel in their sum, and as much again for the sum and for
+    // the comparison; by a softmax's common sum, off by 2^-19 of it, as much of the two
+    // scores, whose biases may make up for them.
+    const float e1 = fabsf(g1), e2 = sums && g2 != -INFINITY ? fabsf(g2) : 0.0f;
+    const float tol = !chosen || s == -INFINITY
+                          ? 0.0f
+                          : 0.25f * (kSig ? 0x1p-20f : 0x1.4p-18f) * largest +
+                                (0x1p-24f * e1 + 0x1p-24f * e2);
     int sure = 0, maybe = 0;
     switch (lanes) {
       case 1: better_groups<1>(s, tol, sure, maybe); break;

@@ -40,3 +40,22 @@ def test_group_sums_past_the_float_range(capi, E, flags):
         x = logits(4, E, turn)
         x[1, n:2 * n] = -np.inf
         check(capi, x, b, 6, 8, 3, flags)
+
+
+@pytest.mark.parametrize("E,G", [(64, 16), (64, 8), (160, 8), (256, 8), (96, 8)])
+@pytest.mark.parametrize("size", [100.0, 1000.0, 10000.0])
+@pytest.mark.parametrize("flags", [SIG | SUM2, SUM2, SIG | REN | SUM2])
+def test_group_sums_that_cancel(capi, E, G, size, flags):
+    """A group's best two of opposite sign, each rounded at its own size: what is left
+    is off by many steps of its own, and the groups differ by less."""
+    rng = np.random.default_rng(E + G)
+    T, n = 48, E // G
+    b = np.full(E, -size, np.float32)
+    b[::n] = size
+    step = size * 2.0 ** -23 * (1 if flags & SIG else G)  # of a choice's float, in these units
+    first = rng.uniform(0.2, 0.8, (T, G))
+    s = np.full((T, G, n), 1e-3)
+    s[..., 0] = first
+    s[..., 1] = 1 - first + rng.uniform(0, 2, (T, G)) * step
+    x = np.log(s) - (np.log1p(-s) if flags & SIG else 0)
+    check(capi, torch.from_numpy(x.reshape(T, E).astype(np.float32)), b, 6, G, 4, flags)
