@@ -448,8 +448,9 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) 
     kept = sure < a.KG;
     unsure = kept && maybe >= a.KG;
     if (kSig && __ballot(unsure)) {  // uniform, and rare: the groups on the border in 64 bits
-      // Of a group that is unsure, the choices that may be its best two.
-      const float least = (sums ? g2 : g1) - (0x1p-18f + 0x1p-20f * fabsf(g1));
+      // Of a group that is unsure, the choices that may be its best two: those as near to
+      // the last of them as two choices may be off.
+      const float edge = sums ? g2 : g1, least = edge - (0x1p-18f + 0x1p-20f * fabsf(edge));
       double d1 = -INFINITY, d2 = -INFINITY;
 #pragma unroll
       for (int j = 0; j < V; ++j) {

@@ -59,3 +59,45 @@ def test_group_sums_that_cancel(capi, E, G, size, flags):
     s[..., 1] = 1 - first + rng.uniform(0, 2, (T, G)) * step
     x = np.log(s) - (np.log1p(-s) if flags & SIG else 0)
     check(capi, torch.from_numpy(x.reshape(T, E).astype(np.float32)), b, 6, G, 4, flags)
+
+
+def sigmoid(x):
+    return 1 / (1 + np.exp(-x.astype(np.float64)))
+
+
+def first_above(s):
+    """The least float whose sigmoid, in 64 bits, is above s."""
+    x = (np.log(s) - np.log1p(-s)).astype(np.float32)
+    while np.any(sigmoid(x) > s):
+        x = np.where(sigmoid(x) > s, np.nextafter(x, np.float32(-99), dtype=np.float32), x)
+    while np.any(sigmoid(x) <= s):
+        x = np.where(sigmoid(x) <= s, np.nextafter(x, np.float32(99), dtype=np.float32), x)
+    return x
+
+
+@pytest.mark.parametrize("first", [0, 1])
+@pytest.mark.parametrize("E", [64, 256, 96])
+def test_second_best_far_larger_than_the_best(capi, E, first):
+    """Second best choices near -1000, whose floats are 2^-14 apart, beside best ones near
+    1. Two experts of a group lie just above a border between two such floats, the larger
+    one with the score that has fewer bits left, so that its float may fall below; the
+    other group's second best lies between the two."""
+    m = (np.arange(1 << 14) + 0.5) * 2.0 ** -14
+    m = m[(m > 0.86) & (m < 0.94)]
+    low = first_above(m - 0.75 + 1e-8)
+    mid = np.nextafter(low, np.float32(99), dtype=np.float32)
+    high = first_above(sigmoid(mid) + 0.75 + 1e-9)
+    T, n = len(m), E // 2
+    x = np.full((T, 2, n), -40.0, np.float32)
+    b = np.full((2, n), -1000.0, np.float32)
+    x[:, :, 0], b[:, 0] = 2.0, 0.0
+    x[:, first, 1], b[first, 1] = high, -1000.75
+    x[:, first, 2] = low
+    x[:, 1 - first, 1] = mid
+    x = torch.from_numpy(x.reshape(T, E)).to(dev())
+    idx = torch.empty(T, 1, dtype=torch.int64, device=dev())
+    w = torch.empty(T, 1, device=dev())
+    capi.moe_gate_grouped(T, E, 1, 2, 1, x, torch.from_numpy(b.reshape(-1)).to(dev()), idx, w,
+                          SIG | SUM2)
+    wrong = int((idx != n * first).sum())
+    assert wrong == 0, (wrong, T)
