@@ -418,11 +418,10 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) 
   }
   bool unsure = false;
   bool kept = true;
-  if (a.G > 1) {
+  if (a.G > 1) {  // so a group has 1, 2, 4 or 8 lanes
     if (lanes > 1) best_two<0xB1>(g1, g2);
     if (lanes > 2) best_two<0x4E>(g1, g2);
     if (lanes > 4) best_two<0x141>(g1, g2);
-    if (lanes > 8) best_two<0x140>(g1, g2);
     // Choices are compared as quarters, so that neither the sum of two nor a tolerance
     // beside it passes the float range; logits as they stand.
     const bool chosen = a.bias || sums;
@@ -442,8 +441,7 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) 
       case 1: better_groups<1>(s, tol, sure, maybe); break;
       case 2: better_groups<2>(s, tol, sure, maybe); break;
       case 4: better_groups<4>(s, tol, sure, maybe); break;
-      case 8: better_groups<8>(s, tol, sure, maybe); break;
-      default: break;
+      default: better_groups<8>(s, tol, sure, maybe);
     }
     kept = sure < a.KG;
     unsure = kept && maybe >= a.KG;
