@@ -97,7 +97,6 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void norm_kernel(N
       if (a.sum && tid + j * kStride < a.nv) a.sum[at + tid + j * kStride] = v[j];
     }
   }
-  if (!a.y && !kFp8) return;  // uniform
   float ss = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
