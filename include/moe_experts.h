@@ -231,11 +231,12 @@ int moe_rms_norm_grad(int32_t T, int32_t H, const uint16_t *sum, const uint16_t 
  * pre [T*N] (SwiGLU [T*2N]) bf16_rne(z), for moe_linear_act_grad; NULL: not
  * written, and NULL without an activation (MOE_ERR_NULL). out and pre overlap
  * nothing else.
- * N % 8 == 0, C % 8 == 0, 8 <= N, C <= 2^20, T <= 2^26 - 64, T*N and N*C at most
+ * N % 8 == 0, C % 8 == 0, 8 <= N, C <= 2^20, T <= 2^26 - 64, T*N, T*C and N*C at most
  * 2^36 (a router of another number of experts pads its weights with rows of zeros
  * and its bias with -infinity, which masks them in moe_gate). All pointers 16-byte aligned.
- * ws: ws_bytes >= moe_linear_workspace_bytes of the same call (0 for most), 16-byte
- * aligned; calls that may run at the same time need one each. */
+ * ws: ws_bytes >= moe_linear_workspace_bytes of the same call (0 for most, and for sizes
+ * that the call refuses), 16-byte aligned; calls that may run at the same time need one
+ * each. */
 size_t moe_linear_workspace_bytes(int32_t T, int32_t N, int32_t C, int32_t flags);
 int moe_linear(int32_t T, int32_t N, int32_t C, const uint16_t *x, const uint16_t *w,
                const float *bias, const uint16_t *residual, void *out, uint16_t *pre,
@@ -246,7 +247,7 @@ int moe_linear(int32_t T, int32_t N, int32_t C, const uint16_t *x, const uint16_
  *   d_bias = sum over the rows of d_z before its rounding, in float; NULL: not computed
  * (and no workspace is needed), zeros if T = 0. Without an activation pre and d_z are NULL (d_z is
  * d_out; MOE_ERR_NULL otherwise). The residual's gradient is d_out. d_z may be
- * pre (SwiGLU too). Sizes, alignment and ws as for moe_linear. */
+ * pre (SwiGLU too). Sizes (but C), alignment and ws as for moe_linear; d_bias 4-byte aligned. */
 size_t moe_linear_act_grad_workspace_bytes(int32_t T, int32_t N, int32_t flags);
 int moe_linear_act_grad(int32_t T, int32_t N, const uint16_t *d_out, const uint16_t *pre,
                         uint16_t *d_z, float *d_bias, int32_t flags, void *ws, size_t ws_bytes,
