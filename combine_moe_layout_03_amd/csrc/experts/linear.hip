@@ -169,18 +169,15 @@ __device__ __forceinline__ bf16x8 fragment(const uint8_t *stage, int t, int kk) 
 // registers, moves sums and fragments to and fro between the two files (dw of 8192 x
 // 4096 x 7168: 461 us, with the sums held in the accumulation registers 389). It
 // still waits for the fragments it reads; that the sums are ready, products_done()
-// sees to (a product takes 8 passes of four clocks): behind its waits every sum is a
-// result of an empty statement of its own, so that no read of one moves ahead of them.
+// sees to (a product takes 8 passes of four clocks). Nothing in the source keeps a copy
+// of a sum from being placed ahead of its waits: as operands of the waits the sums are
+// copied, in part before them (204 us against 202 at 8192 x 7168 x 2048). So a test reads
+// the built code: no result read, and no operand written, within the wait states.
 __device__ __forceinline__ void product(f32x4 &acc, bf16x8 c, bf16x8 r) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(c), "v"(r));
 }
-template <int kRT, int kCT>
-__device__ __forceinline__ void products_done(f32x4 (&acc)[kRT][kCT]) {
+__device__ __forceinline__ void products_done() {
   asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < kRT; ++i)
-#pragma unroll
-    for (int j = 0; j < kCT; ++j) asm volatile("" : "+a"(acc[i][j])::"memory");
 }
 
 // 2 x 2 waves, each with kRT x kCT fragments of 16.
@@ -295,7 +292,7 @@ __global__ __launch_bounds__(256, kRT * kCT > 32 ? 1 : 2) void product_kernel(Pr
     });
   }
   __builtin_amdgcn_s_waitcnt(vmcnt(0));  // no copy outlives the workgroup
-  products_done(acc);
+  products_done();
 
   // The sums go through LDS, 32 rows of a wave at a time, so that a lane finishes eight
   // neighbouring columns: whole lines of the output and the residual.
