@@ -596,12 +596,12 @@ hipError_t gate_rows_vm(const GroupArgs &a, int lanes, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Lanes of a group where a token fits a row of 16: 4, 8, 10 or 16 experts a lane,
-// K + 1 candidates, groups of whole lanes whose number is a power of two, rows on
-// whole words. 0: a wave a token.
+// Lanes of a group where a token fits a row of 16: an even number of experts a lane
+// (whole words of bf16), at most 16 (the places in a key), K + 1 candidates, groups of
+// whole lanes whose number is a power of two, rows on whole words. 0: a wave a token.
 int row_lanes(const GroupArgs &a) {
   const int v = a.E / 16, n = a.E / a.G;
-  if (a.E % 16 || (v != 4 && v != 8 && v != 10 && v != 16) || a.K > 15 || n % v) return 0;
+  if (a.E % 32 || v > 16 || a.K > 15 || n % v) return 0;
   if (reinterpret_cast<uintptr_t>(a.x) & 3u) return 0;
   const int lanes = n / v;
   return lanes & (lanes - 1) ? 0 : lanes;
@@ -611,9 +611,13 @@ template <int kMode>
 hipError_t gate_grouped_m(const GroupArgs &a, hipStream_t s) {
   if (const int lanes = row_lanes(a)) {
     switch (a.E / 16) {
+      case 2: return gate_rows_vm<2, kMode>(a, lanes, s);
       case 4: return gate_rows_vm<4, kMode>(a, lanes, s);
+      case 6: return gate_rows_vm<6, kMode>(a, lanes, s);
       case 8: return gate_rows_vm<8, kMode>(a, lanes, s);
       case 10: return gate_rows_vm<10, kMode>(a, lanes, s);
+      case 12: return gate_rows_vm<12, kMode>(a, lanes, s);
+      case 14: return gate_rows_vm<14, kMode>(a, lanes, s);
       default: return gate_rows_vm<16, kMode>(a, lanes, s);
     }
   }

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 FLT_MAX = np.finfo(np.float32).max
 
 
-@pytest.mark.parametrize("E", [64, 128, 256, 96])  # four tokens a wave; one (96)
+@pytest.mark.parametrize("E", [64, 128, 256, 96, 112])  # four tokens a wave; one (112)
 @pytest.mark.parametrize("flags", [SIG | SUM2, SUM2, SIG | REN | SUM2])
 def test_masked_group_beside_lowest_biases(capi, E, flags):
     """Every bias the lowest float: the sum of two passes the range, and still beats a
@@ -24,7 +24,7 @@ def test_masked_group_beside_lowest_biases(capi, E, flags):
     assert (ids == n + np.arange(4)).all()
 
 
-@pytest.mark.parametrize("E", [64, 160, 256, 96])
+@pytest.mark.parametrize("E", [64, 160, 256, 96, 112])
 @pytest.mark.parametrize("flags", [SIG | SUM2, SUM2, SIG, 0])
 def test_group_sums_past_the_float_range(capi, E, flags):
     """Sums of either sign past the range differ in 64 bits, and from ordinary ones."""
@@ -42,7 +42,7 @@ def test_group_sums_past_the_float_range(capi, E, flags):
         check(capi, x, b, 6, 8, 3, flags)
 
 
-@pytest.mark.parametrize("E,G", [(64, 16), (64, 8), (160, 8), (256, 8), (96, 8)])
+@pytest.mark.parametrize("E,G", [(64, 16), (64, 8), (160, 8), (256, 8), (96, 8), (112, 8)])
 @pytest.mark.parametrize("size", [100.0, 1000.0, 10000.0])
 @pytest.mark.parametrize("flags", [SIG | SUM2, SUM2, SIG | REN | SUM2])
 def test_group_sums_that_cancel(capi, E, G, size, flags):
@@ -76,7 +76,7 @@ def first_above(s):
 
 
 @pytest.mark.parametrize("first", [0, 1])
-@pytest.mark.parametrize("E", [64, 256, 96])
+@pytest.mark.parametrize("E", [64, 256, 96, 112])
 def test_second_best_far_larger_than_the_best(capi, E, first):
     """Second best choices near -1000, whose floats are 2^-14 apart, beside best ones near
     1. Two experts of a group lie just above a border between two such floats, the larger
