@@ -429,12 +429,13 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GroupArgs a, int lanes) 
     if (chosen) s = 0.25f * g1 + (sums && g2 != -INFINITY ? 0.25f * g2 : 0.0f);
     // How far a group's score may be off: each of its two scores by 2^-21; by 2^-24 of
     // each choice, which may cancel in their sum, and as much again for the sum and for
-    // the comparison; by a softmax's common sum, off by 2^-19 of it, as much of the two
-    // scores, whose biases may make up for them.
+    // the comparison. A softmax's common sum, off by 2^-19 of it, moves two groups apart by
+    // as much of the difference of their scores, which biases may make up for: twice the
+    // largest score at most, half of it on each side.
     const float e1 = fabsf(g1), e2 = sums && g2 != -INFINITY ? fabsf(g2) : 0.0f;
     const float tol = !chosen || s == -INFINITY
                           ? 0.0f
-                          : 0.25f * (kSig ? 0x1p-20f : 0x1.4p-18f) * largest +
+                          : 0.25f * (kSig ? 0x1p-20f : 0x1.8p-19f) * largest +
                                 (0x1p-24f * e1 + 0x1p-24f * e2);
     int sure = 0, maybe = 0;
     switch (lanes) {
