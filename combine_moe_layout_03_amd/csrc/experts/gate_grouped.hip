@@ -7,11 +7,11 @@
 // do that. One takes a token a wave and computes every choice in 64 bits; the
 // other, for the usual shapes, takes four tokens a wave, orders floats and goes back
 // to 64 bits only where two are too near to be told apart. 8192 tokens x 256 experts,
-// 8 groups, top 8: 25 us by the first, 8.3 by the second, of which a launch is 1.6;
-// bound by instructions (1100 for four tokens, at two waves a SIMD) and their
+// 8 groups, top 8: 22 us by the first, 8.5 by the second, of which a launch is 1.6;
+// bound by instructions (1155 for four tokens, at two waves a SIMD) and their
 // latencies. Near choices cost little (one token in 100 has some among its best, one
 // in 8000 two groups on the border), a token that is done again 4 us at the call's
-// end. 16 tokens: 5 us.
+// end. 16 tokens: 9.2 and 4.8 us.
 #include "gate.hpp"
 
 #include <type_traits>
@@ -72,10 +72,8 @@ struct GroupArgs {
   int32_t *status;
 };
 
-// What a choice is compared by: the logit itself without a bias (as moe_gate
-// compares), else score + bias as a double.
-//
-// One token, in one wave: expert e = lane + 64 * j in register j, choices as doubles.
+// One token, in one wave: expert e = lane + 64 * j in register j. Its choice is the
+// logit itself without a bias (as moe_gate compares), else score + bias as a double.
 // `choices` is LDS of 64 V keys of the wave's own.
 template <int V, int kMode>
 __device__ void exact_token(const GroupArgs &a, int t, uint64_t *choices, bool *bad) {
@@ -600,6 +598,9 @@ hipError_t gate_rows_vm(const GroupArgs &a, int lanes, hipStream_t s) {
 // Lanes of a group where a token fits a row of 16: an even number of experts a lane
 // (whole words of bf16), at most 16 (the places in a key), K + 1 candidates, groups of
 // whole lanes whose number is a power of two, rows on whole words. 0: a wave a token.
+// 8192 tokens, us, four a wave and one: 32 experts 5.6 and 10.7, 64 6.4 and 12.2, 96 6.8
+// and 15.8, 128 7.1 and 16.1, 160 7.5 and 20.6, 192 7.7 and 21.7, 224 8.2 and 22.3, 256 8.5
+// and 22.1; 16 tokens x 256 4.8 and 9.2. More experts, one token a wave: 320 33, 512 36.
 int row_lanes(const GroupArgs &a) {
   const int v = a.E / 16, n = a.E / a.G;
   if (a.E % 32 || v > 16 || a.K > 15 || n % v) return 0;

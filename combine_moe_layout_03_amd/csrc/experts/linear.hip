@@ -52,12 +52,13 @@ struct ProductArgs {
 // clocks that its products take; with eight waves of 128 x 64 it would be 1536), and
 // LDS is free for the stage after next as soon as the second half is in registers.
 //
-// What bounds it: 8192 x 4096 x 7168 take 314 to 330 us on different GPUs of this kind
-// (1450 to 1530 TFLOP/s; a library product of this size 294 to 308), the gradients 347
-// to 365 both (362 to 385, 488): the matrix units are busy 60% of the clocks at 1.9 GHz,
+// What bounds it: 8192 x 4096 x 7168 take 314 to 353 us on different GPUs of this kind
+// (1360 to 1530 TFLOP/s; a library product of this size 294 to 319), the gradients 347
+// to 390 both (362 to 395, 488): the matrix units are busy 60% of the clocks at 1.9 GHz,
 // where the GPU's power holds them. About 9 us go around every tile: its start, and its
-// sums on their way out. 8192 x 7168 x 2048 186 to 193 us, with bias and residual 214 to
-// 220 (171 to 180 without).
+// sums on their way out. 8192 x 7168 x 2048 186 to 209 us, with bias and residual 214 to
+// 232 (the library 171 to 188 without); SwiGLU of 8192 x 2 x 2048 x 7168 338 to 356, with
+// z kept 344 to 365.
 // Measured and not kept (us, beside the kernel of that time): copies issued in one
 // half of a stage for the next one 364 against 346; reads and copies in clumps before
 // every eight products 351 against 338; tiles taken in turn by resident workgroups that
@@ -389,9 +390,10 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
 // 64, each through a ring of groups in its own part of LDS, without a barrier, and
 // join their sums at the end.
 //
-// 16 tokens, 7168 to 4096 channels: 11.3 us, 5.2 TB/s of weights (they come through L2
-// beside as many bytes of tokens); 128 tokens, 7168 to 256: 7.0 us (13.4 as split tiles),
-// about 35 bytes a clock into a CU. Rings of 2, 3, 4 or 8 groups and 4, 8 or 16 waves: within
+// 16 tokens, 7168 to 4096 channels, weights from memory: 12.1 us, 4.9 TB/s of them (they
+// come through L2 beside as many bytes of tokens); 128 tokens, 7168 to 256: 6.5 us (13.4
+// as split tiles), about 38 bytes a clock into a CU; what bounds it is that each block of
+// 16 tokens brings the weights in again, 88 MB in all for 5.5. Rings of 2, 3, 4 or 8 groups and 4, 8 or 16 waves: within
 // 5%, but for those that leave a CU one workgroup, slower where there are more.
 
 constexpr int kStreamWaves = 4, kStreamRing = 4;
@@ -437,9 +439,9 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(ProductArgs a
     for (int i = 0; i < 2; ++i) copy16_bounded(tbuf, (t_off[i] + more) | mask, to + i * 1024);
 #pragma unroll
     for (int i = 0; i < kW / 8; ++i) {
-      if (blocks == 1)  // 16 x 4096 of 7168 channels 12.6 us, unmarked 13.6
+      if (blocks == 1)  // unmarked 8% more (16 x 4096 of 7168 channels)
         copy16_bounded_once(wbuf, (w_off[i] + more) | mask, to + 2048 + i * 1024);
-      else  // the other tokens' workgroups read them too (128 x 256: 7.05 us, marked 8.0)
+      else  // the other tokens' workgroups read them too (marked 13% more, 128 x 256)
         copy16_bounded(wbuf, (w_off[i] + more) | mask, to + 2048 + i * 1024);
     }
   };

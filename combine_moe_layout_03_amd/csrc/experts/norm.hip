@@ -21,6 +21,11 @@
 // row. A row is loaded while the one before it is computed: two workgroups of a CU
 // then keep 96 KB in flight. 16 rows of 7168 with codes: 3.9 us, most of it the launch
 // and two trips to memory; a row over 16 waves instead of 4 took 1.1 us off.
+// Between 8192 and 16384 channels the gradient fills a SIMD's registers with one wave:
+// 4096 x 12288 in 88 us, 4.6 TB/s (the norm 63, 6.4). Above, a row's values and sums
+// pass the 128 registers of each of 1024 threads and lie in scratch memory (1480 bytes
+// a lane): 2048 x 18432 in 1430 us, 0.2 TB/s, slower than plain operators; the norm
+// itself, 71 us, is not touched by that.
 #include "cast.hpp"
 
 namespace moe {
