@@ -6,7 +6,7 @@
 //   d_x = d_sum + rstd * (g - n * mean(g * n)),  d_weight = sum over the rows of d_y * n.
 //
 // A row stays in the registers of the threads that read it (8 channels a
-// thread and vector), so every tensor passes once. The mean is float: 8 squares
+// thread and vector), so every tensor passes once, but for the widest gradients. The mean is float: 8 squares
 // a lane and vector in order, then the lanes, then the waves, always alike. y is
 // rounded once, from the sum as it is stored, so that the gradient, which has only
 // that, sees the same n. The codes are those of the float y.
@@ -23,9 +23,10 @@
 // and two trips to memory; a row over 16 waves instead of 4 took 1.1 us off.
 // Between 8192 and 16384 channels the gradient fills a SIMD's registers with one wave:
 // 4096 x 12288 in 88 us, 4.6 TB/s (the norm 63, 6.4). Above, a row's values and sums
-// pass the 128 registers of each of 1024 threads and lie in scratch memory (1480 bytes
-// a lane): 2048 x 18432 in 1430 us, 0.2 TB/s, slower than plain operators; the norm
-// itself, 71 us, is not touched by that.
+// pass the 128 registers of each of 1024 threads: the row is read twice, the second time
+// from cache, one vector of a thread at a time. 2048 x 18432 in 75 us with the weight's
+// sums, 4.0 TB/s; kept, the values lay in scratch memory (1464 us, and 1480 bytes a lane
+// that the runtime had to allocate).
 #include "cast.hpp"
 
 namespace moe {
@@ -163,14 +164,18 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void norm_grad_ker
 #pragma unroll
     for (int d = 0; d < 8; ++d) dw[j][d] = 0.0f;
   int turn = 0;
+  // The widest rows do not fit the registers beside their sums for the weight: each
+  // vector is loaded where it is used, for the row's sums and again for its gradient.
+  constexpr bool kHeld = kWaves * V <= 64;
+  constexpr int kHold = kHeld ? V : 1;
   struct Row {
-    ex_u32x4 v[V], e[V], ds[V];
+    ex_u32x4 v[kHold], e[kHold], ds[kHold];
   };
   auto load = [&](int row) {
     Row r;
     const int64_t at = (int64_t)row * a.nv;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < kHold; ++j) {
       const int i = min(tid + j * kStride, a.nv - 1);
       r.v[j] = __builtin_nontemporal_load(a.sum + at + i);
       r.e[j] = __builtin_nontemporal_load(a.dy + at + i);
@@ -178,27 +183,32 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void norm_grad_ker
     }
     return r;
   };
-  ex_u32x4 weight[V];
+  ex_u32x4 weight[kHold];
 #pragma unroll
-  for (int j = 0; j < V; ++j) weight[j] = a.weight[min(tid + j * kStride, a.nv - 1)];
+  for (int j = 0; j < kHold; ++j) weight[j] = a.weight[min(tid + j * kStride, a.nv - 1)];
   const int step = (int)gridDim.x * kRows;
   int row = (int)blockIdx.x * kRows + (kWaves == 1 ? wave : 0);
   if (row >= a.T && kWaves > 1) return;  // (no workgroup is without a row)
-  constexpr bool kAhead = kWaves * V <= 64;  // (the widest rows fill the registers alone)
   Row next;
-  if (kAhead) next = load(min(row, a.T - 1));
+  if (kHeld) next = load(min(row, a.T - 1));
   for (; row < a.T; row += step, turn ^= 1) {
-    const Row now = kAhead ? next : load(row);
-    if (kAhead) next = load(min(row + step, a.T - 1));  // the last one's again behind the end
+    Row now;
+    if (kHeld) {
+      now = next;
+      next = load(min(row + step, a.T - 1));  // the last one's again behind the end
+    }
     const int64_t at = (int64_t)row * a.nv;
-    const ex_u32x4 *v = now.v, *e = now.e, *ds = now.ds;
     float ss = 0.0f, gs = 0.0f;  // of squares, and of sum * g (rstd follows)
+    int self = tid;  // (new to the compiler each time, which would keep values and addresses)
+    if (!kHeld) asm volatile("" : "+v"(self));
 #pragma unroll
     for (int j = 0; j < V; ++j) {
+      if (!kHeld && j * kStride >= a.nv) continue;  // uniform
+      const int k = min(self + j * kStride, a.nv - 1);
       float f[8], g[8], w[8];
-      unpack(v[j], f);
-      unpack(e[j], g);
-      unpack(weight[j], w);
+      unpack(kHeld ? now.v[j % kHold] : a.sum[at + k], f);
+      unpack(kHeld ? now.e[j % kHold] : a.dy[at + k], g);
+      unpack(kHeld ? weight[j % kHold] : a.weight[k], w);
       float s = 0.0f, t = 0.0f;
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
@@ -228,14 +238,19 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void norm_grad_ker
     }
     const float rstd = 1.0f / sqrtf(ss / a.h + a.eps);
     const float c = gs * rstd / a.h;  // mean(g n)
+    if (!kHeld) asm volatile("" : "+v"(self)::"memory");
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int i = tid + j * kStride;
+      if (!kHeld && j * kStride >= a.nv) continue;
+      const int i = self + j * kStride, k = min(i, a.nv - 1);
       float f[8], g[8], w[8], o[8];
-      unpack(v[j], f);
-      unpack(e[j], g);
-      unpack(weight[j], w);
-      unpack(ds[j], o);
+      unpack(kHeld ? now.v[j % kHold] : __builtin_nontemporal_load(a.sum + at + k), f);
+      unpack(kHeld ? now.e[j % kHold] : __builtin_nontemporal_load(a.dy + at + k), g);
+      unpack(kHeld ? weight[j % kHold] : a.weight[k], w);
+      if (kHeld)
+        unpack(now.ds[j % kHold], o);
+      else
+        unpack(a.dsum ? __builtin_nontemporal_load(a.dsum + at + k) : ex_u32x4{0, 0, 0, 0}, o);
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
         const float n = f[d] * rstd;
