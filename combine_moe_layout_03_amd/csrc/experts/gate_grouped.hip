@@ -252,9 +252,9 @@ __device__ __forceinline__ void best_two(float &m1, float &m2) {
   m1 = fmaxf(m1, o1);
 }
 
-// How many groups of the row score more than the lane's by more than the scores may be
-// off (tol, each group's own), and by more than less that; of equal ones the first
-// scores more.
+// How many groups of the row score more than the lane's for sure, and how many may: by
+// more than the two scores may be off together (tol is each group's own), and by more
+// than less that. Of equal ones the first scores more.
 template <int L, int kStart = L>
 __device__ __forceinline__ void better_groups(float s, float tol, int &sure, int &maybe) {
   if constexpr (kStart < 16) {

@@ -170,7 +170,7 @@ __device__ __forceinline__ bf16x8 fragment(const uint8_t *stage, int t, int kk) 
 // registers, moves sums and fragments to and fro between the two files (dw of 8192 x
 // 4096 x 7168: 461 us, with the sums held in the accumulation registers 389). It
 // still waits for the fragments it reads; that the sums are ready, products_done()
-// sees to (a product takes 8 passes of four clocks). Nothing in the source keeps a copy
+// sees to (a product takes 16 clocks). Nothing in the source keeps a copy
 // of a sum from being placed ahead of its waits: as operands of the waits the sums are
 // copied, in part before them (204 us against 202 at 8192 x 7168 x 2048). So a test reads
 // the built code: no result read, and no operand written, within the wait states.
@@ -393,8 +393,9 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
 // 16 tokens, 7168 to 4096 channels, weights from memory: 12.1 us, 4.9 TB/s of them (they
 // come through L2 beside as many bytes of tokens); 128 tokens, 7168 to 256: 6.5 us (13.4
 // as split tiles), about 38 bytes a clock into a CU; what bounds it is that each block of
-// 16 tokens brings the weights in again, 88 MB in all for 5.5. Rings of 2, 3, 4 or 8 groups and 4, 8 or 16 waves: within
-// 5%, but for those that leave a CU one workgroup, slower where there are more.
+// 16 tokens brings the weights in again, 88 MB in all for 5.5. Rings of 2, 3, 4 or 8 groups
+// and 4, 8 or 16 waves: within 5%, but for those that leave a CU one workgroup, slower
+// where there are more.
 
 constexpr int kStreamWaves = 4, kStreamRing = 4;
 

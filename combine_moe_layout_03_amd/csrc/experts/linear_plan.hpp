@@ -58,8 +58,8 @@ inline Plan plan(int64_t rows, int64_t cols, int64_t k, bool pairs, int64_t work
 // 768 of 4096 14.9 and 16.4, 1024 of them 18.6 to 21 and 17.4; 512 of 7168 16 to 20 and 18
 // to 20, 640 of them 23 and 20; 16 rows x 65536 of 256 or 512 channels 20 and 11, 24 and 18,
 // 16 x 32768 of 2048: 27 and 36. (Of several blocks with long sums neither side is near
-// its operands' bytes: 128 x 1024 of 7168 is 17 MB, 3 us.) The second half of a SwiGLU's weights has to be within
-// reach of a 32-bit offset.
+// its operands' bytes: 128 x 1024 of 7168 is 17 MB, 3 us.) The second half of a SwiGLU's
+// weights has to be within reach of a 32-bit offset.
 inline bool streamed(int64_t rows, int64_t N, int64_t k, bool pairs) {
   if (pairs && (N + 16) * k * 2 >= 0xffffffe0ll) return false;
   const int64_t units = (rows + 15) / 16 * ((N * (pairs ? 2 : 1) + 15) / 16);

@@ -6,9 +6,9 @@
 //   d_x = d_sum + rstd * (g - n * mean(g * n)),  d_weight = sum over the rows of d_y * n.
 //
 // A row stays in the registers of the threads that read it (8 channels a
-// thread and vector), so every tensor passes once, but for the widest gradients. The mean is float: 8 squares
-// a lane and vector in order, then the lanes, then the waves, always alike. y is
-// rounded once, from the sum as it is stored, so that the gradient, which has only
+// thread and vector), so every tensor passes once, but for the widest gradients'. The
+// mean is float: 8 squares a lane and vector in order, then the lanes, then the waves,
+// always alike. y is rounded once, from the sum as it is stored, so that the gradient, which has only
 // that, sees the same n. The codes are those of the float y.
 // d_weight: a workgroup adds its rows up in registers and writes one row of
 // partial sums; a second kernel adds those in order.

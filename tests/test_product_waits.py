@@ -10,7 +10,7 @@ import subprocess
 import pytest
 
 OBJDUMP = "/opt/rocm/llvm/bin/llvm-objdump"
-RESULT_WAITS = 18  # wait states (a 16-pass instruction's; these take 8 passes)
+RESULT_WAITS = 18  # wait states (the longest instruction's; these are among the shortest)
 OPERAND_WAITS = 2
 MAGIC = b"__CLANG_OFFLOAD_BUNDLE__"
 
